@@ -79,7 +79,26 @@ typedef enum {
 
 typedef enum { NVFP4_OUT_BF16 = 0, NVFP4_OUT_F32 = 1 } nvfp4_out_dtype;
 
-typedef enum { NVFP4_OP_GEMV_BATCHED = 1, NVFP4_OP_GEMM_QUANT_A = 2 } nvfp4_op;
+typedef enum {
+  NVFP4_OP_GEMV_BATCHED = 1,
+  NVFP4_OP_GEMM_QUANT_A = 2,
+  NVFP4_OP_LAYERNORM_BACKWARD = 3, /* sizes: M = rows, N = k, K ignored */
+  NVFP4_OP_EPILOGUE_BACKWARD = 4   /* sizes: M, N, K ignored */
+} nvfp4_op;
+
+/* Element type of an operand that may be either (values of nvfp4_out_dtype). */
+typedef enum { NVFP4_DTYPE_BF16 = 0, NVFP4_DTYPE_F32 = 1 } nvfp4_dtype;
+
+/* Activations of the product epilogues:
+ *   RELU max(v, 0); GELU v Phi(v) (Phi by erf); GELU_TANH its tanh form
+ *   v / 2 (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))); SILU v / (1 + e^-v). */
+typedef enum {
+  NVFP4_ACT_NONE = 0,
+  NVFP4_ACT_RELU = 1,
+  NVFP4_ACT_GELU = 2,
+  NVFP4_ACT_GELU_TANH = 3,
+  NVFP4_ACT_SILU = 4
+} nvfp4_act;
 
 /* ABI version of this header (bumped on incompatible changes). */
 NVFP4_API int nvfp4_abi_version(void);
@@ -287,6 +306,94 @@ NVFP4_API nvfp4_status nvfp4_gemm_requant(const void* a_codes, const void* a_sf_
                               void* d_sf, nvfp4_sf_layout d_sf_layout, float* amax_d_dev,
                               nvfp4_stream_t stream);
 
+/*
+ * Layer norm over the rows of x [rows, k], in front of a quantizer:
+ *     mean = sum x / k,  var = sum (x - mean)^2 / k,  rstd = 1 / sqrt(var + eps)
+ *     y = (x - mean) * rstd * gamma + beta
+ * in fp32, y rounded once.
+ *   x : x_dtype, pitch ldx >= k elements;  y : out, y_dtype, pitch ldy >= k
+ *   gamma, beta : [k] of param_dtype each; null gamma is 1, null beta is 0
+ *   mean, rstd : out, [rows] fp32 (what nvfp4_layernorm_backward takes), each may be null
+ *   amax_dev : out, max |y| over the stored y, may be null (zeroed by the call
+ *           first): the amax that nvfp4_quantize takes with amax_given = 1, so
+ *           a bf16 y is quantized in one pass.  Non-finite y propagate to it.
+ * rows >= 0 (0: only *amax_dev is written), k >= 1, eps >= 0 and finite.
+ * Pointers and pitches need only element alignment (16-byte aligned rows of
+ * x, y, gamma and beta are the fast case).  y must not overlap x.
+ */
+NVFP4_API nvfp4_status nvfp4_layernorm(const void* x, nvfp4_dtype x_dtype, int64_t rows, int64_t k, int64_t ldx,
+                             const void* gamma, const void* beta, nvfp4_dtype param_dtype, float eps, void* y,
+                             nvfp4_dtype y_dtype, int64_t ldy, float* mean, float* rstd, float* amax_dev,
+                             nvfp4_stream_t stream);
+
+/*
+ * Gradient of nvfp4_layernorm.  With xh = (x - mean) * rstd and a = dy * gamma:
+ *     dx = rstd * (a - sum(a) / k - xh * sum(a * xh) / k)  [+ d_residual]
+ *     dgamma = sum over rows of dy * xh,  dbeta = sum over rows of dy
+ *   dy : dy_dtype, pitch lddy;  x : x_dtype, pitch ldx (as given to the forward call)
+ *   mean, rstd : [rows] fp32 of the forward call;  gamma : [k] of param_dtype or null (1)
+ *   d_residual : x_dtype, pitch ldr, may be null: the gradient that reaches x
+ *           past the norm (a residual stream), added to dx
+ *   dx : out, x_dtype, pitch lddx; may be d_residual itself (same pitch),
+ *           must not overlap the other operands
+ *   dgamma, dbeta : out, [k] fp32, each may be null
+ *   amax_dx : out, max |dx| as stored, may be null (as in nvfp4_layernorm)
+ *   workspace : nvfp4_workspace_bytes(NVFP4_OP_LAYERNORM_BACKWARD, rows, k, 0)
+ *           bytes, 16-byte aligned; may be null if dgamma and dbeta are.  It
+ *           needs no clearing; calls sharing one must not overlap.
+ * The column sums are taken in a fixed order: equal inputs give equal bits.
+ * rows >= 0 (0: dgamma, dbeta and *amax_dx are 0), k >= 1; alignment as in
+ * nvfp4_layernorm.
+ */
+NVFP4_API nvfp4_status nvfp4_layernorm_backward(const void* dy, nvfp4_dtype dy_dtype, int64_t lddy, const void* x,
+                                      nvfp4_dtype x_dtype, int64_t ldx, const float* mean, const float* rstd,
+                                      const void* gamma, nvfp4_dtype param_dtype, const void* d_residual,
+                                      int64_t ldr, int64_t rows, int64_t k, void* dx, int64_t lddx, float* dgamma,
+                                      float* dbeta, float* amax_dx, void* workspace, size_t ws_bytes,
+                                      nvfp4_stream_t stream);
+
+/*
+ * nvfp4_gemm with bias, activation and residual in its epilogue:
+ *     v = alpha * acc + bias[n]     (acc the block-scaled product, fp32)
+ *     D[m, n] = act(v) + residual[m, n]
+ * in fp32, each output rounded once to out_dtype.
+ *   bias : [N] of bias_dtype, or null
+ *   residual : [M, N] of out_dtype, pitch ldr >= N, or null; may be d itself (ldr == ldd)
+ *   d : out, [M, N] of out_dtype, pitch ldd >= N
+ *   pre : out, v as out_dtype, pitch ldp >= N, or null: what
+ *           nvfp4_epilogue_backward takes
+ *   amax_d_dev : out, max |D| as stored, or null (zeroed by the call first):
+ *           the amax nvfp4_quantize takes with amax_given = 1.  Non-finite D
+ *           propagate to it.
+ * bias, residual, d and pre need only element alignment (16-byte aligned rows
+ * are the fast case); apart from residual == d they must not overlap.  Other
+ * arguments, shapes and errors as nvfp4_gemm.
+ */
+NVFP4_API nvfp4_status nvfp4_gemm_epilogue(const void* a_codes, const void* a_sf_tc, const float* g_a_dev,
+                                 const void* b_codes, const void* b_sf_tc, const float* g_b_dev, int64_t M,
+                                 int64_t N, int64_t K, const void* bias, nvfp4_dtype bias_dtype, nvfp4_act act,
+                                 const void* residual, int64_t ldr, void* d, int64_t ldd, nvfp4_out_dtype out_dtype,
+                                 void* pre, int64_t ldp, float* amax_d_dev, nvfp4_stream_t stream);
+
+/*
+ * Gradient of that epilogue (of the residual it is dD itself):
+ *     dpre = dD * act'(pre),  dbias = sum over rows of dpre (before rounding)
+ *   dd : [M, N] of dtype, pitch ldd;  pre : the same, pitch ldp (may be null for NVFP4_ACT_NONE)
+ *   dpre : out, of dtype, pitch lddp; may be dd itself (same pitch); may be
+ *           null, for dbias alone
+ *   dbias : out, [N] fp32, or null;  amax_dpre : out, max |dpre| as stored, or
+ *           null (zeroed by the call first; needs no dpre)
+ *   workspace : nvfp4_workspace_bytes(NVFP4_OP_EPILOGUE_BACKWARD, M, N, 0)
+ *           bytes, 16-byte aligned; may be null if dbias is.  It needs no
+ *           clearing; calls sharing one must not overlap.
+ * dbias is summed in a fixed order: equal inputs give equal bits.  M >= 0 (0:
+ * dbias and *amax_dpre are 0), N >= 1; element alignment.  Relu's slope at 0 is 0.
+ */
+NVFP4_API nvfp4_status nvfp4_epilogue_backward(const void* dd, int64_t ldd, const void* pre, int64_t ldp,
+                                     nvfp4_dtype dtype, nvfp4_act act, int64_t M, int64_t N, void* dpre,
+                                     int64_t lddp, float* dbias, float* amax_dpre, void* workspace,
+                                     size_t ws_bytes, nvfp4_stream_t stream);
+
 /* Workspace bytes needed by an op for the given sizes (0 for bad sizes). */
 NVFP4_API size_t nvfp4_workspace_bytes(nvfp4_op op, int64_t M, int64_t N, int64_t K);
 
@@ -315,6 +422,21 @@ NVFP4_API size_t nvfp4_workspace_bytes(nvfp4_op op, int64_t M, int64_t N, int64_
 NVFP4_API nvfp4_status nvfp4_gemv_batched(const void* x_bf16, int64_t M, int64_t ldx, const void* w_codes,
                                 const void* w_sf_tc, const float* g_w_dev, int64_t N, int64_t K, void* y_bf16,
                                 int64_t ldy, void* workspace, size_t ws_bytes, nvfp4_stream_t stream);
+
+/*
+ * nvfp4_gemv_batched with bias, activation and residual in its epilogue, the
+ * single-token form of nvfp4_gemm_epilogue: with v = alpha * acc + bias[n],
+ * y[m, n] = act(v) + residual[m, n] in fp32, rounded once to bf16.
+ *   bias : [N] of bias_dtype, or null;  residual : bf16 [M, N], pitch ldr >= N,
+ *           or null; may be y itself (ldr == ldy)
+ * Element alignment for bias, residual and y.  Other arguments, workspace,
+ * shapes and errors as nvfp4_gemv_batched.
+ */
+NVFP4_API nvfp4_status nvfp4_gemv_batched_epilogue(const void* x_bf16, int64_t M, int64_t ldx, const void* w_codes,
+                                         const void* w_sf_tc, const float* g_w_dev, int64_t N, int64_t K,
+                                         const void* bias, nvfp4_dtype bias_dtype, nvfp4_act act,
+                                         const void* residual, int64_t ldr, void* y_bf16, int64_t ldy,
+                                         void* workspace, size_t ws_bytes, nvfp4_stream_t stream);
 
 /*
  * nvfp4_gemv_batched without a workspace argument, for callers that cannot

@@ -346,6 +346,11 @@ nvfp4_status nvfp4_gemm_requant(const void* a_codes, const void* a_sf_tc, const 
 }
 
 size_t nvfp4_workspace_bytes(nvfp4_op op, int64_t M, int64_t N, int64_t K) {
+  if (op == NVFP4_OP_LAYERNORM_BACKWARD || op == NVFP4_OP_EPILOGUE_BACKWARD) {
+    if (M < 0 || N < 1 || M > 0x7FFFFFFF || N > 0x7FFFFFFF) return 0;
+    return op == NVFP4_OP_LAYERNORM_BACKWARD ? layernorm_backward_workspace_bytes(M, N)
+                                             : epilogue_backward_workspace_bytes(M, N);
+  }
   if (M < 1 || N < 1 || K < 1 || (K % 64) != 0) return 0;
   if (op == NVFP4_OP_GEMV_BATCHED) {
     if (M > 32) return 0;
@@ -359,9 +364,9 @@ size_t nvfp4_workspace_bytes(nvfp4_op op, int64_t M, int64_t N, int64_t K) {
   return 0;
 }
 
-nvfp4_status nvfp4_gemv_batched(const void* x_bf16, int64_t M, int64_t ldx, const void* w_codes,
-                                const void* w_sf_tc, const float* g_w_dev, int64_t N, int64_t K, void* y_bf16,
-                                int64_t ldy, void* workspace, size_t ws_bytes, nvfp4_stream_t stream) {
+static nvfp4_status check_gemv(const void* x_bf16, int64_t M, int64_t ldx, const void* w_codes, const void* w_sf_tc,
+                               const float* g_w_dev, int64_t N, int64_t K, const void* y_bf16, int64_t ldy,
+                               const void* workspace, size_t ws_bytes) {
   nvfp4_status st = check_bf16_input(x_bf16, M, K, ldx);
   if (st != NVFP4_OK) return st;
   if (!w_codes || !w_sf_tc || !g_w_dev || !y_bf16 || !workspace) return NVFP4_ERR_INVALID_ARG;
@@ -370,6 +375,14 @@ nvfp4_status nvfp4_gemv_batched(const void* x_bf16, int64_t M, int64_t ldx, cons
   if (!aligned16(w_codes) || !aligned16(w_sf_tc) || !aligned16(workspace)) return NVFP4_ERR_MISALIGNED;
   if ((reinterpret_cast<uintptr_t>(y_bf16) & 1u)) return NVFP4_ERR_MISALIGNED;
   if (ws_bytes < gemv_workspace_bytes(M, N, K)) return NVFP4_ERR_WORKSPACE;
+  return NVFP4_OK;
+}
+
+nvfp4_status nvfp4_gemv_batched(const void* x_bf16, int64_t M, int64_t ldx, const void* w_codes,
+                                const void* w_sf_tc, const float* g_w_dev, int64_t N, int64_t K, void* y_bf16,
+                                int64_t ldy, void* workspace, size_t ws_bytes, nvfp4_stream_t stream) {
+  nvfp4_status st = check_gemv(x_bf16, M, ldx, w_codes, w_sf_tc, g_w_dev, N, K, y_bf16, ldy, workspace, ws_bytes);
+  if (st != NVFP4_OK) return st;
   if ((st = check_arch()) != NVFP4_OK) return st;
   return launch_gemv(x_bf16, M, ldx, w_codes, w_sf_tc, g_w_dev, N, K, y_bf16, ldy, workspace,
                      reinterpret_cast<cudaStream_t>(stream));
@@ -474,6 +487,123 @@ nvfp4_status nvfp4_gemm_quant_a_amax(const void* a_bf16, int64_t lda, const floa
   if (!amax_dev) return NVFP4_ERR_INVALID_ARG;
   return gemm_quant_a_common(QaMode::kAmaxGiven, a_bf16, lda, amax_dev, b_codes, b_sf_tc, g_b_dev, M, N, K, d, ldd,
                              out_dtype, workspace, ws_bytes, stream);
+}
+
+// Row-major [rows, cols] operand of dtype t: pitch and element alignment.
+static nvfp4_status check_rows(const void* p, nvfp4_dtype t, int64_t cols, int64_t ld) {
+  if (ld < cols) return NVFP4_ERR_INVALID_ARG;
+  return (reinterpret_cast<uintptr_t>(p) & (t == NVFP4_DTYPE_F32 ? 3u : 1u)) ? NVFP4_ERR_MISALIGNED : NVFP4_OK;
+}
+
+static bool bad_dtype(nvfp4_dtype t) { return t != NVFP4_DTYPE_BF16 && t != NVFP4_DTYPE_F32; }
+static bool bad_act(nvfp4_act a) { return a < NVFP4_ACT_NONE || a > NVFP4_ACT_SILU; }
+static bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+nvfp4_status nvfp4_layernorm(const void* x, nvfp4_dtype x_dtype, int64_t rows, int64_t k, int64_t ldx,
+                             const void* gamma, const void* beta, nvfp4_dtype param_dtype, float eps, void* y,
+                             nvfp4_dtype y_dtype, int64_t ldy, float* mean, float* rstd, float* amax_dev,
+                             nvfp4_stream_t stream) {
+  if (rows < 0 || k < 1 || bad_dtype(x_dtype) || bad_dtype(y_dtype) || bad_dtype(param_dtype)) return NVFP4_ERR_INVALID_ARG;
+  if (!(eps >= 0.0f) || eps > 3.402823466e38f) return NVFP4_ERR_INVALID_ARG;
+  if (rows > 0 && (!x || !y)) return NVFP4_ERR_INVALID_ARG;
+  if (rows > 0x7FFFFFFF || k > 0x7FFFFFFF) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  nvfp4_status st;
+  if ((st = check_rows(x, x_dtype, k, ldx)) != NVFP4_OK || (st = check_rows(y, y_dtype, k, ldy)) != NVFP4_OK ||
+      (st = check_rows(gamma, param_dtype, 0, 0)) != NVFP4_OK || (st = check_rows(beta, param_dtype, 0, 0)) != NVFP4_OK)
+    return st;
+  if (misaligned4(mean) || misaligned4(rstd) || misaligned4(amax_dev)) return NVFP4_ERR_MISALIGNED;
+  if ((st = check_arch()) != NVFP4_OK) return st;
+  const LayerNorm a{x, x_dtype, rows, k, ldx, gamma, beta, param_dtype, eps, y, y_dtype, ldy, mean, rstd, amax_dev};
+  return launch_layernorm(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+nvfp4_status nvfp4_layernorm_backward(const void* dy, nvfp4_dtype dy_dtype, int64_t lddy, const void* x,
+                                      nvfp4_dtype x_dtype, int64_t ldx, const float* mean, const float* rstd,
+                                      const void* gamma, nvfp4_dtype param_dtype, const void* d_residual,
+                                      int64_t ldr, int64_t rows, int64_t k, void* dx, int64_t lddx, float* dgamma,
+                                      float* dbeta, float* amax_dx, void* workspace, size_t ws_bytes,
+                                      nvfp4_stream_t stream) {
+  if (rows < 0 || k < 1 || bad_dtype(x_dtype) || bad_dtype(dy_dtype) || bad_dtype(param_dtype)) return NVFP4_ERR_INVALID_ARG;
+  if (rows > 0 && (!dy || !x || !mean || !rstd || !dx)) return NVFP4_ERR_INVALID_ARG;
+  if (dx && dx == d_residual && lddx != ldr) return NVFP4_ERR_INVALID_ARG;
+  if (rows > 0x7FFFFFFF || k > 0x7FFFFFFF) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  nvfp4_status st;
+  if ((st = check_rows(dy, dy_dtype, k, lddy)) != NVFP4_OK || (st = check_rows(x, x_dtype, k, ldx)) != NVFP4_OK ||
+      (st = check_rows(gamma, param_dtype, 0, 0)) != NVFP4_OK || (st = check_rows(dx, x_dtype, k, lddx)) != NVFP4_OK ||
+      (d_residual && (st = check_rows(d_residual, x_dtype, k, ldr)) != NVFP4_OK))
+    return st;
+  if (misaligned4(mean) || misaligned4(rstd) || misaligned4(dgamma) || misaligned4(dbeta) || misaligned4(amax_dx))
+    return NVFP4_ERR_MISALIGNED;
+  if ((dgamma || dbeta) && rows > 0) {
+    if (!workspace) return NVFP4_ERR_INVALID_ARG;
+    if (!aligned16(workspace)) return NVFP4_ERR_MISALIGNED;
+    if (ws_bytes < layernorm_backward_workspace_bytes(rows, k)) return NVFP4_ERR_WORKSPACE;
+  }
+  if ((st = check_arch()) != NVFP4_OK) return st;
+  const LayerNormBackward a{dy, dy_dtype, lddy, x, x_dtype, ldx, mean, rstd, gamma, param_dtype, d_residual, ldr,
+                            rows, k, dx, lddx, dgamma, dbeta, amax_dx, workspace};
+  return launch_layernorm_backward(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+nvfp4_status nvfp4_gemm_epilogue(const void* a_codes, const void* a_sf_tc, const float* g_a_dev, const void* b_codes,
+                                 const void* b_sf_tc, const float* g_b_dev, int64_t M, int64_t N, int64_t K,
+                                 const void* bias, nvfp4_dtype bias_dtype, nvfp4_act act, const void* residual,
+                                 int64_t ldr, void* d, int64_t ldd, nvfp4_out_dtype out_dtype, void* pre, int64_t ldp,
+                                 float* amax_d_dev, nvfp4_stream_t stream) {
+  nvfp4_status st = check_gemm_operands(a_codes, a_sf_tc, g_a_dev, b_codes, b_sf_tc, g_b_dev, M, N, K, d);
+  if (st != NVFP4_OK) return st;
+  if (out_dtype != NVFP4_OUT_BF16 && out_dtype != NVFP4_OUT_F32) return NVFP4_ERR_INVALID_ARG;
+  const nvfp4_dtype t = out_dtype == NVFP4_OUT_F32 ? NVFP4_DTYPE_F32 : NVFP4_DTYPE_BF16;
+  if (bad_dtype(bias_dtype) || bad_act(act) || pre == d || (residual == d && ldr != ldd) || (pre && pre == residual))
+    return NVFP4_ERR_INVALID_ARG;
+  if ((st = check_rows(d, t, N, ldd)) != NVFP4_OK || (pre && (st = check_rows(pre, t, N, ldp)) != NVFP4_OK) ||
+      (residual && (st = check_rows(residual, t, N, ldr)) != NVFP4_OK) ||
+      (st = check_rows(bias, bias_dtype, 0, 0)) != NVFP4_OK)
+    return st;
+  if (misaligned4(amax_d_dev)) return NVFP4_ERR_MISALIGNED;
+  if ((st = check_arch()) != NVFP4_OK) return st;
+  const Epilogue e{bias, bias_dtype == NVFP4_DTYPE_F32, act, residual, ldr, pre, ldp, amax_d_dev};
+  return launch_gemm_epilogue(a_codes, a_sf_tc, g_a_dev, b_codes, b_sf_tc, g_b_dev, M, N, K, d, ldd, out_dtype, e,
+                              reinterpret_cast<cudaStream_t>(stream));
+}
+
+nvfp4_status nvfp4_gemv_batched_epilogue(const void* x_bf16, int64_t M, int64_t ldx, const void* w_codes,
+                                         const void* w_sf_tc, const float* g_w_dev, int64_t N, int64_t K,
+                                         const void* bias, nvfp4_dtype bias_dtype, nvfp4_act act,
+                                         const void* residual, int64_t ldr, void* y_bf16, int64_t ldy,
+                                         void* workspace, size_t ws_bytes, nvfp4_stream_t stream) {
+  nvfp4_status st = check_gemv(x_bf16, M, ldx, w_codes, w_sf_tc, g_w_dev, N, K, y_bf16, ldy, workspace, ws_bytes);
+  if (st != NVFP4_OK) return st;
+  if (bad_dtype(bias_dtype) || bad_act(act) || (residual == y_bf16 && ldr != ldy)) return NVFP4_ERR_INVALID_ARG;
+  if ((residual && (st = check_rows(residual, NVFP4_DTYPE_BF16, N, ldr)) != NVFP4_OK) ||
+      (st = check_rows(bias, bias_dtype, 0, 0)) != NVFP4_OK)
+    return st;
+  if ((st = check_arch()) != NVFP4_OK) return st;
+  const Epilogue e{bias, bias_dtype == NVFP4_DTYPE_F32, act, residual, ldr, nullptr, 0, nullptr};
+  return launch_gemv(x_bf16, M, ldx, w_codes, w_sf_tc, g_w_dev, N, K, y_bf16, ldy, workspace,
+                     reinterpret_cast<cudaStream_t>(stream), &e);
+}
+
+nvfp4_status nvfp4_epilogue_backward(const void* dd, int64_t ldd, const void* pre, int64_t ldp, nvfp4_dtype dtype,
+                                     nvfp4_act act, int64_t M, int64_t N, void* dpre, int64_t lddp, float* dbias,
+                                     float* amax_dpre, void* workspace, size_t ws_bytes, nvfp4_stream_t stream) {
+  if (M < 0 || N < 1 || bad_dtype(dtype) || bad_act(act)) return NVFP4_ERR_INVALID_ARG;
+  if (M > 0 && (!dd || (!pre && act != NVFP4_ACT_NONE))) return NVFP4_ERR_INVALID_ARG;
+  if (dpre && ((dpre == dd && lddp != ldd) || dpre == pre)) return NVFP4_ERR_INVALID_ARG;
+  if (M > 0x7FFFFFFF || N > 0x7FFFFFFF) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  nvfp4_status st;
+  if ((st = check_rows(dd, dtype, N, ldd)) != NVFP4_OK || (pre && (st = check_rows(pre, dtype, N, ldp)) != NVFP4_OK) ||
+      (dpre && (st = check_rows(dpre, dtype, N, lddp)) != NVFP4_OK))
+    return st;
+  if (misaligned4(dbias) || misaligned4(amax_dpre)) return NVFP4_ERR_MISALIGNED;
+  if (dbias && M > 0) {
+    if (!workspace) return NVFP4_ERR_INVALID_ARG;
+    if (!aligned16(workspace)) return NVFP4_ERR_MISALIGNED;
+    if (ws_bytes < epilogue_backward_workspace_bytes(M, N)) return NVFP4_ERR_WORKSPACE;
+  }
+  if ((st = check_arch()) != NVFP4_OK) return st;
+  const EpilogueBackward a{dd, ldd, pre, ldp, dtype, act, M, N, dpre, lddp, dbias, amax_dpre, workspace};
+  return launch_epilogue_backward(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 nvfp4_status nvfp4_check_device_status(nvfp4_stream_t stream) {

@@ -22,6 +22,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include "epilogue.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 #include "quant_core.cuh"
@@ -103,7 +104,19 @@ struct GemmParams {
   int q_sf_tc;      // 1: tensor-core layout, 0: row-major [M, N/16]
   int q_kb_pad;     // blocks per row of the tensor-core layout (N/16 rounded up to 4)
   const float* g_d;
-  float* amax_d;    // max |alpha acc| over D, or null
+  float* amax_d;    // max |alpha acc| over D, or null (with an epilogue: max |D| as stored)
+  // Epilogue kernels only: D = act(alpha acc + bias) + residual, pre the value
+  // before act; residual and pre have D's type (vec_res / vec_pre: 16-byte
+  // aligned rows).
+  const void* bias;
+  int bias_f32;
+  int act;
+  const void* res;
+  int64_t ldr;
+  int vec_res;
+  void* pre;
+  int64_t ldp;
+  int vec_pre;
   uint64_t wait_limit_ns;
   int* status;
   // Quantize-and-GEMM kernel only: A arrives as bf16 rows (qa_x, pitch
@@ -280,7 +293,100 @@ __device__ __forceinline__ void store_row(const GemmParams& p, int row, int col0
   }
 }
 
-template <int BN, bool kMx>
+// Eight values of row `row`, columns c .. c+7, as T: one or two 16-byte
+// accesses when the row is aligned (vec) and whole, else the n_valid elements
+// one by one.
+template <typename T>
+__device__ __forceinline__ void load8(const void* base, int64_t ld, int row, int c, int n_valid, bool vec, float (&x)[8]) {
+  const T* in = static_cast<const T*>(base) + static_cast<int64_t>(row) * ld + c;
+  if (vec && n_valid >= 8) {
+    if constexpr (sizeof(T) == 2) {
+      const uint4 w = *reinterpret_cast<const uint4*>(in);
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+      }
+    } else {
+      const float4 a = *reinterpret_cast<const float4*>(in), b = *reinterpret_cast<const float4*>(in + 4);
+      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = i < n_valid ? to_f32(in[i]) : 0.0f;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(void* base, int64_t ld, int row, int c, int n_valid, bool vec, const float (&x)[8]) {
+  T* out = static_cast<T*>(base) + static_cast<int64_t>(row) * ld + c;
+  if (vec && n_valid >= 8) {
+    if constexpr (sizeof(T) == 2) {
+      *reinterpret_cast<uint4*>(out) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                                  pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    } else {
+      *reinterpret_cast<float4*>(out) = make_float4(x[0], x[1], x[2], x[3]);
+      *reinterpret_cast<float4*>(out + 4) = make_float4(x[4], x[5], x[6], x[7]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n_valid) out[i] = from_f32<T>(x[i]);
+  }
+}
+
+// Epilogue of NV columns of one row held in v (the accumulator): v = alpha
+// acc + bias, pre = v, D = act(v) + residual, each rounded once to T; mag is
+// the running maximum of |D| as stored.
+template <typename T, int NV>
+__device__ __forceinline__ void store_row_epi(const GemmParams& p, int row, int col0, const uint32_t (&v)[NV],
+                                              float alpha, uint32_t& mag) {
+  if (row >= p.M) return;
+#pragma unroll
+  for (int g = 0; g < NV / 8; ++g) {
+    const int c = col0 + 8 * g;
+    const int n_valid = p.N - c;
+    if (n_valid <= 0) break;
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float b = p.bias && i < n_valid ? load_param(p.bias, p.bias_f32, c + i) : 0.0f;
+      x[i] = fmaf(__uint_as_float(v[8 * g + i]), alpha, b);
+    }
+    if (p.pre) store8<T>(p.pre, p.ldp, row, c, n_valid, p.vec_pre, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = act_value(x[i], p.act);
+    if (p.res) {
+      float r[8];
+      load8<T>(p.res, p.ldr, row, c, n_valid, p.vec_res, r);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] += r[i];
+    }
+    store8<T>(p.d, p.ldd, row, c, n_valid, p.vec_store, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n_valid) mag = max(mag, mag_bits(from_f32<T>(x[i])));
+  }
+}
+
+template <int NV>
+__device__ __forceinline__ void store_row_epi(const GemmParams& p, int row, int col0, const uint32_t (&v)[NV],
+                                              float alpha, uint32_t& mag) {
+  if (p.out_f32)
+    store_row_epi<float, NV>(p, row, col0, v, alpha, mag);
+  else
+    store_row_epi<__nv_bfloat16, NV>(p, row, col0, v, alpha, mag);
+}
+
+__device__ __forceinline__ void publish_mag(const GemmParams& p, uint32_t mag) {
+  if (!p.amax_d) return;
+  mag = __reduce_max_sync(0xFFFFFFFFu, mag);
+  if ((threadIdx.x & 31) == 0) atomicMax(reinterpret_cast<unsigned int*>(p.amax_d), mag);
+}
+
+// kE: the epilogue applies bias, activation and residual (store_row_epi).
+template <int BN, bool kMx, bool kE>
 __global__ void __launch_bounds__(GemmCfg<BN, kMx>::THREADS, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const GemmParams p) {
@@ -445,8 +551,9 @@ __global__ void __launch_bounds__(GemmCfg<BN, kMx>::THREADS, 1)
     const int half = ew >> 2;                  // which half of the tile's columns
     constexpr int HALF = BN / 2;
     const float alpha = kMx ? 1.0f : __fdiv_rn(1.0f, __fmul_rn(*p.g_a, *p.g_b));
-    const float gd = p.out_q ? *p.g_d : 0.0f;
+    const float gd = !kE && p.out_q ? *p.g_d : 0.0f;
     float amax_run = 0.0f;
+    uint32_t mag = 0;
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
@@ -469,13 +576,18 @@ __global__ void __launch_bounds__(GemmCfg<BN, kMx>::THREADS, 1)
       const int row = tm * BM + quad * 32 + lane;
       const int col0 = tn * BN + half * HALF;
       if (col0 < p.N) {
-        if (p.out_q)
+        if constexpr (kE)
+          store_row_epi<HALF>(p, row, col0, v, alpha, mag);
+        else if (p.out_q)
           store_row_q<HALF>(p, row, col0, v, alpha, gd, amax_run);
         else
           store_row<HALF>(p, row, col0, v, alpha);
       }
     }
-    publish_amax(p, amax_run);
+    if constexpr (kE)
+      publish_mag(p, mag);
+    else
+      publish_amax(p, amax_run);
   }
 
   __syncwarp();
@@ -654,7 +766,8 @@ __device__ __forceinline__ void qa_quantize_store(const GemmParams& p, int r, in
 // path's registers out of it.
 // kQA: the quantize-and-GEMM kernel (bf16 A quantized by extra warps, tiles
 // taken in row-major order so the first tiles need only the first rows).
-template <bool kMx, bool kQ, bool kQA = false>
+// kE: the epilogue applies bias, activation and residual (store_row_epi).
+template <bool kMx, bool kQ, bool kQA = false, bool kE = false>
 __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>::THREADS, 1)
     gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmSFA, const __grid_constant__ CUtensorMap tmSFB,
@@ -911,6 +1024,7 @@ __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>:
     }
     const float gd = kQ ? *p.g_d : 0.0f;
     float amax_run = 0.0f;
+    uint32_t mag = 0;
     const uint32_t acc_empty_leader = mapa_shared(smem_u32(acc_empty), 0);
     const uint32_t ovl_free_leader = mapa_shared(smem_u32(ovl_free), 0);
     int j = 0;
@@ -928,10 +1042,11 @@ __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>:
       uint32_t v[HALF];
       const uint32_t taddr =
           tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + (b ? C::ACC1_COL : 0) + half * HALF;
-      if constexpr (kQA) {
+      if constexpr (kQA || kE) {
         // 64 columns at a time (the quantizer warps take the registers a
-        // 128-column drain would hold), the columns shared with the other
-        // accumulator first; bf16 or fp32 D, no quantized output.
+        // 128-column drain would hold; the epilogue's code stays half as
+        // long), the columns shared with the other accumulator first; bf16 or
+        // fp32 D, no quantized output.
         const bool shared_cols = (b == 0 && half == 1) || (b == 1 && half == 0);
         const int first = (b == 0 && half == 1) ? 64 : 0;
         const int row0 = tm * 256 + static_cast<int>(rank) * 128 + quad * 32;
@@ -949,7 +1064,9 @@ __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>:
             if (part == 1) mbar_arrive_cluster_relaxed(acc_empty_leader + 8u * b);
           }
           const int col0 = tn * C::BN + half * HALF + c_off;
-          if (p.tma_store) {
+          if constexpr (kE) {
+            if (col0 < p.N) store_row_epi<64>(p, row0 + lane, col0, v, alpha, mag);
+          } else if (p.tma_store) {
             if (row0 < p.M) {
 #pragma unroll
               for (int cc = 0; cc < 2; ++cc) {
@@ -1048,8 +1165,9 @@ __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>:
         store_row<HALF>(p, row0 + lane, col0, v, alpha);
       }
     }
-    if (!kQ && p.tma_store && lane == 0) bulk_wait_group<0>();
+    if (!kQ && !kE && p.tma_store && lane == 0) bulk_wait_group<0>();
     if constexpr (kQ) publish_amax(p, amax_run);
+    if constexpr (kE) publish_mag(p, mag);
   } else if constexpr (kQA) {
     // ------------------- A quantizers (quantize-and-GEMM) -------------------
     // Units taken in ticket order (qa_unit maps a ticket to a row and a K
@@ -1167,6 +1285,22 @@ void set_quant_out(GemmParams& p, const QuantOut* q, int64_t N) {
   p.amax_d = q->amax_d;
 }
 
+// Epilogue fields of the parameters (none when e is null).
+void set_epilogue(GemmParams& p, const Epilogue* e) {
+  if (!e) return;
+  const int64_t size = p.out_f32 ? 4 : 2;
+  p.bias = e->bias;
+  p.bias_f32 = e->bias_f32;
+  p.act = e->act;
+  p.res = e->residual;
+  p.ldr = e->ldr;
+  p.vec_res = aligned16(e->residual) && (e->ldr * size) % 16 == 0;
+  p.pre = e->pre;
+  p.ldp = e->ldp;
+  p.vec_pre = aligned16(e->pre) && (e->ldp * size) % 16 == 0;
+  p.amax_d = e->amax_d;
+}
+
 // In-kernel quantization of a bf16 A (the quantize-and-GEMM kernel).
 struct QuantA {
   const void* x;
@@ -1180,7 +1314,8 @@ struct QuantA {
 template <bool kMx>
 nvfp4_status run_gemm_pair(const void* a_codes, const void* a_sf, const float* g_a, const void* b_codes,
                            const void* b_sf, const float* g_b, int64_t M, int64_t N, int64_t K, void* d, int64_t ldd,
-                           nvfp4_out_dtype out, const QuantOut* q, cudaStream_t s, const QuantA* qa = nullptr) {
+                           nvfp4_out_dtype out, const QuantOut* q, cudaStream_t s, const QuantA* qa = nullptr,
+                           const Epilogue* epi = nullptr) {
   using C = PairCfg<kMx>;
   using F = typename C::F;
   CUtensorMap tmA, tmB, tmSFA, tmSFB, tmD;
@@ -1192,7 +1327,7 @@ nvfp4_status run_gemm_pair(const void* a_codes, const void* a_sf, const float* g
   // 16-B chunks, so a row end inside a chunk would be overrun: such D takes
   // the direct-store path.
   const bool tma_store =
-      !(q && q->mode) && out == NVFP4_OUT_BF16 && aligned16(d) && (ldd * 2) % 16 == 0 && N % 8 == 0;
+      !(q && q->mode) && !epi && out == NVFP4_OUT_BF16 && aligned16(d) && (ldd * 2) % 16 == 0 && N % 8 == 0;
   memset(&tmD, 0, sizeof(tmD));
   if (tma_store && !make_out_map(&tmD, d, M, N, ldd)) return NVFP4_ERR_CUDA;
   GemmParams p{};
@@ -1213,6 +1348,7 @@ nvfp4_status run_gemm_pair(const void* a_codes, const void* a_sf, const float* g
   p.vec_store = aligned16(d) && (row_bytes % 16) == 0;
   p.tma_store = tma_store;
   set_quant_out(p, q, N);
+  set_epilogue(p, epi);
   p.wait_limit_ns = wait_limit_ns();
   p.status = device_status_ptr();
   if (!p.status) return NVFP4_ERR_CUDA;
@@ -1221,6 +1357,7 @@ nvfp4_status run_gemm_pair(const void* a_codes, const void* a_sf, const float* g
   int threads = C::THREADS, smem = C::SMEM_BYTES;
   if constexpr (!kMx) {
     if (p.out_q) kern = gemm_pair_kernel<false, true>;
+    if (epi) kern = gemm_pair_kernel<false, false, false, true>;
     if (qa) {
       if (p.out_q) return NVFP4_ERR_INVALID_ARG;
       kern = gemm_pair_kernel<false, false, true>;
@@ -1256,10 +1393,10 @@ nvfp4_status run_gemm_pair(const void* a_codes, const void* a_sf, const float* g
   cfg.attrs = attr;
   cfg.numAttrs = qa ? 2 : 1;
   // as many resident pairs as the device holds at once, never more than tiles
-  static int max_pairs[2][64] = {{0}};
+  static int max_pairs[3][64] = {{0}};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return launch_status(cudaGetLastError());
-  int* mp = &max_pairs[qa ? 1 : 0][dev < 64 ? dev : 0];
+  int* mp = &max_pairs[epi ? 2 : qa ? 1 : 0][dev < 64 ? dev : 0];
   if (dev >= 64 || *mp == 0) {
     cfg.gridDim = dim3(2 * (device_sm_count() / 2));
     int clusters = 0;
@@ -1277,7 +1414,7 @@ nvfp4_status run_gemm_pair(const void* a_codes, const void* a_sf, const float* g
 template <int BN, bool kMx>
 nvfp4_status run_gemm(const void* a_codes, const void* a_sf, const float* g_a, const void* b_codes,
                       const void* b_sf, const float* g_b, int64_t M, int64_t N, int64_t K, void* d, int64_t ldd,
-                      nvfp4_out_dtype out, const QuantOut* q, cudaStream_t s) {
+                      nvfp4_out_dtype out, const QuantOut* q, cudaStream_t s, const Epilogue* epi) {
   using C = GemmCfg<BN, kMx>;
   CUtensorMap tmA, tmB;
   if (!make_code_map(&tmA, a_codes, M, K, BM) || !make_code_map(&tmB, b_codes, N, K, BN)) return NVFP4_ERR_CUDA;
@@ -1298,15 +1435,19 @@ nvfp4_status run_gemm(const void* a_codes, const void* a_sf, const float* g_a, c
   const int64_t row_bytes = ldd * (p.out_f32 ? 4 : 2);
   p.vec_store = aligned16(d) && (row_bytes % 16) == 0;
   set_quant_out(p, q, N);
+  set_epilogue(p, epi);
   p.wait_limit_ns = wait_limit_ns();
   p.status = device_status_ptr();
   if (!p.status) return NVFP4_ERR_CUDA;
+  auto kern = gemm_kernel<BN, kMx, false>;
+  if constexpr (!kMx) {
+    if (epi) kern = gemm_kernel<BN, false, true>;
+  }
   const int tiles = p.tiles_m * p.tiles_n;
   const int grid = tiles < device_sm_count() ? tiles : device_sm_count();
-  cudaError_t e = cudaFuncSetAttribute(gemm_kernel<BN, kMx>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       C::SMEM_BYTES);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return launch_status(e);
-  gemm_kernel<BN, kMx><<<grid, C::THREADS, C::SMEM_BYTES, s>>>(tmA, tmB, p);
+  kern<<<grid, C::THREADS, C::SMEM_BYTES, s>>>(tmA, tmB, p);
   return launch_status(cudaGetLastError());
 }
 
@@ -1315,10 +1456,10 @@ nvfp4_status run_gemm(const void* a_codes, const void* a_sf, const float* g_a, c
 template <bool kMx>
 nvfp4_status dispatch_gemm(const void* a_codes, const void* a_sf, const float* g_a, const void* b_codes,
                            const void* b_sf, const float* g_b, int64_t M, int64_t N, int64_t K, void* d, int64_t ldd,
-                           nvfp4_out_dtype out, const QuantOut* q, cudaStream_t s) {
-  if (N <= 128) return run_gemm<128, kMx>(a_codes, a_sf, g_a, b_codes, b_sf, g_b, M, N, K, d, ldd, out, q, s);
-  if (M <= 128) return run_gemm<256, kMx>(a_codes, a_sf, g_a, b_codes, b_sf, g_b, M, N, K, d, ldd, out, q, s);
-  return run_gemm_pair<kMx>(a_codes, a_sf, g_a, b_codes, b_sf, g_b, M, N, K, d, ldd, out, q, s);
+                           nvfp4_out_dtype out, const QuantOut* q, cudaStream_t s, const Epilogue* epi = nullptr) {
+  if (N <= 128) return run_gemm<128, kMx>(a_codes, a_sf, g_a, b_codes, b_sf, g_b, M, N, K, d, ldd, out, q, s, epi);
+  if (M <= 128) return run_gemm<256, kMx>(a_codes, a_sf, g_a, b_codes, b_sf, g_b, M, N, K, d, ldd, out, q, s, epi);
+  return run_gemm_pair<kMx>(a_codes, a_sf, g_a, b_codes, b_sf, g_b, M, N, K, d, ldd, out, q, s, nullptr, epi);
 }
 
 nvfp4_status launch_gemm(const void* a_codes, const void* a_sf, const float* g_a, const void* b_codes,
@@ -1335,6 +1476,16 @@ nvfp4_status launch_gemm_q(const void* a_codes, const void* a_sf, const float* g
     if (e != cudaSuccess) return launch_status(e);
   }
   return dispatch_gemm<false>(a_codes, a_sf, g_a, b_codes, b_sf, g_b, M, N, K, d, ldd_bytes, NVFP4_OUT_BF16, &q, s);
+}
+
+nvfp4_status launch_gemm_epilogue(const void* a_codes, const void* a_sf, const float* g_a, const void* b_codes,
+                                  const void* b_sf, const float* g_b, int64_t M, int64_t N, int64_t K, void* d,
+                                  int64_t ldd, nvfp4_out_dtype out, const Epilogue& e, cudaStream_t s) {
+  if (e.amax_d) {
+    const cudaError_t err = cudaMemsetAsync(e.amax_d, 0, sizeof(float), s);
+    if (err != cudaSuccess) return launch_status(err);
+  }
+  return dispatch_gemm<false>(a_codes, a_sf, g_a, b_codes, b_sf, g_b, M, N, K, d, ldd, out, nullptr, s, &e);
 }
 
 // K chunks of one A row in the quantize-and-GEMM kernel (units of

@@ -17,6 +17,7 @@
 
 #include <atomic>
 
+#include "epilogue.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 #include "quant_core.cuh"
@@ -45,6 +46,31 @@ constexpr int GV_THREADS = (2 + GV_EPI_WARPS) * 32;
 constexpr int GV_SMEM_BYTES = GV_STAGES * GV_STAGE_BYTES + 256 + 1024;
 static_assert(GV_SF_BASE + GV_STAGES * GV_SF_COLS_PER_STAGE <= (int)TMEM_COLS, "TMEM budget");
 
+// Output m, n of a product row: v = alpha * acc, or with kE the epilogue
+// act(alpha * acc + bias) + residual (bias: the value of column n, loaded once
+// per column).
+struct GemvEpi {
+  const void* bias;
+  int bias_f32;
+  int act;
+  const __nv_bfloat16* residual;
+  int64_t ldr;
+};
+
+template <bool kE>
+__device__ __forceinline__ float gv_bias(const GemvEpi& e, int n, int n_end) {
+  if constexpr (!kE) return 0.0f;
+  return e.bias && n < n_end ? load_param(e.bias, e.bias_f32, n) : 0.0f;
+}
+
+template <bool kE>
+__device__ __forceinline__ __nv_bfloat16 gv_out(const GemvEpi& e, int m, int n, float acc, float alpha, float bias) {
+  if constexpr (!kE) return __float2bfloat16_rn(acc * alpha);
+  float v = act_value(fmaf(acc, alpha, bias), e.act);
+  if (e.residual) v += __bfloat162float(e.residual[static_cast<int64_t>(m) * e.ldr + n]);
+  return __float2bfloat16_rn(v);
+}
+
 struct GemvParams {
   const uint8_t* wsf;      // weight scales, tensor-core layout
   const uint8_t* xsf;      // activation scales, tensor-core layout (128 padded rows)
@@ -54,6 +80,7 @@ struct GemvParams {
   int* counters;           // [tiles * 4] arrivals per (weight tile, 32-row quarter); cleared by the prologue
   __nv_bfloat16* y;
   int64_t ldy;
+  GemvEpi epi;
   int M, N, K;
   int kb4;
   int tiles;
@@ -74,6 +101,7 @@ __device__ __forceinline__ int gv_stage_k(int u, int tile, int num_kt) {
   return k >= num_kt ? k - num_kt : k;
 }
 
+template <bool kE>
 __global__ void __launch_bounds__(GV_THREADS, 1)
     gemv_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                 const GemvParams p) {
@@ -277,11 +305,12 @@ __global__ void __launch_bounds__(GV_THREADS, 1)
       }
       const int col = quad * 32 + lane;                         // row of the weight tile
       const int n = tile * BM + col;                            // output column
+      const float bias = gv_bias<kE>(p.epi, n, p.N);
       if (has_head && has_tail) {
         if (n < p.N) {
 #pragma unroll
           for (int m = 0; m < GV_N; ++m)
-            if (m < p.M) p.y[static_cast<int64_t>(m) * p.ldy + n] = __float2bfloat16_rn(__uint_as_float(v[m]) * alpha);
+            if (m < p.M) p.y[static_cast<int64_t>(m) * p.ldy + n] = gv_out<kE>(p.epi, m, n, __uint_as_float(v[m]), alpha, bias);
         }
         continue;
       }
@@ -302,7 +331,7 @@ __global__ void __launch_bounds__(GV_THREADS, 1)
           for (int m = 0; m < GV_N; ++m)
             if (m < p.M) {
               const float sum = __uint_as_float(v[m]) + __ldcg(other + m * BM + col);
-              p.y[static_cast<int64_t>(m) * p.ldy + n] = __float2bfloat16_rn(sum * alpha);
+              p.y[static_cast<int64_t>(m) * p.ldy + n] = gv_out<kE>(p.epi, m, n, sum, alpha, bias);
             }
         }
         continue;
@@ -322,7 +351,7 @@ __global__ void __launch_bounds__(GV_THREADS, 1)
           for (int m = 0; m < GV_N; ++m)
             if (m < p.M) {
               const float sum = __uint_as_float(v[m]) + __ldcg(other + m * BM + col);
-              p.y[static_cast<int64_t>(m) * p.ldy + n] = __float2bfloat16_rn(sum * alpha);
+              p.y[static_cast<int64_t>(m) * p.ldy + n] = gv_out<kE>(p.epi, m, n, sum, alpha, bias);
             }
         }
       }
@@ -391,6 +420,7 @@ struct GemvFusedParams {
   unsigned long long tag;  // this launch's 48-bit tag (never 0)
   __nv_bfloat16* y;
   int64_t ldy;
+  GemvEpi epi;
   int M, N, K;
   int kb4;
   int tiles;
@@ -413,6 +443,7 @@ __device__ __forceinline__ int tagged_arrive(unsigned long long* c, unsigned lon
   return 0;   // two contributors per tile cannot contend 64 times; reached only on corruption
 }
 
+template <bool kE>
 __global__ void __launch_bounds__(GF_THREADS, 1)
     gemv_fused_kernel(const __grid_constant__ CUtensorMap tmW, const GemvFusedParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -654,11 +685,12 @@ __global__ void __launch_bounds__(GF_THREADS, 1)
       }
       const int col = quad * 32 + lane;
       const int n = tile * BM + col;
+      const float bias = gv_bias<kE>(p.epi, n, p.N);
       if (has_head && has_tail) {
         if (n < p.N) {
 #pragma unroll
           for (int m = 0; m < GF_MAX_M; ++m)
-            if (m < p.M) p.y[static_cast<int64_t>(m) * p.ldy + n] = __float2bfloat16_rn(__uint_as_float(v[m]) * alpha);
+            if (m < p.M) p.y[static_cast<int64_t>(m) * p.ldy + n] = gv_out<kE>(p.epi, m, n, __uint_as_float(v[m]), alpha, bias);
         }
         continue;
       }
@@ -677,7 +709,7 @@ __global__ void __launch_bounds__(GF_THREADS, 1)
           for (int m = 0; m < GF_MAX_M; ++m)
             if (m < p.M) {
               const float sum = __uint_as_float(v[m]) + __ldcg(other + m * BM + col);
-              p.y[static_cast<int64_t>(m) * p.ldy + n] = __float2bfloat16_rn(sum * alpha);
+              p.y[static_cast<int64_t>(m) * p.ldy + n] = gv_out<kE>(p.epi, m, n, sum, alpha, bias);
             }
         }
         if (lane == 0) *reinterpret_cast<volatile unsigned long long*>(counter) = 0ull;   // tile done: reset
@@ -698,7 +730,7 @@ __global__ void __launch_bounds__(GF_THREADS, 1)
           for (int m = 0; m < GF_MAX_M; ++m)
             if (m < p.M) {
               const float sum = __uint_as_float(v[m]) + __ldcg(other + m * BM + col);
-              p.y[static_cast<int64_t>(m) * p.ldy + n] = __float2bfloat16_rn(sum * alpha);
+              p.y[static_cast<int64_t>(m) * p.ldy + n] = gv_out<kE>(p.epi, m, n, sum, alpha, bias);
             }
         }
         if (lane == 0) *reinterpret_cast<volatile unsigned long long*>(counter) = 0ull;   // tile done: reset
@@ -921,9 +953,14 @@ unsigned long long next_launch_tag() {
   }
 }
 
+static GemvEpi gemv_epi(const Epilogue* e) {
+  if (!e) return GemvEpi{};
+  return GemvEpi{e->bias, e->bias_f32, e->act, static_cast<const __nv_bfloat16*>(e->residual), e->ldr};
+}
+
 static nvfp4_status launch_gemv_fused(const void* x, int64_t M, int64_t ldx, const void* w_codes, const void* w_sf,
                                       const float* g_w, int64_t N, int64_t K, void* y, int64_t ldy,
-                                      const GemvWs& L, uint8_t* base, cudaStream_t s) {
+                                      const GemvWs& L, uint8_t* base, cudaStream_t s, const Epilogue* epi) {
   const int tiles = static_cast<int>((N + BM - 1) / BM);
   const int sms = device_sm_count();
   CUtensorMap tmW;
@@ -938,6 +975,7 @@ static nvfp4_status launch_gemv_fused(const void* x, int64_t M, int64_t ldx, con
   p.tag = next_launch_tag();
   p.y = static_cast<__nv_bfloat16*>(y);
   p.ldy = ldy;
+  p.epi = gemv_epi(epi);
   p.M = static_cast<int>(M);
   p.N = static_cast<int>(N);
   p.K = static_cast<int>(K);
@@ -949,17 +987,19 @@ static nvfp4_status launch_gemv_fused(const void* x, int64_t M, int64_t ldx, con
   if (!p.status) return NVFP4_ERR_CUDA;
   int grid = tiles < sms ? tiles : sms;       // grid <= tiles: at most two contributors per tile
   if (grid > GV_MAX_CTAS) grid = GV_MAX_CTAS;
-  cudaError_t e = cudaFuncSetAttribute(gemv_fused_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GF_SMEM_BYTES);
+  auto kern = epi ? gemv_fused_kernel<true> : gemv_fused_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GF_SMEM_BYTES);
   if (e != cudaSuccess) return launch_status(e);
-  gemv_fused_kernel<<<grid, GF_THREADS, GF_SMEM_BYTES, s>>>(tmW, p);
+  kern<<<grid, GF_THREADS, GF_SMEM_BYTES, s>>>(tmW, p);
   return launch_status(cudaGetLastError());
 }
 
 nvfp4_status launch_gemv(const void* x, int64_t M, int64_t ldx, const void* w_codes, const void* w_sf,
-                         const float* g_w, int64_t N, int64_t K, void* y, int64_t ldy, void* ws, cudaStream_t s) {
+                         const float* g_w, int64_t N, int64_t K, void* y, int64_t ldy, void* ws, cudaStream_t s,
+                         const Epilogue* epi) {
   const GemvWs L = gemv_ws_layout(M, N, K);
   if (M <= GF_MAX_M && K <= GF_MAX_K && static_cast<int64_t>((N + BM - 1) / BM) * ((K + BK - 1) / BK) < (int64_t{1} << 30))
-    return launch_gemv_fused(x, M, ldx, w_codes, w_sf, g_w, N, K, y, ldy, L, static_cast<uint8_t*>(ws), s);
+    return launch_gemv_fused(x, M, ldx, w_codes, w_sf, g_w, N, K, y, ldy, L, static_cast<uint8_t*>(ws), s, epi);
   uint8_t* base = static_cast<uint8_t*>(ws);
   uint8_t* xq = base + L.xq;
   uint8_t* xsf = base + L.xsf;
@@ -1002,6 +1042,7 @@ nvfp4_status launch_gemv(const void* x, int64_t M, int64_t ldx, const void* w_co
   p.counters = cnt;
   p.y = static_cast<__nv_bfloat16*>(y);
   p.ldy = ldy;
+  p.epi = gemv_epi(epi);
   p.M = static_cast<int>(M);
   p.N = static_cast<int>(N);
   p.K = static_cast<int>(K);
@@ -1015,7 +1056,8 @@ nvfp4_status launch_gemv(const void* x, int64_t M, int64_t ldx, const void* w_co
   // of stages, so each tile has at most two contributors
   int grid = tiles < sms ? tiles : sms;
   if (grid > GV_MAX_CTAS) grid = GV_MAX_CTAS;
-  cudaError_t e = cudaFuncSetAttribute(gemv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GV_SMEM_BYTES);
+  auto kern = epi ? gemv_kernel<true> : gemv_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GV_SMEM_BYTES);
   if (e != cudaSuccess) return launch_status(e);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
@@ -1027,7 +1069,7 @@ nvfp4_status launch_gemv(const void* x, int64_t M, int64_t ldx, const void* w_co
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, gemv_kernel, tmW, tmX, p);
+  e = cudaLaunchKernelEx(&cfg, kern, tmW, tmX, p);
   return launch_status(e);
 }
 

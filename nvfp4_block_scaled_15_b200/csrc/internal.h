@@ -84,9 +84,84 @@ nvfp4_status launch_gemm_quant_a_fused(const void* a_bf16, int64_t lda, const fl
 nvfp4_status launch_mx_gemm(const void* a_codes, const void* a_sf, const void* b_codes, const void* b_sf,
                             int64_t M, int64_t N, int64_t K, void* d, int64_t ldd, nvfp4_out_dtype out,
                             cudaStream_t s);
+// Epilogue of a product: d = act(alpha acc + bias) [+ residual], optionally
+// pre = alpha acc + bias and max |d| (gemm only).
+struct Epilogue {
+  const void* bias;        // [N] or null
+  int bias_f32;
+  int act;                 // nvfp4_act
+  const void* residual;    // the type of d, or null
+  int64_t ldr;
+  void* pre;               // the type of d, or null
+  int64_t ldp;
+  float* amax_d;           // or null
+};
 nvfp4_status launch_gemv(const void* x, int64_t M, int64_t ldx, const void* w_codes, const void* w_sf,
-                         const float* g_w, int64_t N, int64_t K, void* y, int64_t ldy, void* ws, cudaStream_t s);
+                         const float* g_w, int64_t N, int64_t K, void* y, int64_t ldy, void* ws, cudaStream_t s,
+                         const Epilogue* epi = nullptr);
 size_t gemv_workspace_bytes(int64_t M, int64_t N, int64_t K);
+// Layer norm and its gradient (arguments as in nvfp4.h, already validated).
+struct LayerNorm {
+  const void* x;
+  nvfp4_dtype x_dtype;
+  int64_t rows, k, ldx;
+  const void* gamma;
+  const void* beta;
+  nvfp4_dtype param_dtype;
+  float eps;
+  void* y;
+  nvfp4_dtype y_dtype;
+  int64_t ldy;
+  float* mean;
+  float* rstd;
+  float* amax;
+};
+nvfp4_status launch_layernorm(const LayerNorm& a, cudaStream_t s);
+struct LayerNormBackward {
+  const void* dy;
+  nvfp4_dtype dy_dtype;
+  int64_t lddy;
+  const void* x;
+  nvfp4_dtype x_dtype;
+  int64_t ldx;
+  const float* mean;
+  const float* rstd;
+  const void* gamma;
+  nvfp4_dtype param_dtype;
+  const void* residual;
+  int64_t ldr;
+  int64_t rows, k;
+  void* dx;
+  int64_t lddx;
+  float* dgamma;
+  float* dbeta;
+  float* amax;
+  void* workspace;
+};
+nvfp4_status launch_layernorm_backward(const LayerNormBackward& a, cudaStream_t s);
+size_t layernorm_backward_workspace_bytes(int64_t rows, int64_t k);
+nvfp4_status launch_gemm_epilogue(const void* a_codes, const void* a_sf, const float* g_a, const void* b_codes,
+                                  const void* b_sf, const float* g_b, int64_t M, int64_t N, int64_t K, void* d,
+                                  int64_t ldd, nvfp4_out_dtype out, const Epilogue& e, cudaStream_t s);
+// Gradient of that epilogue.
+struct EpilogueBackward {
+  const void* dd;
+  int64_t ldd;
+  const void* pre;
+  int64_t ldp;
+  nvfp4_dtype dtype;
+  int act;
+  int64_t M, N;
+  void* dpre;
+  int64_t lddp;
+  float* dbias;
+  float* amax;
+  void* workspace;
+};
+nvfp4_status launch_epilogue_backward(const EpilogueBackward& a, cudaStream_t s);
+size_t epilogue_backward_workspace_bytes(int64_t M, int64_t N);
+// out[i] = sum over c < chunks of partial[c * stride + i], i < n.
+void launch_sum_chunks(const float* partial, int chunks, int64_t stride, int64_t n, float* out, cudaStream_t s);
 // Per-launch 48-bit tag of workspace counters (never 0).
 unsigned long long next_launch_tag();
 

@@ -37,8 +37,20 @@ OUT_F32 = 1
 # nvfp4_op
 OP_GEMV_BATCHED = 1
 OP_GEMM_QUANT_A = 2
+OP_LAYERNORM_BACKWARD = 3
+OP_EPILOGUE_BACKWARD = 4
+# nvfp4_dtype
+DTYPE_BF16 = 0
+DTYPE_F32 = 1
+# nvfp4_act
+ACT_NONE = 0
+ACT_RELU = 1
+ACT_GELU = 2
+ACT_GELU_TANH = 3
+ACT_SILU = 4
 
 _vp, _i64, _sz, _i32, _u64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int, ctypes.c_uint64
+_f32 = ctypes.c_float
 _SIGS = {
     "nvfp4_abi_version": ([], _i32),
     "nvfp4_status_string": ([_i32], ctypes.c_char_p),
@@ -66,6 +78,15 @@ _SIGS = {
     "nvfp4_mxfp4_sf_bytes": ([_i64, _i64, _i32], _sz),
     "nvfp4_mxfp4_quantize": ([_vp, _i64, _i64, _i64, _vp, _vp, _i32, _vp], _i32),
     "nvfp4_mxfp4_gemm": ([_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _i32, _vp], _i32),
+    "nvfp4_layernorm": ([_vp, _i32, _i64, _i64, _i64, _vp, _vp, _i32, _f32, _vp, _i32, _i64, _vp, _vp, _vp, _vp], _i32),
+    "nvfp4_layernorm_backward": ([_vp, _i32, _i64, _vp, _i32, _i64, _vp, _vp, _vp, _i32, _vp, _i64, _i64, _i64, _vp,
+                                  _i64, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
+    "nvfp4_gemm_epilogue": ([_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _i32, _i32, _vp, _i64, _vp, _i64,
+                             _i32, _vp, _i64, _vp, _vp], _i32),
+    "nvfp4_gemv_batched_epilogue": ([_vp, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _i32, _i32, _vp, _i64, _vp, _i64,
+                                     _vp, _sz, _vp], _i32),
+    "nvfp4_epilogue_backward": ([_vp, _i64, _vp, _i64, _i32, _i32, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _sz, _vp],
+                                _i32),
     "nvfp4_check_device_status": ([_vp], _i32),
     "nvfp4_set_wait_limit_ns": ([_u64], None),
     "nvfp4_selftest_wait_timeout": ([_u64, _vp], _i32),
@@ -222,6 +243,40 @@ def nvfp4_mxfp4_quantize(x, rows, k, ldx, codes, sf, layout, stream=None) -> Non
 def nvfp4_mxfp4_gemm(a_codes, a_sf, b_codes, b_sf, m, n, k, d, ldd, out_dtype=OUT_BF16, stream=None) -> None:
     _check(_lib.nvfp4_mxfp4_gemm(_p(a_codes), _p(a_sf), _p(b_codes), _p(b_sf), m, n, k, _p(d), ldd, out_dtype,
                                  _s(stream)), "nvfp4_mxfp4_gemm")
+
+
+def nvfp4_layernorm(x, x_dtype, rows, k, ldx, gamma, beta, param_dtype, eps, y, y_dtype, ldy, mean=None, rstd=None,
+                    amax_dev=None, stream=None) -> None:
+    _check(_lib.nvfp4_layernorm(_p(x), x_dtype, rows, k, ldx, _p(gamma), _p(beta), param_dtype, eps, _p(y), y_dtype,
+                                ldy, _p(mean), _p(rstd), _p(amax_dev), _s(stream)), "nvfp4_layernorm")
+
+
+def nvfp4_layernorm_backward(dy, dy_dtype, lddy, x, x_dtype, ldx, mean, rstd, gamma, param_dtype, d_residual, ldr,
+                             rows, k, dx, lddx, dgamma, dbeta, amax_dx, workspace, ws_bytes, stream=None) -> None:
+    _check(_lib.nvfp4_layernorm_backward(_p(dy), dy_dtype, lddy, _p(x), x_dtype, ldx, _p(mean), _p(rstd), _p(gamma),
+                                         param_dtype, _p(d_residual), ldr, rows, k, _p(dx), lddx, _p(dgamma),
+                                         _p(dbeta), _p(amax_dx), _p(workspace), ws_bytes, _s(stream)),
+           "nvfp4_layernorm_backward")
+
+
+def nvfp4_gemm_epilogue(a_codes, a_sf, g_a, b_codes, b_sf, g_b, m, n, k, bias, bias_dtype, act, residual, ldr, d, ldd,
+                        out_dtype=OUT_BF16, pre=None, ldp=0, amax_d=None, stream=None) -> None:
+    _check(_lib.nvfp4_gemm_epilogue(_p(a_codes), _p(a_sf), _p(g_a), _p(b_codes), _p(b_sf), _p(g_b), m, n, k, _p(bias),
+                                    bias_dtype, act, _p(residual), ldr, _p(d), ldd, out_dtype, _p(pre), ldp,
+                                    _p(amax_d), _s(stream)), "nvfp4_gemm_epilogue")
+
+
+def nvfp4_gemv_batched_epilogue(x, m, ldx, w_codes, w_sf, g_w, n, k, bias, bias_dtype, act, residual, ldr, y, ldy,
+                                workspace, ws_bytes, stream=None) -> None:
+    _check(_lib.nvfp4_gemv_batched_epilogue(_p(x), m, ldx, _p(w_codes), _p(w_sf), _p(g_w), n, k, _p(bias), bias_dtype,
+                                            act, _p(residual), ldr, _p(y), ldy, _p(workspace), ws_bytes, _s(stream)),
+           "nvfp4_gemv_batched_epilogue")
+
+
+def nvfp4_epilogue_backward(dd, ldd, pre, ldp, dtype, act, m, n, dpre, lddp, dbias, amax_dpre, workspace, ws_bytes,
+                            stream=None) -> None:
+    _check(_lib.nvfp4_epilogue_backward(_p(dd), ldd, _p(pre), ldp, dtype, act, m, n, _p(dpre), lddp, _p(dbias),
+                                        _p(amax_dpre), _p(workspace), ws_bytes, _s(stream)), "nvfp4_epilogue_backward")
 
 
 def nvfp4_check_device_status(stream=None) -> int:
@@ -415,3 +470,126 @@ def mxfp4_gemm(a: MXQuantized, b: MXQuantized, out_dtype=torch.bfloat16, out: to
     d = out if out is not None else torch.empty((a.rows, b.rows), dtype=out_dtype, device=a.codes.device)
     nvfp4_mxfp4_gemm(a.codes, a.sf, b.codes, b.sf, a.rows, b.rows, a.k, d, d.stride(0), od, stream)
     return d
+
+
+# ---------------------------------------------------------------------------
+# layer norm and the product epilogues
+# ---------------------------------------------------------------------------
+ACTIVATIONS = {None: ACT_NONE, "none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH,
+               "silu": ACT_SILU}
+
+
+def _dtype_of(t) -> int:
+    """nvfp4_dtype of a tensor (bf16 for None, where the library reads nothing)."""
+    if t is None:
+        return DTYPE_BF16
+    assert t.dtype in (torch.bfloat16, torch.float32), t.dtype
+    return DTYPE_F32 if t.dtype == torch.float32 else DTYPE_BF16
+
+
+def _rows_of(t, shape=None):
+    assert t.dim() == 2 and (t.shape[1] <= 1 or t.stride(1) == 1), "a row-major matrix"
+    assert shape is None or tuple(t.shape) == tuple(shape), (tuple(t.shape), tuple(shape))
+    return max(t.stride(0), t.shape[1])
+
+
+class Normalized:
+    """Result of layernorm: y [rows, k], mean and rstd [rows] fp32, amax (max |y|, one fp32) for quantize(y, amax=)."""
+
+    def __init__(self, y, mean, rstd, amax):
+        self.y, self.mean, self.rstd, self.amax = y, mean, rstd, amax
+
+
+def layernorm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+              eps: float = 1e-5, out_dtype=torch.bfloat16, out: torch.Tensor | None = None,
+              stream=None) -> Normalized:
+    """Layer norm of x [rows, k] (bf16 or fp32); weight and bias [k] of one dtype.  The amax makes the
+    quantizer behind it a single pass: ``quantize(n.y, amax=n.amax)``."""
+    rows, k = x.shape
+    ldx = _rows_of(x)
+    for t in (weight, bias):
+        assert t is None or (t.shape == (k,) and t.is_contiguous()), "contiguous [k] weight and bias"
+    assert weight is None or bias is None or weight.dtype == bias.dtype, "weight and bias of one dtype"
+    y = out if out is not None else torch.empty((rows, k), dtype=out_dtype, device=x.device)
+    stats = torch.empty(2 * rows + 1, dtype=torch.float32, device=x.device)
+    mean, rstd, amax = stats[:rows], stats[rows:2 * rows], stats[2 * rows:]
+    nvfp4_layernorm(x, _dtype_of(x), rows, k, ldx, weight, bias, _dtype_of(weight if weight is not None else bias), eps,
+                    y, _dtype_of(y), _rows_of(y, (rows, k)), mean, rstd, amax, stream)
+    return Normalized(y, mean, rstd, amax)
+
+
+def layernorm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                       weight: torch.Tensor | None = None, d_residual: torch.Tensor | None = None,
+                       out: torch.Tensor | None = None, workspace=None, stream=None):
+    """(dx, dweight, dbias, amax of dx): dx in x's dtype with d_residual added, dweight and dbias fp32."""
+    rows, k = x.shape
+    for t in (mean, rstd):
+        assert t.shape == (rows,) and t.dtype == torch.float32 and t.is_contiguous(), "mean and rstd of the forward call"
+    assert weight is None or (weight.shape == (k,) and weight.is_contiguous()), "contiguous [k] weight"
+    assert d_residual is None or d_residual.dtype == x.dtype, "d_residual in x's dtype"
+    dx = out if out is not None else torch.empty((rows, k), dtype=x.dtype, device=x.device)
+    assert dx.dtype == x.dtype, "dx in x's dtype"
+    grads = torch.empty(2 * k + 1, dtype=torch.float32, device=x.device)
+    ws_bytes = nvfp4_workspace_bytes(OP_LAYERNORM_BACKWARD, rows, k, 0)
+    ws = workspace if workspace is not None else torch.empty(ws_bytes, dtype=torch.uint8, device=x.device)
+    nvfp4_layernorm_backward(dy, _dtype_of(dy), _rows_of(dy, (rows, k)), x, _dtype_of(x), _rows_of(x), mean, rstd, weight,
+                             _dtype_of(weight), d_residual, 0 if d_residual is None else _rows_of(d_residual, (rows, k)),
+                             rows, k, dx, _rows_of(dx, (rows, k)), grads[:k], grads[k:2 * k], grads[2 * k:], ws,
+                             ws.numel(), stream)
+    return dx, grads[:k], grads[k:2 * k], grads[2 * k:]
+
+
+def _check_epilogue(m, n, bias, residual, dtype) -> int:
+    assert bias is None or (bias.shape == (n,) and bias.is_contiguous()), "contiguous [n] bias"
+    assert residual is None or residual.dtype == dtype, "residual in the output's dtype"
+    return 0 if residual is None else _rows_of(residual, (m, n))
+
+
+def gemm_epilogue(a: Quantized, b: Quantized, bias: torch.Tensor | None = None, act: str | None = None,
+                  residual: torch.Tensor | None = None, out_dtype=torch.bfloat16, out: torch.Tensor | None = None,
+                  pre: torch.Tensor | bool = False, amax: torch.Tensor | None = None, stream=None):
+    """D = act(alpha (s_a A)(s_b B)^T + bias) + residual.  pre: a tensor (or True: a new one, returned as
+    (D, pre)) for the value before act; amax: one fp32 on the device that receives max |D|."""
+    assert a.layout == SF_TCGEN05 and b.layout == SF_TCGEN05 and a.k == b.k
+    m, n = a.rows, b.rows
+    d = out if out is not None else torch.empty((m, n), dtype=out_dtype, device=a.codes.device)
+    p = torch.empty((m, n), dtype=d.dtype, device=d.device) if pre is True else (None if pre is False else pre)
+    assert p is None or p.dtype == d.dtype, "pre in the output's dtype"
+    ldr = _check_epilogue(m, n, bias, residual, d.dtype)
+    nvfp4_gemm_epilogue(a.codes, a.sf, a.g, b.codes, b.sf, b.g, m, n, a.k, bias, _dtype_of(bias), ACTIVATIONS[act],
+                        residual, ldr, d, _rows_of(d, (m, n)), _dtype_of(d), p, 0 if p is None else _rows_of(p, (m, n)),
+                        amax, stream)
+    return (d, p) if pre is True else d
+
+
+def gemv_batched_epilogue(x: torch.Tensor, w: Quantized, bias: torch.Tensor | None = None, act: str | None = None,
+                          residual: torch.Tensor | None = None, out: torch.Tensor | None = None, workspace=None,
+                          stream=None) -> torch.Tensor:
+    """y [M, N] = act(x w^T + bias) + residual for bf16 activations x [M, K] (M <= 32) and NVFP4 weights w."""
+    assert x.dtype == torch.bfloat16 and x.shape[1] == w.k and w.layout == SF_TCGEN05
+    m, k = x.shape
+    n = w.rows
+    ws_bytes = nvfp4_workspace_bytes(OP_GEMV_BATCHED, m, n, k)
+    ws = workspace if workspace is not None else torch.empty(ws_bytes, dtype=torch.uint8, device=x.device)
+    y = out if out is not None else torch.empty((m, n), dtype=torch.bfloat16, device=x.device)
+    assert y.dtype == torch.bfloat16
+    ldr = _check_epilogue(m, n, bias, residual, y.dtype)
+    nvfp4_gemv_batched_epilogue(x, m, _rows_of(x), w.codes, w.sf, w.g, n, k, bias, _dtype_of(bias), ACTIVATIONS[act],
+                                residual, ldr, y, _rows_of(y, (m, n)), ws, ws.numel(), stream)
+    return y
+
+
+def epilogue_backward(dd: torch.Tensor, pre: torch.Tensor | None, act: str | None = None,
+                      out: torch.Tensor | None = None, workspace=None, stream=None):
+    """(dpre, dbias, amax of dpre) of D = act(pre) [+ residual], pre = product + bias; dbias fp32."""
+    m, n = dd.shape
+    assert pre is None or pre.dtype == dd.dtype, "pre in dd's dtype"
+    dpre = out if out is not None else torch.empty((m, n), dtype=dd.dtype, device=dd.device)
+    assert dpre.dtype == dd.dtype, "dpre in dd's dtype"
+    grads = torch.empty(n + 1, dtype=torch.float32, device=dd.device)
+    ws_bytes = nvfp4_workspace_bytes(OP_EPILOGUE_BACKWARD, m, n, 0)
+    ws = workspace if workspace is not None else torch.empty(ws_bytes, dtype=torch.uint8, device=dd.device)
+    nvfp4_epilogue_backward(dd, _rows_of(dd), pre, 0 if pre is None else _rows_of(pre, (m, n)), _dtype_of(dd),
+                            ACTIVATIONS[act], m, n, dpre, _rows_of(dpre, (m, n)), grads[:n], grads[n:], ws, ws.numel(),
+                            stream)
+    return dpre, grads[:n], grads[n:]

@@ -1,0 +1,115 @@
+"""Argument checks of the layer norm and product epilogue entry points (no GPU needed): refusals come before any
+device work, valid arguments stop only at the device check."""
+import pytest
+import torch
+
+FAKE = 1 << 20                      # 16-byte aligned, never dereferenced
+
+
+@pytest.fixture(scope="module")
+def nv():
+    from nvfp4_block_scaled_15_b200 import build
+    build.build()
+    from nvfp4_block_scaled_15_b200 import nvfp4
+    return nvfp4
+
+
+def call(nv, name, base, **change):
+    args = dict(base)
+    assert set(change) <= set(args), change
+    args.update(change)
+    return nv.raw_status(name, *args.values())
+
+
+def passes(nv, status):
+    return status in ((nv.ERR_CUDA, nv.ERR_ARCH) if not torch.cuda.is_available() else (nv.OK,))
+
+
+LN = dict(x=FAKE, x_dtype=0, rows=4, k=33, ldx=33, gamma=FAKE, beta=FAKE, p_dtype=1, eps=1e-5, y=FAKE, y_dtype=0, ldy=33,
+          mean=FAKE, rstd=FAKE, amax=FAKE, stream=None)
+LNB = dict(dy=FAKE, dy_dtype=0, lddy=33, x=FAKE, x_dtype=0, ldx=33, mean=FAKE, rstd=FAKE, gamma=FAKE, p_dtype=0, res=None,
+           ldr=0, rows=4, k=33, dx=FAKE, lddx=33, dgamma=FAKE, dbeta=FAKE, amax=FAKE, ws=FAKE, ws_bytes=1 << 30, stream=None)
+GEMM = dict(a=FAKE, a_sf=FAKE, g_a=FAKE, b=FAKE, b_sf=FAKE, g_b=FAKE, m=8, n=10, k=64, bias=FAKE, b_dtype=0, act=2,
+            res=None, ldr=0, d=FAKE, ldd=10, out=0, pre=None, ldp=0, amax=FAKE, stream=None)
+GEMV = dict(x=FAKE, m=4, ldx=64, w=FAKE, w_sf=FAKE, g_w=FAKE, n=10, k=64, bias=FAKE, b_dtype=0, act=2, res=None, ldr=0,
+            y=FAKE, ldy=10, ws=FAKE, ws_bytes=1 << 30, stream=None)
+EB = dict(dd=FAKE, ldd=10, pre=FAKE, ldp=10, dtype=0, act=2, m=8, n=10, dpre=FAKE + (1 << 16), lddp=10, dbias=FAKE,
+          amax=FAKE, ws=FAKE, ws_bytes=1 << 30, stream=None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(rows=-1), "INVALID_ARG"), (dict(k=0, ldx=0, ldy=0), "INVALID_ARG"), (dict(ldx=32), "INVALID_ARG"),
+    (dict(ldy=32), "INVALID_ARG"), (dict(x=None), "INVALID_ARG"), (dict(y=None), "INVALID_ARG"),
+    (dict(x_dtype=2), "INVALID_ARG"), (dict(y_dtype=-1), "INVALID_ARG"), (dict(p_dtype=7), "INVALID_ARG"),
+    (dict(eps=-1e-5), "INVALID_ARG"), (dict(eps=float("nan")), "INVALID_ARG"), (dict(eps=float("inf")), "INVALID_ARG"),
+    (dict(rows=1 << 31), "UNSUPPORTED_SHAPE"), (dict(k=1 << 31, ldx=1 << 31, ldy=1 << 31), "UNSUPPORTED_SHAPE"),
+    (dict(x=FAKE + 1), "MISALIGNED"), (dict(x=FAKE + 2, x_dtype=1), "MISALIGNED"), (dict(y=FAKE + 1), "MISALIGNED"),
+    (dict(gamma=FAKE + 2), "MISALIGNED"), (dict(beta=FAKE + 1, p_dtype=0), "MISALIGNED"), (dict(mean=FAKE + 2), "MISALIGNED"),
+    (dict(amax=FAKE + 1), "MISALIGNED")], ids=str)
+def test_layernorm_refuses(nv, change, status):
+    assert call(nv, "nvfp4_layernorm", LN, **change) == getattr(nv, "ERR_" + status)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(rows=-1), "INVALID_ARG"), (dict(k=0), "INVALID_ARG"), (dict(dy=None), "INVALID_ARG"),
+    (dict(mean=None), "INVALID_ARG"), (dict(rstd=None), "INVALID_ARG"), (dict(dx=None), "INVALID_ARG"),
+    (dict(lddy=32), "INVALID_ARG"), (dict(lddx=32), "INVALID_ARG"), (dict(res=FAKE + 64, ldr=32), "INVALID_ARG"),
+    (dict(res=FAKE, ldr=40), "INVALID_ARG"), (dict(dy_dtype=3), "INVALID_ARG"), (dict(ws=None), "INVALID_ARG"),
+    (dict(ws_bytes=64), "WORKSPACE"), (dict(ws=FAKE + 8), "MISALIGNED"), (dict(dgamma=FAKE + 2), "MISALIGNED"),
+    (dict(res=FAKE + 1, ldr=33), "MISALIGNED"), (dict(rows=1 << 31), "UNSUPPORTED_SHAPE")], ids=str)
+def test_layernorm_backward_refuses(nv, change, status):
+    assert call(nv, "nvfp4_layernorm_backward", LNB, **change) == getattr(nv, "ERR_" + status)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(m=0), "INVALID_ARG"), (dict(k=96), "UNSUPPORTED_SHAPE"), (dict(act=5), "INVALID_ARG"), (dict(act=-1), "INVALID_ARG"),
+    (dict(b_dtype=2), "INVALID_ARG"), (dict(out=2), "INVALID_ARG"), (dict(ldd=9), "INVALID_ARG"), (dict(d=None), "INVALID_ARG"),
+    (dict(res=FAKE + 64, ldr=9), "INVALID_ARG"), (dict(res=FAKE, ldr=12), "INVALID_ARG"), (dict(pre=FAKE, ldp=10), "INVALID_ARG"),
+    (dict(pre=FAKE + 64, ldp=9), "INVALID_ARG"), (dict(pre=FAKE + 64, ldp=10, res=FAKE + 64, ldr=10), "INVALID_ARG"),
+    (dict(d=FAKE + 1), "MISALIGNED"), (dict(pre=FAKE + 65, ldp=10), "MISALIGNED"), (dict(bias=FAKE + 1), "MISALIGNED"),
+    (dict(bias=FAKE + 2, b_dtype=1), "MISALIGNED"), (dict(a=FAKE + 8), "MISALIGNED"), (dict(amax=FAKE + 2), "MISALIGNED"),
+    (dict(res=FAKE + 66, ldr=10, out=1), "MISALIGNED")], ids=str)
+def test_gemm_epilogue_refuses(nv, change, status):
+    assert call(nv, "nvfp4_gemm_epilogue", GEMM, **change) == getattr(nv, "ERR_" + status)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(m=33), "UNSUPPORTED_SHAPE"), (dict(m=0), "INVALID_ARG"), (dict(act=9), "INVALID_ARG"), (dict(b_dtype=2), "INVALID_ARG"),
+    (dict(res=FAKE, ldr=12), "INVALID_ARG"), (dict(res=FAKE + 64, ldr=9), "INVALID_ARG"), (dict(res=FAKE + 1, ldr=10), "MISALIGNED"),
+    (dict(bias=FAKE + 1), "MISALIGNED"), (dict(ws_bytes=64), "WORKSPACE"), (dict(ws=None), "INVALID_ARG"),
+    (dict(ldy=9), "INVALID_ARG")], ids=str)
+def test_gemv_epilogue_refuses(nv, change, status):
+    assert call(nv, "nvfp4_gemv_batched_epilogue", GEMV, **change) == getattr(nv, "ERR_" + status)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(m=-1), "INVALID_ARG"), (dict(n=0), "INVALID_ARG"), (dict(pre=None), "INVALID_ARG"), (dict(dd=None), "INVALID_ARG"),
+    (dict(act=6), "INVALID_ARG"), (dict(dtype=2), "INVALID_ARG"), (dict(ldd=9), "INVALID_ARG"), (dict(lddp=9), "INVALID_ARG"),
+    (dict(dpre=FAKE, lddp=12), "INVALID_ARG"), (dict(pre=FAKE + (1 << 16)), "INVALID_ARG"), (dict(ws=None), "INVALID_ARG"),
+    (dict(ws_bytes=16), "WORKSPACE"), (dict(ws=FAKE + 4), "MISALIGNED"), (dict(dd=FAKE + 1), "MISALIGNED"),
+    (dict(dbias=FAKE + 1), "MISALIGNED")], ids=str)
+def test_epilogue_backward_refuses(nv, change, status):
+    assert call(nv, "nvfp4_epilogue_backward", EB, **change) == getattr(nv, "ERR_" + status)
+
+
+def test_valid_arguments_stop_at_the_device_check(nv):
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    for name, base, changes in [
+            ("nvfp4_layernorm", LN, [{}, dict(gamma=None, beta=None, mean=None, rstd=None, amax=None), dict(rows=0, x=None, y=None)]),
+            ("nvfp4_layernorm_backward", LNB, [{}, dict(dgamma=None, dbeta=None, ws=None, ws_bytes=0), dict(res=FAKE, ldr=33),
+                                               dict(rows=0, ws=None)]),
+            ("nvfp4_gemm_epilogue", GEMM, [{}, dict(bias=None, act=0, amax=None), dict(res=FAKE, ldr=10)]),
+            ("nvfp4_gemv_batched_epilogue", GEMV, [{}, dict(bias=None, act=0), dict(res=FAKE, ldr=10)]),
+            ("nvfp4_epilogue_backward", EB, [{}, dict(pre=None, act=0), dict(dpre=None), dict(dbias=None, ws=None), dict(m=0)])]:
+        for change in changes:
+            assert passes(nv, call(nv, name, base, **change)), (name, change)
+
+
+def test_workspace_sizes(nv):
+    for op in (nv.OP_LAYERNORM_BACKWARD, nv.OP_EPILOGUE_BACKWARD):
+        assert nv.nvfp4_workspace_bytes(op, 4, 33, 0) > 0
+        assert nv.nvfp4_workspace_bytes(op, 0, 33, 0) > 0
+        assert nv.nvfp4_workspace_bytes(op, -1, 33, 0) == 0
+        assert nv.nvfp4_workspace_bytes(op, 4, 0, 0) == 0
+        assert nv.nvfp4_workspace_bytes(op, 1 << 31, 33, 0) == 0
