@@ -77,8 +77,10 @@ nvfp4_status launch_epilogue_backward(const EpilogueBackward& a, cudaStream_t s)
     epilogue_backward_kernel<float><<<grid, EB_THREADS, 0, s>>>(p, per);
   else
     epilogue_backward_kernel<__nv_bfloat16><<<grid, EB_THREADS, 0, s>>>(p, per);
-  if (a.dbias) launch_sum_chunks(p.partial, chunks, a.N, a.N, a.dbias, s);
-  return launch_status(cudaGetLastError());
+  e = cudaGetLastError();
+  if (e == cudaSuccess && a.dbias)
+    e = launch_sum_partials(p.partial, chunks, a.N, static_cast<int>(a.N), 0, a.dbias, nullptr, nullptr, nullptr, s);
+  return launch_status(e);
 }
 
 }  // namespace nvfp4

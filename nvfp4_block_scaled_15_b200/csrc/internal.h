@@ -160,8 +160,12 @@ struct EpilogueBackward {
 };
 nvfp4_status launch_epilogue_backward(const EpilogueBackward& a, cudaStream_t s);
 size_t epilogue_backward_workspace_bytes(int64_t M, int64_t N);
-// out[i] = sum over c < chunks of partial[c * stride + i], i < n.
-void launch_sum_chunks(const float* partial, int chunks, int64_t stride, int64_t n, float* out, cudaStream_t s);
+// Joins the blocks' partials [blocks][stride] of an earlier kernel on the
+// stream: the sums of the first n0 columns to out0, of the next n1 to out1
+// (either may be null), and max over mags[blocks] (fp32 bits) to *amax (may be
+// null).
+cudaError_t launch_sum_partials(const float* partial, int blocks, int64_t stride, int n0, int n1, float* out0, float* out1,
+                                const uint32_t* mags, float* amax, cudaStream_t s);
 // Per-launch 48-bit tag of workspace counters (never 0).
 unsigned long long next_launch_tag();
 

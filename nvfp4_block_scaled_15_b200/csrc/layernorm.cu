@@ -171,23 +171,574 @@ __global__ void __launch_bounds__(LN_THREADS) ln_backward_params_long_kernel(con
   out[p.k + i] = db;
 }
 
-// out[i] = sum over chunks of partial[c][i]; each column's sum runs over the
-// chunks in order, so the result does not depend on timing.
-__global__ void __launch_bounds__(LN_THREADS) sum_chunks_kernel(const float* partial, int chunks, int64_t stride, int n,
-                                                                 float* out) {
-  const int i = blockIdx.x * LN_THREADS + threadIdx.x;
-  if (i >= n) return;
+// ---------------------------------------------------------------------------
+// Rows held in registers
+// ---------------------------------------------------------------------------
+// A row is cut into chunks of 8 elements; thread t of the T threads that share
+// a row holds chunks t, t + T, ... (kVec: 16-byte accesses; every row of every
+// operand 16-byte aligned), or the single elements t, t + T, ... where some
+// row is not.  col() is the column of a thread's element (chunk j, element e).
+template <bool kVec>
+__device__ __forceinline__ int col(int t, int T, int j, int e) {
+  return kVec ? 8 * (t + T * j) + e : t + T * (8 * j + e);
+}
+
+// Chunk j of a thread: whole (every element inside the row), or element by
+// element where the row ends.
+template <bool kVec>
+__device__ __forceinline__ bool whole(int t, int T, int j, int k) {
+  return kVec ? 8 * (t + T * j) + 8 <= k : t + T * (8 * j + 7) < k;
+}
+
+__device__ __forceinline__ void unpack8(const uint4 w, float (&x)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(u[i] << 16);
+    x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+  }
+}
+
+// Streaming 16-byte load (read once, not kept in L1).
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// Chunk j of a row of x; elements past the row are 0.
+template <typename T, bool kVec>
+__device__ __forceinline__ void load_chunk(const T* row, int t, int nt, int j, int k, float (&x)[8]) {
+  if (whole<kVec>(t, nt, j, k)) {
+    if constexpr (!kVec) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = to_f32(row[col<kVec>(t, nt, j, e)]);
+    } else if constexpr (sizeof(T) == 2) {
+      unpack8(ld_stream(row + col<kVec>(t, nt, j, 0)), x);
+    } else {
+      const uint4 a = ld_stream(row + col<kVec>(t, nt, j, 0)), b = ld_stream(row + col<kVec>(t, nt, j, 4));
+      x[0] = __uint_as_float(a.x), x[1] = __uint_as_float(a.y), x[2] = __uint_as_float(a.z), x[3] = __uint_as_float(a.w);
+      x[4] = __uint_as_float(b.x), x[5] = __uint_as_float(b.y), x[6] = __uint_as_float(b.z), x[7] = __uint_as_float(b.w);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int c = col<kVec>(t, nt, j, e);
+      x[e] = c < k ? to_f32(row[c]) : 0.0f;
+    }
+  }
+}
+
+// The same columns of gamma or beta (cached: every row reads them).
+template <bool kVec>
+__device__ __forceinline__ void load_param_chunk(const void* p, int f32, int t, int nt, int j, int k, float dflt,
+                                                 float (&x)[8]) {
+  if (!p) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = dflt;
+  } else if (kVec && whole<kVec>(t, nt, j, k)) {
+    const int c = col<kVec>(t, nt, j, 0);
+    if (f32) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c));
+      const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c + 4));
+      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    } else {
+      unpack8(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + c)), x);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int c = col<kVec>(t, nt, j, e);
+      x[e] = c < k ? load_param(p, f32, c) : dflt;
+    }
+  }
+}
+
+// Stores a chunk rounded to T; returns the largest stored magnitude.
+template <typename T, bool kVec>
+__device__ __forceinline__ uint32_t store_chunk(T* row, int t, int nt, int j, int k, const float (&x)[8]) {
+  uint32_t mag = 0;
+  if (kVec && whole<kVec>(t, nt, j, k)) {
+    T* out = row + col<kVec>(t, nt, j, 0);
+    if constexpr (sizeof(T) == 2) {
+      uint32_t u[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        u[i] = *reinterpret_cast<const uint32_t*>(&h);
+        mag = __vmaxu2(mag, u[i] & 0x7FFF7FFFu);
+      }
+      *reinterpret_cast<uint4*>(out) = make_uint4(u[0], u[1], u[2], u[3]);
+      mag = max(mag << 16, mag & 0xFFFF0000u);
+    } else {
+      *reinterpret_cast<float4*>(out) = make_float4(x[0], x[1], x[2], x[3]);
+      *reinterpret_cast<float4*>(out + 4) = make_float4(x[4], x[5], x[6], x[7]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) mag = max(mag, mag_bits(x[e]));
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int c = col<kVec>(t, nt, j, e);
+      if (c < k) {
+        const T o = from_f32<T>(x[e]);
+        row[c] = o;
+        mag = max(mag, mag_bits(o));
+      }
+    }
+  }
+  return mag;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+// Forward, WARPS warps per row (one warp: 8 rows per block), NV chunks per
+// thread: one pass over x.  Each warp takes the mean and the squared
+// deviations about it of its own elements; the row's statistics follow from
+// the warps' (sum, deviations) by
+//   mean = sum_w s_w / k,  sum (x - mean)^2 = sum_w (M_w + n_w (s_w / n_w - mean)^2)
+// (no cancellation, as with sum x^2 - k mean^2), so a row needs one barrier.
+template <typename TX, bool kVec, int WARPS, int NV>
+__global__ void __launch_bounds__(WARPS == 1 ? 256 : 32 * WARPS) ln_forward_rows_kernel(const LnParams p) {
+  constexpr int T = 32 * WARPS;
+  constexpr int ROWS = WARPS == 1 ? 8 : 1;
+  __shared__ float2 red[2][WARPS];
+  __shared__ uint32_t mags[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = WARPS == 1 ? lane : threadIdx.x;
+  const float inv_k = 1.0f / static_cast<float>(p.k);
+  // elements of this warp, of warp w
+  auto count = [&](int w) {
+    int n = 0;
+    if constexpr (kVec) {
+      for (int j = 0; j < NV; ++j) n += min(max(p.k - 8 * (32 * w + T * j), 0), 256);
+    } else {
+      for (int j = 0; j < 8 * NV; ++j) n += min(max(p.k - (32 * w + T * j), 0), 32);
+    }
+    return static_cast<float>(n);
+  };
+  const float n_own = count(WARPS == 1 ? 0 : warp);
+  const float inv_own = n_own > 0.0f ? 1.0f / n_own : 0.0f;
+  const float n_lane = WARPS > 1 && lane < WARPS ? count(lane) : 0.0f;
+  const float inv_lane = n_lane > 0.0f ? 1.0f / n_lane : 0.0f;
+  uint32_t mag = 0;
+  int parity = 0;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * ROWS;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * ROWS + (WARPS == 1 ? warp : 0); r < p.rows; r += step) {
+    const TX* row = static_cast<const TX*>(p.x) + r * p.ldx;
+    float x[NV][8];
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) load_chunk<TX, kVec>(row, t, T, j, p.k, x[j]);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s += x[j][e];
+    s = warp_sum(s);
+    float mean = s * inv_own, m2 = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const bool all = whole<kVec>(t, T, j, p.k);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float d = all || col<kVec>(t, T, j, e) < p.k ? x[j][e] - mean : 0.0f;
+        m2 = fmaf(d, d, m2);
+      }
+    }
+    m2 = warp_sum(m2);
+    if constexpr (WARPS > 1) {
+      if (lane == 0) red[parity][warp] = make_float2(s, m2);
+      __syncthreads();
+      const float2 w = lane < WARPS ? red[parity][lane] : make_float2(0.0f, 0.0f);
+      parity ^= 1;
+      mean = warp_sum(w.x) * inv_k;
+      const float d = fmaf(w.x, inv_lane, -mean);
+      m2 = warp_sum(n_lane > 0.0f ? fmaf(n_lane * d, d, w.y) : 0.0f);
+    }
+    const float rstd = __frsqrt_rn(fmaf(m2, inv_k, p.eps));
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float g[8], b[8], y[8];
+      load_param_chunk<kVec>(p.gamma, p.param_f32, t, T, j, p.k, 1.0f, g);
+      load_param_chunk<kVec>(p.beta, p.param_f32, t, T, j, p.k, 0.0f, b);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = fmaf((x[j][e] - mean) * rstd, g[e], b[e]);
+      if (p.y_f32)
+        mag = max(mag, store_chunk<float, kVec>(static_cast<float*>(p.y) + r * p.ldy, t, T, j, p.k, y));
+      else
+        mag = max(mag, store_chunk<__nv_bfloat16, kVec>(static_cast<__nv_bfloat16*>(p.y) + r * p.ldy, t, T, j, p.k, y));
+    }
+    if (t == 0) {
+      if (p.mean) p.mean[r] = mean;
+      if (p.rstd) p.rstd[r] = rstd;
+    }
+  }
+  if (p.amax) {
+    mag = __reduce_max_sync(0xFFFFFFFFu, mag);
+    if (lane == 0) mags[warp] = mag;
+    __syncthreads();
+    if (warp == 0) {
+      mag = __reduce_max_sync(0xFFFFFFFFu, lane < static_cast<int>(blockDim.x >> 5) ? mags[lane] : 0u);
+      if (lane == 0) atomicMax(reinterpret_cast<unsigned int*>(p.amax), mag);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Backward in one pass
+// ---------------------------------------------------------------------------
+// cp.async copies into this thread's own slots of shared memory: nobody else
+// reads them, so waiting for the own copies is all the ordering needed.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+constexpr int LB_THREADS = 512;        // most threads of a block; 128 registers each
+constexpr int LB_NV = 2;               // chunks of 8 elements per thread
+constexpr int LB_MAX_K = LB_THREADS * 8 * LB_NV;
+
+// Ring stages: what 192 KB hold of the rows in flight, four at most.
+template <typename TX, typename TDY>
+constexpr int lb_stages() {
+  const int bytes = LB_MAX_K * (2 * static_cast<int>(sizeof(TX)) + static_cast<int>(sizeof(TDY)));
+  return 196608 / bytes < 4 ? 196608 / bytes : 4;
+}
+
+// One operand's slots of one ring stage: slot (j, part) of thread t at
+// [(j * parts + part) * T + t], 16 bytes each with kVec (conflict-free), an
+// element each otherwise.
+template <typename T, bool kVec>
+__device__ __forceinline__ void stage_in(uint8_t* slots, const T* row, int t, int nt, int k) {
+#pragma unroll
+  for (int j = 0; j < LB_NV; ++j) {
+    if constexpr (kVec) {
+      constexpr int PARTS = sizeof(T) / 2;
+      if (whole<kVec>(t, nt, j, k)) {
+#pragma unroll
+        for (int h = 0; h < PARTS; ++h)
+          cp_async16(slots + ((j * PARTS + h) * nt + t) * 16, row + col<kVec>(t, nt, j, 0) + h * (16 / sizeof(T)));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int c = col<kVec>(t, nt, j, e);
+          reinterpret_cast<T*>(slots + ((j * PARTS + e / (16 / sizeof(T))) * nt + t) * 16)[e % (16 / sizeof(T))] =
+              c < k ? row[c] : from_f32<T>(0.0f);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int c = col<kVec>(t, nt, j, e);
+        T* slot = reinterpret_cast<T*>(slots) + (j * 8 + e) * nt + t;
+        if (c >= k)
+          *slot = from_f32<T>(0.0f);
+        else if constexpr (sizeof(T) == 4)
+          cp_async4(slot, row + c);
+        else
+          *slot = row[c];
+      }
+    }
+  }
+}
+
+template <typename T, bool kVec>
+__device__ __forceinline__ void stage_out(const uint8_t* slots, int t, int nt, int j, float (&x)[8]) {
+  if constexpr (!kVec) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = to_f32(reinterpret_cast<const T*>(slots)[(j * 8 + e) * nt + t]);
+  } else if constexpr (sizeof(T) == 2) {
+    unpack8(*reinterpret_cast<const uint4*>(slots + (j * nt + t) * 16), x);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float4 v = *reinterpret_cast<const float4*>(slots + ((j * 2 + h) * nt + t) * 16);
+      x[4 * h] = v.x, x[4 * h + 1] = v.y, x[4 * h + 2] = v.z, x[4 * h + 3] = v.w;
+    }
+  }
+}
+
+// Backward of rows of up to LB_MAX_K elements.  A block has G groups of nt
+// threads; a group takes one row at a time, a thread the same columns of every
+// row, so dgamma and dbeta are sums in its registers until the end.  The rows
+// ahead are on their way into a ring in shared memory (the accumulators leave
+// no room for a second row in registers).  At the end the groups' sums meet in
+// shared memory and the block writes one partial [2][k]; the sum over blocks
+// (sum_partials_kernel) runs in block order, so results do not depend on
+// timing.
+template <typename TX, typename TDY, bool kVec>
+__global__ void __launch_bounds__(LB_THREADS, 1) ln_backward_rows_kernel(const LnBwdParams p, int nt, uint32_t* mag_out) {
+  constexpr int S = lb_stages<TX, TDY>();
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float2 red[2][LB_THREADS / 32];
+  __shared__ uint32_t mags[LB_THREADS / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int groups = blockDim.x / nt, g = threadIdx.x / nt, t = threadIdx.x - g * nt;
+  const int gw = nt >> 5, w0 = g * gw;                   // warps of a group, its first
+  const int slots = nt * 8 * LB_NV;                      // elements of a group's row slots
+  const int dy_bytes = slots * static_cast<int>(sizeof(TDY)), x_bytes = slots * static_cast<int>(sizeof(TX));
+  const int stage_bytes = dy_bytes + x_bytes * (p.res ? 2 : 1);
+  uint8_t* own = ring + static_cast<size_t>(g) * S * stage_bytes;
+  const float inv_k = 1.0f / static_cast<float>(p.k);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * groups + g;
+
+  auto issue = [&](int64_t r, int stage) {
+    if (r < p.rows) {
+      uint8_t* b = own + stage * stage_bytes;
+      stage_in<TDY, kVec>(b, static_cast<const TDY*>(p.dy) + r * p.lddy, t, nt, p.k);
+      stage_in<TX, kVec>(b + dy_bytes, static_cast<const TX*>(p.x) + r * p.ldx, t, nt, p.k);
+      if (p.res) stage_in<TX, kVec>(b + dy_bytes + x_bytes, static_cast<const TX*>(p.res) + r * p.ldr, t, nt, p.k);
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) issue(r0 + i * step, i);
+
+  float gam[LB_NV][8], dg[LB_NV][8], db[LB_NV][8];
+#pragma unroll
+  for (int j = 0; j < LB_NV; ++j) {
+    load_param_chunk<kVec>(p.gamma, p.param_f32, t, nt, j, p.k, 1.0f, gam[j]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dg[j][e] = db[j][e] = 0.0f;
+  }
+  uint32_t mag = 0;
+  int parity = 0, stage = 0;
+  float mean_next = r0 < p.rows ? p.mean[r0] : 0.0f, rstd_next = r0 < p.rows ? p.rstd[r0] : 0.0f;
+  for (int64_t r = r0; r < p.rows; r += step) {
+    // the slot read in the last turn takes the row S - 1 turns ahead
+    issue(r + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);
+    const float mean = mean_next, rstd = rstd_next;
+    if (r + step < p.rows) {
+      mean_next = p.mean[r + step];
+      rstd_next = p.rstd[r + step];
+    }
+    cp_async_wait<S - 1>();
+    const uint8_t* b = own + stage * stage_bytes;
+    float dy[LB_NV][8], xh[LB_NV][8];
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int j = 0; j < LB_NV; ++j) {
+      stage_out<TDY, kVec>(b, t, nt, j, dy[j]);
+      stage_out<TX, kVec>(b + dy_bytes, t, nt, j, xh[j]);
+      const bool all = whole<kVec>(t, nt, j, p.k);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        xh[j][e] = all || col<kVec>(t, nt, j, e) < p.k ? (xh[j][e] - mean) * rstd : 0.0f;
+        const float a = dy[j][e] * gam[j][e];         // 0 past the row's end, as dy is
+        s1 += a;
+        s2 = fmaf(a, xh[j][e], s2);
+        dg[j][e] = fmaf(dy[j][e], xh[j][e], dg[j][e]);
+        db[j][e] += dy[j][e];
+      }
+    }
+    s1 = warp_sum(s1);
+    s2 = warp_sum(s2);
+    if (gw > 1) {
+      if (lane == 0) red[parity][warp] = make_float2(s1, s2);
+      asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(nt) : "memory");
+      const float2 w = lane < gw ? red[parity][w0 + lane] : make_float2(0.0f, 0.0f);
+      parity ^= 1;
+      s1 = warp_sum(w.x);
+      s2 = warp_sum(w.y);
+    }
+    const float c1 = s1 * inv_k, c2 = s2 * inv_k;
+#pragma unroll
+    for (int j = 0; j < LB_NV; ++j) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = rstd * (dy[j][e] * gam[j][e] - fmaf(xh[j][e], c2, c1));
+      if (p.res) {
+        float res[8];
+        stage_out<TX, kVec>(b + dy_bytes + x_bytes, t, nt, j, res);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += res[e];
+      }
+      mag = max(mag, store_chunk<TX, kVec>(static_cast<TX*>(p.dx) + r * p.lddx, t, nt, j, p.k, v));
+    }
+    if (++stage == S) stage = 0;
+  }
+  cp_async_wait<0>();
+  mag = __reduce_max_sync(0xFFFFFFFFu, mag);
+  if (lane == 0) mags[warp] = mag;
+  __syncthreads();                                        // every group is done with the ring
+  if (p.partial) {
+    float* acc = reinterpret_cast<float*>(ring);          // [groups][2][k]
+#pragma unroll
+    for (int j = 0; j < LB_NV; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int c = col<kVec>(t, nt, j, e);
+        if (c < p.k) {
+          acc[(2 * g) * p.k + c] = dg[j][e];
+          acc[(2 * g + 1) * p.k + c] = db[j][e];
+        }
+      }
+    __syncthreads();
+    float* out = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * p.k;
+    for (int i = threadIdx.x; i < 2 * p.k; i += blockDim.x) {
+      float s = 0.0f;
+      for (int h = 0; h < groups; ++h) s += acc[2 * h * p.k + i];
+      out[i] = s;
+    }
+  }
+  if (warp == 0) {
+    mag = __reduce_max_sync(0xFFFFFFFFu, lane < static_cast<int>(blockDim.x >> 5) ? mags[lane] : 0u);
+    if (lane == 0) {
+      if (mag_out)
+        mag_out[blockIdx.x] = mag;
+      else if (p.amax)
+        atomicMax(reinterpret_cast<unsigned int*>(p.amax), mag);
+    }
+  }
+}
+
+// First n0 columns of the blocks' partials [blocks][stride] to out0, the next
+// n1 to out1 (either may be null), and the largest of their magnitudes to
+// amax.  A block of 8 warps takes 32 columns; warp w sums the partials w, w +
+// 8, ..., and the warps' sums are added in order.
+__global__ void __launch_bounds__(256) sum_partials_kernel(const float* partial, int blocks, int64_t stride, int n0, int n1,
+                                                           float* out0, float* out1, const uint32_t* mags, float* amax) {
+  __shared__ float part[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");      // launched as a programmatic dependent of the rows' kernel
+  const int i = blockIdx.x * 32 + lane;
   float s = 0.0f;
-  for (int c = 0; c < chunks; ++c) s += partial[c * stride + i];
-  out[i] = s;
+  if (i < n0 + n1) {
+#pragma unroll 8
+    for (int b = warp; b < blocks; b += 8) s += __ldcg(partial + b * stride + i);
+  }
+  part[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && i < n0 + n1) {
+#pragma unroll
+    for (int w = 1; w < 8; ++w) s += part[w][lane];
+    if (i < n0) {
+      if (out0) out0[i] = s;
+    } else if (out1) {
+      out1[i - n0] = s;
+    }
+  }
+  if (blockIdx.x == 0 && warp == 1 && amax) {
+    uint32_t m = 0;
+    for (int b = lane; b < blocks; b += 32) m = max(m, __ldcg(mags + b));
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if (lane == 0) *amax = __uint_as_float(m);
+  }
 }
 
 constexpr int LN_CHUNKS = 64;
+constexpr int LB_MAX_BLOCKS = 160;     // of the one-pass backward kernel; a workspace is sized for it
+
+template <typename TX, bool kVec, int WARPS, int NV>
+cudaError_t run_forward(const LnParams& p, cudaStream_t s) {
+  constexpr int ROWS = WARPS == 1 ? 8 : 1;
+  constexpr int THREADS = WARPS == 1 ? 256 : 32 * WARPS;
+  const int64_t need = (p.rows + ROWS - 1) / ROWS;
+  const int64_t most = static_cast<int64_t>(device_sm_count()) * (2048 / THREADS);
+  ln_forward_rows_kernel<TX, kVec, WARPS, NV><<<static_cast<int>(need < most ? need : most), THREADS, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename TX, bool kVec>
+cudaError_t dispatch_forward(const LnParams& p, cudaStream_t s) {
+  if (p.k <= 256) return run_forward<TX, kVec, 1, 1>(p, s);
+  if (p.k <= 1024) return run_forward<TX, kVec, 1, 4>(p, s);
+  if (p.k <= 4096) return run_forward<TX, kVec, 4, 4>(p, s);
+  if (p.k <= 8192) return run_forward<TX, kVec, 8, 4>(p, s);
+  if (p.k <= 16384) return run_forward<TX, kVec, 16, 4>(p, s);
+  if (p.k <= 32768) return run_forward<TX, kVec, 32, 4>(p, s);
+  const int grid = static_cast<int>(p.rows < 8 * device_sm_count() ? p.rows : 8 * device_sm_count());
+  ln_forward_long_kernel<TX><<<grid, LN_THREADS, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+// Every row of the operand starts on a 16-byte boundary.
+bool rows_aligned16(const void* p, int64_t ld, bool f32) { return aligned16(p) && (ld * (f32 ? 4 : 2)) % 16 == 0; }
+
+template <typename TX, typename TDY, bool kVec>
+cudaError_t run_backward_rows(LnBwdParams p, float* dgamma, float* dbeta, uint32_t* mags, cudaStream_t s) {
+  const int per_warp = 32 * 8 * LB_NV;
+  const int nt = (p.k + per_warp - 1) / per_warp * 32;
+  // as many groups as the block holds (named barriers 1..15 for groups of several warps)
+  int groups = LB_THREADS / nt;
+  if (groups > p.rows) groups = static_cast<int>(p.rows);
+  const int sms = device_sm_count() < LB_MAX_BLOCKS ? device_sm_count() : LB_MAX_BLOCKS;
+  const int64_t need = (p.rows + groups - 1) / groups;
+  const int blocks = static_cast<int>(need < sms ? need : sms);
+  const int elem = static_cast<int>(sizeof(TDY) + sizeof(TX) * (p.res ? 2 : 1));
+  size_t smem = static_cast<size_t>(lb_stages<TX, TDY>()) * groups * nt * 8 * LB_NV * elem;
+  const size_t sums = static_cast<size_t>(groups) * 2 * p.k * sizeof(float);
+  if (sums > smem) smem = sums;
+  auto kern = ln_backward_rows_kernel<TX, TDY, kVec>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  kern<<<blocks, groups * nt, smem, s>>>(p, nt, mags);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !p.partial) return e;
+  return launch_sum_partials(p.partial, blocks, 2 * p.k, p.k, p.k, dgamma, dbeta, mags, p.amax, s);
+}
+
+template <typename TX, typename TDY>
+cudaError_t run_backward_long(const LnBwdParams& p, float* dgamma, float* dbeta, cudaStream_t s) {
+  const int grid = static_cast<int>(p.rows < 8 * device_sm_count() ? p.rows : 8 * device_sm_count());
+  ln_backward_dx_long_kernel<TX><<<grid, LN_THREADS, 0, s>>>(p);
+  if (p.partial) {
+    const int per = static_cast<int>((p.rows + LN_CHUNKS - 1) / LN_CHUNKS);
+    const int chunks = static_cast<int>((p.rows + per - 1) / per);
+    const int cols = (p.k + LN_THREADS - 1) / LN_THREADS;
+    ln_backward_params_long_kernel<TX><<<dim3(cols, chunks), LN_THREADS, 0, s>>>(p, per);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_sum_partials(p.partial, chunks, 2 * static_cast<int64_t>(p.k), p.k, p.k, dgamma, dbeta, nullptr, nullptr, s);
+  }
+  return cudaGetLastError();
+}
+
+template <typename TX, typename TDY>
+cudaError_t dispatch_backward(const LnBwdParams& p, bool vec, float* dgamma, float* dbeta, uint32_t* mags, cudaStream_t s) {
+  if (p.k > LB_MAX_K) return run_backward_long<TX, TDY>(p, dgamma, dbeta, s);
+  return vec ? run_backward_rows<TX, TDY, true>(p, dgamma, dbeta, mags, s)
+             : run_backward_rows<TX, TDY, false>(p, dgamma, dbeta, mags, s);
+}
 
 }  // namespace
 
+cudaError_t launch_sum_partials(const float* partial, int blocks, int64_t stride, int n0, int n1, float* out0, float* out1,
+                                const uint32_t* mags, float* amax, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(n0) + n1 + 31) / 32));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, sum_partials_kernel, partial, blocks, stride, n0, n1, out0, out1, mags, amax);
+}
+
+// [blocks][2][k] partials, then one magnitude per block.
 size_t layernorm_backward_workspace_bytes(int64_t rows, int64_t k) {
-  return rows > 0 ? static_cast<size_t>(LN_CHUNKS) * 2 * k * sizeof(float) : 256;
+  const int64_t blocks = k > LB_MAX_K ? LN_CHUNKS : LB_MAX_BLOCKS;
+  return static_cast<size_t>(round_up(blocks * 2 * k * 4, 256) + round_up(4 * LB_MAX_BLOCKS, 256));
 }
 
 nvfp4_status launch_layernorm(const LayerNorm& a, cudaStream_t s) {
@@ -196,50 +747,43 @@ nvfp4_status launch_layernorm(const LayerNorm& a, cudaStream_t s) {
     if (e != cudaSuccess) return launch_status(e);
   }
   if (a.rows == 0) return NVFP4_OK;
+  const bool xf = a.x_dtype == NVFP4_DTYPE_F32, yf = a.y_dtype == NVFP4_DTYPE_F32;
   const LnParams p{a.x, a.ldx, a.gamma, a.beta, a.param_dtype == NVFP4_DTYPE_F32, a.eps, a.y, a.ldy,
-                   a.y_dtype == NVFP4_DTYPE_F32, a.mean, a.rstd, a.amax, a.rows, static_cast<int>(a.k)};
-  const int grid = static_cast<int>(a.rows < 8 * device_sm_count() ? a.rows : 8 * device_sm_count());
-  if (a.x_dtype == NVFP4_DTYPE_F32)
-    ln_forward_long_kernel<float><<<grid, LN_THREADS, 0, s>>>(p);
-  else
-    ln_forward_long_kernel<__nv_bfloat16><<<grid, LN_THREADS, 0, s>>>(p);
-  return launch_status(cudaGetLastError());
+                   yf, a.mean, a.rstd, a.amax, a.rows, static_cast<int>(a.k)};
+  const bool vec = rows_aligned16(a.x, a.ldx, xf) && rows_aligned16(a.y, a.ldy, yf) && aligned16(a.gamma) && aligned16(a.beta);
+  if (xf) return launch_status(vec ? dispatch_forward<float, true>(p, s) : dispatch_forward<float, false>(p, s));
+  return launch_status(vec ? dispatch_forward<__nv_bfloat16, true>(p, s) : dispatch_forward<__nv_bfloat16, false>(p, s));
 }
 
 nvfp4_status launch_layernorm_backward(const LayerNormBackward& a, cudaStream_t s) {
+  const bool sums = a.dgamma || a.dbeta;
   cudaError_t e = cudaSuccess;
-  if (a.amax) e = cudaMemsetAsync(a.amax, 0, sizeof(float), s);
+  // with column sums the last kernel also joins the blocks' maxima: no clearing needed
+  if (a.amax && (a.rows == 0 || !sums || a.k > LB_MAX_K)) e = cudaMemsetAsync(a.amax, 0, sizeof(float), s);
   if (a.rows == 0) {
     if (e == cudaSuccess && a.dgamma) e = cudaMemsetAsync(a.dgamma, 0, a.k * sizeof(float), s);
     if (e == cudaSuccess && a.dbeta) e = cudaMemsetAsync(a.dbeta, 0, a.k * sizeof(float), s);
     return launch_status(e);
   }
   if (e != cudaSuccess) return launch_status(e);
-  const LnBwdParams p{a.dy, a.lddy, a.dy_dtype == NVFP4_DTYPE_F32, a.x, a.ldx, a.mean, a.rstd, a.gamma,
+  const bool xf = a.x_dtype == NVFP4_DTYPE_F32, df = a.dy_dtype == NVFP4_DTYPE_F32;
+  const LnBwdParams p{a.dy, a.lddy, df, a.x, a.ldx, a.mean, a.rstd, a.gamma,
                       a.param_dtype == NVFP4_DTYPE_F32, a.residual, a.ldr, a.dx, a.lddx,
-                      static_cast<float*>(a.workspace), a.amax, a.rows, static_cast<int>(a.k)};
-  const bool f32 = a.x_dtype == NVFP4_DTYPE_F32;
-  const int grid = static_cast<int>(a.rows < 8 * device_sm_count() ? a.rows : 8 * device_sm_count());
-  if (f32)
-    ln_backward_dx_long_kernel<float><<<grid, LN_THREADS, 0, s>>>(p);
+                      sums ? static_cast<float*>(a.workspace) : nullptr, a.amax, a.rows, static_cast<int>(a.k)};
+  const bool vec = rows_aligned16(a.dy, a.lddy, df) && rows_aligned16(a.x, a.ldx, xf) && rows_aligned16(a.dx, a.lddx, xf) &&
+                   aligned16(a.gamma) && (!a.residual || rows_aligned16(a.residual, a.ldr, xf));
+  uint32_t* mags = sums ? reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.workspace) +
+                                                      layernorm_backward_workspace_bytes(a.rows, a.k) -
+                                                      round_up(4 * LB_MAX_BLOCKS, 256))
+                        : nullptr;
+  using bf16 = __nv_bfloat16;
+  if (xf)
+    e = df ? dispatch_backward<float, float>(p, vec, a.dgamma, a.dbeta, mags, s)
+           : dispatch_backward<float, bf16>(p, vec, a.dgamma, a.dbeta, mags, s);
   else
-    ln_backward_dx_long_kernel<__nv_bfloat16><<<grid, LN_THREADS, 0, s>>>(p);
-  if (!a.dgamma && !a.dbeta) return launch_status(cudaGetLastError());
-  const int per = static_cast<int>((a.rows + LN_CHUNKS - 1) / LN_CHUNKS);
-  const int chunks = static_cast<int>((a.rows + per - 1) / per);
-  const int cols = static_cast<int>((a.k + LN_THREADS - 1) / LN_THREADS);
-  if (f32)
-    ln_backward_params_long_kernel<float><<<dim3(cols, chunks), LN_THREADS, 0, s>>>(p, per);
-  else
-    ln_backward_params_long_kernel<__nv_bfloat16><<<dim3(cols, chunks), LN_THREADS, 0, s>>>(p, per);
-  if (a.dgamma) launch_sum_chunks(p.partial, chunks, 2 * a.k, a.k, a.dgamma, s);
-  if (a.dbeta) launch_sum_chunks(p.partial + a.k, chunks, 2 * a.k, a.k, a.dbeta, s);
-  return launch_status(cudaGetLastError());
-}
-
-void launch_sum_chunks(const float* partial, int chunks, int64_t stride, int64_t n, float* out, cudaStream_t s) {
-  sum_chunks_kernel<<<static_cast<unsigned>((n + LN_THREADS - 1) / LN_THREADS), LN_THREADS, 0, s>>>(
-      partial, chunks, stride, static_cast<int>(n), out);
+    e = df ? dispatch_backward<bf16, float>(p, vec, a.dgamma, a.dbeta, mags, s)
+           : dispatch_backward<bf16, bf16>(p, vec, a.dgamma, a.dbeta, mags, s);
+  return launch_status(e);
 }
 
 }  // namespace nvfp4
