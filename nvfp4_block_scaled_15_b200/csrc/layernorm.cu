@@ -41,6 +41,15 @@ __device__ __forceinline__ void publish_mag(uint32_t m, float* amax_dev) {
   if ((threadIdx.x & 31) == 0) atomicMax(reinterpret_cast<unsigned int*>(amax_dev), m);
 }
 
+// Maximum of mag over the block, in warp 0.
+__device__ __forceinline__ uint32_t block_max(uint32_t mag, uint32_t* mags) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  mag = __reduce_max_sync(0xFFFFFFFFu, mag);
+  if (lane == 0) mags[warp] = mag;
+  __syncthreads();
+  return warp == 0 ? __reduce_max_sync(0xFFFFFFFFu, lane < static_cast<int>(blockDim.x >> 5) ? mags[lane] : 0u) : 0u;
+}
+
 struct LnParams {
   const void* x;
   int64_t ldx;
@@ -174,21 +183,11 @@ __global__ void __launch_bounds__(LN_THREADS) ln_backward_params_long_kernel(con
 // ---------------------------------------------------------------------------
 // Rows held in registers
 // ---------------------------------------------------------------------------
-// A row is cut into chunks of 8 elements; thread t of the T threads that share
-// a row holds chunks t, t + T, ... (kVec: 16-byte accesses; every row of every
-// operand 16-byte aligned), or the single elements t, t + T, ... where some
-// row is not.  col() is the column of a thread's element (chunk j, element e).
-template <bool kVec>
-__device__ __forceinline__ int col(int t, int T, int j, int e) {
-  return kVec ? 8 * (t + T * j) + e : t + T * (8 * j + e);
-}
-
-// Chunk j of a thread: whole (every element inside the row), or element by
-// element where the row ends.
-template <bool kVec>
-__device__ __forceinline__ bool whole(int t, int T, int j, int k) {
-  return kVec ? 8 * (t + T * j) + 8 <= k : t + T * (8 * j + 7) < k;
-}
+// Rows that all start on 16-byte boundaries are cut into chunks of 8 elements;
+// thread t of the nt threads that share a row holds chunks t, t + nt, ...
+// (16-byte accesses; the chunk at the row's end element by element).
+__device__ __forceinline__ int chunk_col(int t, int nt, int j) { return 8 * (t + nt * j); }
+__device__ __forceinline__ bool whole(int t, int nt, int j, int k) { return chunk_col(t, nt, j) + 8 <= k; }
 
 __device__ __forceinline__ void unpack8(const uint4 w, float (&x)[8]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -199,47 +198,14 @@ __device__ __forceinline__ void unpack8(const uint4 w, float (&x)[8]) {
   }
 }
 
-// Streaming 16-byte load (read once, not kept in L1).
-__device__ __forceinline__ uint4 ld_stream(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-
-// Chunk j of a row of x; elements past the row are 0.
-template <typename T, bool kVec>
-__device__ __forceinline__ void load_chunk(const T* row, int t, int nt, int j, int k, float (&x)[8]) {
-  if (whole<kVec>(t, nt, j, k)) {
-    if constexpr (!kVec) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = to_f32(row[col<kVec>(t, nt, j, e)]);
-    } else if constexpr (sizeof(T) == 2) {
-      unpack8(ld_stream(row + col<kVec>(t, nt, j, 0)), x);
-    } else {
-      const uint4 a = ld_stream(row + col<kVec>(t, nt, j, 0)), b = ld_stream(row + col<kVec>(t, nt, j, 4));
-      x[0] = __uint_as_float(a.x), x[1] = __uint_as_float(a.y), x[2] = __uint_as_float(a.z), x[3] = __uint_as_float(a.w);
-      x[4] = __uint_as_float(b.x), x[5] = __uint_as_float(b.y), x[6] = __uint_as_float(b.z), x[7] = __uint_as_float(b.w);
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = col<kVec>(t, nt, j, e);
-      x[e] = c < k ? to_f32(row[c]) : 0.0f;
-    }
-  }
-}
-
-// The same columns of gamma or beta (cached: every row reads them).
-template <bool kVec>
+// Chunk j's columns of gamma or beta (cached: every row reads them).
 __device__ __forceinline__ void load_param_chunk(const void* p, int f32, int t, int nt, int j, int k, float dflt,
                                                  float (&x)[8]) {
   if (!p) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = dflt;
-  } else if (kVec && whole<kVec>(t, nt, j, k)) {
-    const int c = col<kVec>(t, nt, j, 0);
+  } else if (whole(t, nt, j, k)) {
+    const int c = chunk_col(t, nt, j);
     if (f32) {
       const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c));
       const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c + 4));
@@ -250,18 +216,18 @@ __device__ __forceinline__ void load_param_chunk(const void* p, int f32, int t, 
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int c = col<kVec>(t, nt, j, e);
+      const int c = chunk_col(t, nt, j) + e;
       x[e] = c < k ? load_param(p, f32, c) : dflt;
     }
   }
 }
 
 // Stores a chunk rounded to T; returns the largest stored magnitude.
-template <typename T, bool kVec>
+template <typename T>
 __device__ __forceinline__ uint32_t store_chunk(T* row, int t, int nt, int j, int k, const float (&x)[8]) {
   uint32_t mag = 0;
-  if (kVec && whole<kVec>(t, nt, j, k)) {
-    T* out = row + col<kVec>(t, nt, j, 0);
+  if (whole(t, nt, j, k)) {
+    T* out = row + chunk_col(t, nt, j);
     if constexpr (sizeof(T) == 2) {
       uint32_t u[4];
 #pragma unroll
@@ -281,7 +247,7 @@ __device__ __forceinline__ uint32_t store_chunk(T* row, int t, int nt, int j, in
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int c = col<kVec>(t, nt, j, e);
+      const int c = chunk_col(t, nt, j) + e;
       if (c < k) {
         const T o = from_f32<T>(x[e]);
         row[c] = o;
@@ -298,101 +264,6 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Forward, WARPS warps per row (one warp: 8 rows per block), NV chunks per
-// thread: one pass over x.  Each warp takes the mean and the squared
-// deviations about it of its own elements; the row's statistics follow from
-// the warps' (sum, deviations) by
-//   mean = sum_w s_w / k,  sum (x - mean)^2 = sum_w (M_w + n_w (s_w / n_w - mean)^2)
-// (no cancellation, as with sum x^2 - k mean^2), so a row needs one barrier.
-template <typename TX, bool kVec, int WARPS, int NV>
-__global__ void __launch_bounds__(WARPS == 1 ? 256 : 32 * WARPS) ln_forward_rows_kernel(const LnParams p) {
-  constexpr int T = 32 * WARPS;
-  constexpr int ROWS = WARPS == 1 ? 8 : 1;
-  __shared__ float2 red[2][WARPS];
-  __shared__ uint32_t mags[32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = WARPS == 1 ? lane : threadIdx.x;
-  const float inv_k = 1.0f / static_cast<float>(p.k);
-  // elements of this warp, of warp w
-  auto count = [&](int w) {
-    int n = 0;
-    if constexpr (kVec) {
-      for (int j = 0; j < NV; ++j) n += min(max(p.k - 8 * (32 * w + T * j), 0), 256);
-    } else {
-      for (int j = 0; j < 8 * NV; ++j) n += min(max(p.k - (32 * w + T * j), 0), 32);
-    }
-    return static_cast<float>(n);
-  };
-  const float n_own = count(WARPS == 1 ? 0 : warp);
-  const float inv_own = n_own > 0.0f ? 1.0f / n_own : 0.0f;
-  const float n_lane = WARPS > 1 && lane < WARPS ? count(lane) : 0.0f;
-  const float inv_lane = n_lane > 0.0f ? 1.0f / n_lane : 0.0f;
-  uint32_t mag = 0;
-  int parity = 0;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * ROWS;
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * ROWS + (WARPS == 1 ? warp : 0); r < p.rows; r += step) {
-    const TX* row = static_cast<const TX*>(p.x) + r * p.ldx;
-    float x[NV][8];
-    float s = 0.0f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) load_chunk<TX, kVec>(row, t, T, j, p.k, x[j]);
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s += x[j][e];
-    s = warp_sum(s);
-    float mean = s * inv_own, m2 = 0.0f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const bool all = whole<kVec>(t, T, j, p.k);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float d = all || col<kVec>(t, T, j, e) < p.k ? x[j][e] - mean : 0.0f;
-        m2 = fmaf(d, d, m2);
-      }
-    }
-    m2 = warp_sum(m2);
-    if constexpr (WARPS > 1) {
-      if (lane == 0) red[parity][warp] = make_float2(s, m2);
-      __syncthreads();
-      const float2 w = lane < WARPS ? red[parity][lane] : make_float2(0.0f, 0.0f);
-      parity ^= 1;
-      mean = warp_sum(w.x) * inv_k;
-      const float d = fmaf(w.x, inv_lane, -mean);
-      m2 = warp_sum(n_lane > 0.0f ? fmaf(n_lane * d, d, w.y) : 0.0f);
-    }
-    const float rstd = __frsqrt_rn(fmaf(m2, inv_k, p.eps));
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      float g[8], b[8], y[8];
-      load_param_chunk<kVec>(p.gamma, p.param_f32, t, T, j, p.k, 1.0f, g);
-      load_param_chunk<kVec>(p.beta, p.param_f32, t, T, j, p.k, 0.0f, b);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = fmaf((x[j][e] - mean) * rstd, g[e], b[e]);
-      if (p.y_f32)
-        mag = max(mag, store_chunk<float, kVec>(static_cast<float*>(p.y) + r * p.ldy, t, T, j, p.k, y));
-      else
-        mag = max(mag, store_chunk<__nv_bfloat16, kVec>(static_cast<__nv_bfloat16*>(p.y) + r * p.ldy, t, T, j, p.k, y));
-    }
-    if (t == 0) {
-      if (p.mean) p.mean[r] = mean;
-      if (p.rstd) p.rstd[r] = rstd;
-    }
-  }
-  if (p.amax) {
-    mag = __reduce_max_sync(0xFFFFFFFFu, mag);
-    if (lane == 0) mags[warp] = mag;
-    __syncthreads();
-    if (warp == 0) {
-      mag = __reduce_max_sync(0xFFFFFFFFu, lane < static_cast<int>(blockDim.x >> 5) ? mags[lane] : 0u);
-      if (lane == 0) atomicMax(reinterpret_cast<unsigned int*>(p.amax), mag);
-    }
-  }
-}
-
-// ---------------------------------------------------------------------------
-// Backward in one pass
-// ---------------------------------------------------------------------------
 // cp.async copies into this thread's own slots of shared memory: nobody else
 // reads them, so waiting for the own copies is all the ordering needed.
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
@@ -411,6 +282,158 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// One operand's slots of one ring stage: 16 bytes each, slot (j, part) of
+// thread t at [(j * parts + part) * nt + t] (conflict-free).
+template <typename T, int NV>
+__device__ __forceinline__ void stage_in(uint8_t* slots, const T* row, int t, int nt, int k) {
+  constexpr int PARTS = sizeof(T) / 2, PER = 16 / sizeof(T);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = chunk_col(t, nt, j);
+    if (c + 8 <= k) {
+#pragma unroll
+      for (int h = 0; h < PARTS; ++h) cp_async16(slots + ((j * PARTS + h) * nt + t) * 16, row + c + h * PER);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        reinterpret_cast<T*>(slots + ((j * PARTS + e / PER) * nt + t) * 16)[e % PER] =
+            c + e < k ? row[c + e] : from_f32<T>(0.0f);
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void stage_out(const uint8_t* slots, int t, int nt, int j, float (&x)[8]) {
+  if constexpr (sizeof(T) == 2) {
+    unpack8(*reinterpret_cast<const uint4*>(slots + (j * nt + t) * 16), x);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float4 v = *reinterpret_cast<const float4*>(slots + ((j * 2 + h) * nt + t) * 16);
+      x[4 * h] = v.x, x[4 * h + 1] = v.y, x[4 * h + 2] = v.z, x[4 * h + 3] = v.w;
+    }
+  }
+}
+
+// Named barrier of the nt threads of group g (its warps only).
+__device__ __forceinline__ void group_sync(int g, int nt) {
+  asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(nt) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// Forward in one pass
+// ---------------------------------------------------------------------------
+// A block has G groups of nt threads; a group takes one row at a time, NV
+// chunks per thread, and S rows ahead are on their way into a ring in shared
+// memory.  Each warp takes the mean and the squared deviations about it of its
+// own elements; the row's statistics follow from the warps' (sum, deviations) by
+//   mean = sum_w s_w / k,  sum (x - mean)^2 = sum_w (M_w + n_w (s_w / n_w - mean)^2)
+// (no cancellation, as with sum x^2 - k mean^2), so a row needs one barrier.
+constexpr int LF_THREADS = 512;
+constexpr int LF_MAX_NV = 8;
+constexpr int LF_MAX_K = LF_THREADS * 8 * LF_MAX_NV;
+
+// Blocks per SM, and ring stages: what their share of 192 KB holds of the
+// longest rows of the variant.
+template <int NV>
+constexpr int lf_blocks() { return NV <= 2 ? 2 : 1; }
+template <typename TX, int NV>
+constexpr int lf_stages() { return 196608 / lf_blocks<NV>() / (LF_THREADS * 8 * NV * static_cast<int>(sizeof(TX))); }
+
+template <typename TX, int NV>
+__global__ void __launch_bounds__(LF_THREADS, lf_blocks<NV>()) ln_forward_rows_kernel(const LnParams p, int nt) {
+  constexpr int S = lf_stages<TX, NV>();
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float2 red[2][LF_THREADS / 32];
+  __shared__ uint32_t mags[LF_THREADS / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int groups = blockDim.x / nt, g = threadIdx.x / nt, t = threadIdx.x - g * nt;
+  const int gw = nt >> 5, w0 = g * gw;                   // warps of a group, its first
+  const int row_bytes = nt * 8 * NV * static_cast<int>(sizeof(TX));
+  uint8_t* own = ring + static_cast<size_t>(g) * S * row_bytes;
+  const float inv_k = 1.0f / static_cast<float>(p.k);
+  // elements that warp w of a group holds
+  auto count = [&](int w) {
+    int n = 0;
+    for (int j = 0; j < NV; ++j) n += min(max(p.k - 8 * (32 * w + nt * j), 0), 256);
+    return static_cast<float>(n);
+  };
+  const float n_own = count(warp - w0);
+  const float inv_own = n_own > 0.0f ? 1.0f / n_own : 0.0f;
+  const float n_lane = lane < gw ? count(lane) : 0.0f;
+  const float inv_lane = n_lane > 0.0f ? 1.0f / n_lane : 0.0f;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * groups + g;
+  auto issue = [&](int64_t r, int stage) {
+    if (r < p.rows)
+      stage_in<TX, NV>(own + stage * row_bytes, static_cast<const TX*>(p.x) + r * p.ldx, t, nt, p.k);
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < S; ++i) issue(r0 + i * step, i);
+  uint32_t mag = 0;
+  int parity = 0, stage = 0;
+  for (int64_t r = r0; r < p.rows; r += step) {
+    cp_async_wait<S - 1>();
+    float x[NV][8];
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) stage_out<TX>(own + stage * row_bytes, t, nt, j, x[j]);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s += x[j][e];          // 0 past the row's end
+    issue(r + S * step, stage);                          // the slot is read
+    if (++stage == S) stage = 0;
+    s = warp_sum(s);
+    float mean = s * inv_own, m2 = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const bool all = whole(t, nt, j, p.k);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float d = all || chunk_col(t, nt, j) + e < p.k ? x[j][e] - mean : 0.0f;
+        m2 = fmaf(d, d, m2);
+      }
+    }
+    m2 = warp_sum(m2);
+    if (gw > 1) {
+      if (lane == 0) red[parity][warp] = make_float2(s, m2);
+      group_sync(g, nt);
+      const float2 w = lane < gw ? red[parity][w0 + lane] : make_float2(0.0f, 0.0f);
+      parity ^= 1;
+      mean = warp_sum(w.x) * inv_k;
+      const float d = fmaf(w.x, inv_lane, -mean);
+      m2 = warp_sum(n_lane > 0.0f ? fmaf(n_lane * d, d, w.y) : 0.0f);
+    }
+    const float rstd = __frsqrt_rn(fmaf(m2, inv_k, p.eps));
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float gm[8], bt[8], y[8];
+      load_param_chunk(p.gamma, p.param_f32, t, nt, j, p.k, 1.0f, gm);
+      load_param_chunk(p.beta, p.param_f32, t, nt, j, p.k, 0.0f, bt);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = fmaf((x[j][e] - mean) * rstd, gm[e], bt[e]);
+      if (p.y_f32)
+        mag = max(mag, store_chunk<float>(static_cast<float*>(p.y) + r * p.ldy, t, nt, j, p.k, y));
+      else
+        mag = max(mag, store_chunk<__nv_bfloat16>(static_cast<__nv_bfloat16*>(p.y) + r * p.ldy, t, nt, j, p.k, y));
+    }
+    if (t == 0) {
+      if (p.mean) p.mean[r] = mean;
+      if (p.rstd) p.rstd[r] = rstd;
+    }
+  }
+  cp_async_wait<0>();
+  if (p.amax) {
+    mag = block_max(mag, mags);
+    if (threadIdx.x == 0) atomicMax(reinterpret_cast<unsigned int*>(p.amax), mag);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Backward in one pass
+// ---------------------------------------------------------------------------
 constexpr int LB_THREADS = 512;        // most threads of a block; 128 registers each
 constexpr int LB_NV = 2;               // chunks of 8 elements per thread
 constexpr int LB_MAX_K = LB_THREADS * 8 * LB_NV;
@@ -422,57 +445,26 @@ constexpr int lb_stages() {
   return 196608 / bytes < 4 ? 196608 / bytes : 4;
 }
 
-// One operand's slots of one ring stage: slot (j, part) of thread t at
-// [(j * parts + part) * T + t], 16 bytes each with kVec (conflict-free), an
-// element each otherwise.
-template <typename T, bool kVec>
-__device__ __forceinline__ void stage_in(uint8_t* slots, const T* row, int t, int nt, int k) {
-#pragma unroll
-  for (int j = 0; j < LB_NV; ++j) {
-    if constexpr (kVec) {
-      constexpr int PARTS = sizeof(T) / 2;
-      if (whole<kVec>(t, nt, j, k)) {
-#pragma unroll
-        for (int h = 0; h < PARTS; ++h)
-          cp_async16(slots + ((j * PARTS + h) * nt + t) * 16, row + col<kVec>(t, nt, j, 0) + h * (16 / sizeof(T)));
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int c = col<kVec>(t, nt, j, e);
-          reinterpret_cast<T*>(slots + ((j * PARTS + e / (16 / sizeof(T))) * nt + t) * 16)[e % (16 / sizeof(T))] =
-              c < k ? row[c] : from_f32<T>(0.0f);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int c = col<kVec>(t, nt, j, e);
-        T* slot = reinterpret_cast<T*>(slots) + (j * 8 + e) * nt + t;
-        if (c >= k)
-          *slot = from_f32<T>(0.0f);
-        else if constexpr (sizeof(T) == 4)
-          cp_async4(slot, row + c);
-        else
-          *slot = row[c];
-      }
-    }
+// The groups' column sums acc[groups][2][k], added in order, as this block's
+// partial.
+__device__ __forceinline__ void write_partial(const LnBwdParams& p, const float* acc, int groups) {
+  __syncthreads();
+  float* out = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * p.k;
+  for (int i = threadIdx.x; i < 2 * p.k; i += blockDim.x) {
+    float s = 0.0f;
+    for (int h = 0; h < groups; ++h) s += acc[2 * h * p.k + i];
+    out[i] = s;
   }
 }
 
-template <typename T, bool kVec>
-__device__ __forceinline__ void stage_out(const uint8_t* slots, int t, int nt, int j, float (&x)[8]) {
-  if constexpr (!kVec) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = to_f32(reinterpret_cast<const T*>(slots)[(j * 8 + e) * nt + t]);
-  } else if constexpr (sizeof(T) == 2) {
-    unpack8(*reinterpret_cast<const uint4*>(slots + (j * nt + t) * 16), x);
-  } else {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float4 v = *reinterpret_cast<const float4*>(slots + ((j * 2 + h) * nt + t) * 16);
-      x[4 * h] = v.x, x[4 * h + 1] = v.y, x[4 * h + 2] = v.z, x[4 * h + 3] = v.w;
-    }
-  }
+// The block's largest |dx| (in warp 0): to its slot, for the sum over blocks
+// to join, or straight to the maximum where no such kernel follows.
+__device__ __forceinline__ void publish_block(const LnBwdParams& p, uint32_t mag, uint32_t* mag_out) {
+  if (threadIdx.x != 0) return;
+  if (mag_out)
+    mag_out[blockIdx.x] = mag;
+  else if (p.amax)
+    atomicMax(reinterpret_cast<unsigned int*>(p.amax), mag);
 }
 
 // Backward of rows of up to LB_MAX_K elements.  A block has G groups of nt
@@ -483,7 +475,7 @@ __device__ __forceinline__ void stage_out(const uint8_t* slots, int t, int nt, i
 // shared memory and the block writes one partial [2][k]; the sum over blocks
 // (sum_partials_kernel) runs in block order, so results do not depend on
 // timing.
-template <typename TX, typename TDY, bool kVec>
+template <typename TX, typename TDY>
 __global__ void __launch_bounds__(LB_THREADS, 1) ln_backward_rows_kernel(const LnBwdParams p, int nt, uint32_t* mag_out) {
   constexpr int S = lb_stages<TX, TDY>();
   extern __shared__ __align__(16) uint8_t ring[];
@@ -503,9 +495,9 @@ __global__ void __launch_bounds__(LB_THREADS, 1) ln_backward_rows_kernel(const L
   auto issue = [&](int64_t r, int stage) {
     if (r < p.rows) {
       uint8_t* b = own + stage * stage_bytes;
-      stage_in<TDY, kVec>(b, static_cast<const TDY*>(p.dy) + r * p.lddy, t, nt, p.k);
-      stage_in<TX, kVec>(b + dy_bytes, static_cast<const TX*>(p.x) + r * p.ldx, t, nt, p.k);
-      if (p.res) stage_in<TX, kVec>(b + dy_bytes + x_bytes, static_cast<const TX*>(p.res) + r * p.ldr, t, nt, p.k);
+      stage_in<TDY, LB_NV>(b, static_cast<const TDY*>(p.dy) + r * p.lddy, t, nt, p.k);
+      stage_in<TX, LB_NV>(b + dy_bytes, static_cast<const TX*>(p.x) + r * p.ldx, t, nt, p.k);
+      if (p.res) stage_in<TX, LB_NV>(b + dy_bytes + x_bytes, static_cast<const TX*>(p.res) + r * p.ldr, t, nt, p.k);
     }
     cp_async_commit();
   };
@@ -515,7 +507,7 @@ __global__ void __launch_bounds__(LB_THREADS, 1) ln_backward_rows_kernel(const L
   float gam[LB_NV][8], dg[LB_NV][8], db[LB_NV][8];
 #pragma unroll
   for (int j = 0; j < LB_NV; ++j) {
-    load_param_chunk<kVec>(p.gamma, p.param_f32, t, nt, j, p.k, 1.0f, gam[j]);
+    load_param_chunk(p.gamma, p.param_f32, t, nt, j, p.k, 1.0f, gam[j]);
 #pragma unroll
     for (int e = 0; e < 8; ++e) dg[j][e] = db[j][e] = 0.0f;
   }
@@ -536,12 +528,12 @@ __global__ void __launch_bounds__(LB_THREADS, 1) ln_backward_rows_kernel(const L
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int j = 0; j < LB_NV; ++j) {
-      stage_out<TDY, kVec>(b, t, nt, j, dy[j]);
-      stage_out<TX, kVec>(b + dy_bytes, t, nt, j, xh[j]);
-      const bool all = whole<kVec>(t, nt, j, p.k);
+      stage_out<TDY>(b, t, nt, j, dy[j]);
+      stage_out<TX>(b + dy_bytes, t, nt, j, xh[j]);
+      const bool all = whole(t, nt, j, p.k);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        xh[j][e] = all || col<kVec>(t, nt, j, e) < p.k ? (xh[j][e] - mean) * rstd : 0.0f;
+        xh[j][e] = all || chunk_col(t, nt, j) + e < p.k ? (xh[j][e] - mean) * rstd : 0.0f;
         const float a = dy[j][e] * gam[j][e];         // 0 past the row's end, as dy is
         s1 += a;
         s2 = fmaf(a, xh[j][e], s2);
@@ -553,7 +545,7 @@ __global__ void __launch_bounds__(LB_THREADS, 1) ln_backward_rows_kernel(const L
     s2 = warp_sum(s2);
     if (gw > 1) {
       if (lane == 0) red[parity][warp] = make_float2(s1, s2);
-      asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(nt) : "memory");
+      group_sync(g, nt);
       const float2 w = lane < gw ? red[parity][w0 + lane] : make_float2(0.0f, 0.0f);
       parity ^= 1;
       s1 = warp_sum(w.x);
@@ -567,47 +559,243 @@ __global__ void __launch_bounds__(LB_THREADS, 1) ln_backward_rows_kernel(const L
       for (int e = 0; e < 8; ++e) v[e] = rstd * (dy[j][e] * gam[j][e] - fmaf(xh[j][e], c2, c1));
       if (p.res) {
         float res[8];
-        stage_out<TX, kVec>(b + dy_bytes + x_bytes, t, nt, j, res);
+        stage_out<TX>(b + dy_bytes + x_bytes, t, nt, j, res);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += res[e];
       }
-      mag = max(mag, store_chunk<TX, kVec>(static_cast<TX*>(p.dx) + r * p.lddx, t, nt, j, p.k, v));
+      mag = max(mag, store_chunk<TX>(static_cast<TX*>(p.dx) + r * p.lddx, t, nt, j, p.k, v));
     }
     if (++stage == S) stage = 0;
   }
   cp_async_wait<0>();
-  mag = __reduce_max_sync(0xFFFFFFFFu, mag);
-  if (lane == 0) mags[warp] = mag;
-  __syncthreads();                                        // every group is done with the ring
+  mag = block_max(mag, mags);                            // its barrier: every group is done with the ring
   if (p.partial) {
     float* acc = reinterpret_cast<float*>(ring);          // [groups][2][k]
 #pragma unroll
     for (int j = 0; j < LB_NV; ++j)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int c = col<kVec>(t, nt, j, e);
+        const int c = chunk_col(t, nt, j) + e;
         if (c < p.k) {
           acc[(2 * g) * p.k + c] = dg[j][e];
           acc[(2 * g + 1) * p.k + c] = db[j][e];
         }
       }
-    __syncthreads();
-    float* out = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * p.k;
-    for (int i = threadIdx.x; i < 2 * p.k; i += blockDim.x) {
-      float s = 0.0f;
-      for (int h = 0; h < groups; ++h) s += acc[2 * h * p.k + i];
-      out[i] = s;
+    write_partial(p, acc, groups);
+  }
+  publish_block(p, mag, mag_out);
+}
+
+// ---------------------------------------------------------------------------
+// Rows that start anywhere (an odd pitch, a view into a buffer)
+// ---------------------------------------------------------------------------
+// The same groups and rings, but a ring stage holds the row's bytes as they
+// lie in memory, copied in 4-byte words: a bf16 row may start in the middle of
+// a word, so element c sits at 2-byte slot c + shift, and the words at the
+// row's two ends are copied element by element.  Any thread may have copied a
+// thread's elements: each row has one more barrier than above, after which the
+// copies are visible and the slot read in the turn before is free.  A thread's
+// elements are t, t + nt, ...
+template <typename T>
+__device__ __forceinline__ int row_shift(const T* row) {
+  return sizeof(T) == 2 ? static_cast<int>((reinterpret_cast<uintptr_t>(row) >> 1) & 1) : 0;
+}
+
+template <typename T>
+__device__ __forceinline__ void odd_in(uint8_t* slot, const T* row, int t, int nt, int k) {
+  if constexpr (sizeof(T) == 4) {
+    for (int c = t; c < k; c += nt) cp_async4(slot + 4 * c, row + c);
+  } else {
+    const int shift = row_shift(row);
+    T* dst = reinterpret_cast<T*>(slot);
+    for (int w = t; 2 * w - shift < k; w += nt) {
+      const int c = 2 * w - shift;
+      if (c >= 0 && c + 1 < k)
+        cp_async4(dst + 2 * w, row + c);
+      else
+        dst[2 * w + (c < 0)] = row[c < 0 ? 0 : c];
     }
   }
-  if (warp == 0) {
-    mag = __reduce_max_sync(0xFFFFFFFFu, lane < static_cast<int>(blockDim.x >> 5) ? mags[lane] : 0u);
-    if (lane == 0) {
-      if (mag_out)
-        mag_out[blockIdx.x] = mag;
-      else if (p.amax)
-        atomicMax(reinterpret_cast<unsigned int*>(p.amax), mag);
+}
+
+// Bytes of one row in a stage.
+__host__ __device__ constexpr int odd_row_bytes(int k, int size) { return (k * size + 4 + 15) / 16 * 16; }
+
+constexpr int LO_THREADS = 512;
+constexpr int LO_STAGES = 3;
+constexpr int LO_SMEM = 220 * 1024;
+
+template <typename TX>
+__global__ void __launch_bounds__(LO_THREADS, 2) ln_forward_odd_kernel(const LnParams p, int nt) {
+  constexpr int S = LO_STAGES;
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float2 red[2][LO_THREADS / 32];
+  __shared__ uint32_t mags[LO_THREADS / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int groups = blockDim.x / nt, g = threadIdx.x / nt, t = threadIdx.x - g * nt;
+  const int gw = nt >> 5, w0 = g * gw;
+  const int row_bytes = odd_row_bytes(p.k, sizeof(TX));
+  uint8_t* own = ring + static_cast<size_t>(g) * S * row_bytes;
+  const float inv_k = 1.0f / static_cast<float>(p.k);
+  auto count = [&](int w) {                              // elements that warp w of a group holds
+    const int full = p.k / nt, rest = min(max(p.k - full * nt - 32 * w, 0), 32);
+    return static_cast<float>(32 * full + rest);
+  };
+  const float n_own = count(warp - w0);
+  const float inv_own = n_own > 0.0f ? 1.0f / n_own : 0.0f;
+  const float n_lane = lane < gw ? count(lane) : 0.0f;
+  const float inv_lane = n_lane > 0.0f ? 1.0f / n_lane : 0.0f;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * groups + g;
+  auto issue = [&](int64_t r, int stage) {
+    if (r < p.rows) odd_in(own + stage * row_bytes, static_cast<const TX*>(p.x) + r * p.ldx, t, nt, p.k);
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) issue(r0 + i * step, i);
+  uint32_t mag = 0;
+  int parity = 0, stage = 0;
+  for (int64_t r = r0; r < p.rows; r += step) {
+    cp_async_wait<S - 2>();
+    if (gw > 1) group_sync(g, nt); else __syncwarp();
+    issue(r + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);
+    const TX* row = reinterpret_cast<const TX*>(own + stage * row_bytes) + row_shift(static_cast<const TX*>(p.x) + r * p.ldx);
+    if (++stage == S) stage = 0;
+    float s = 0.0f, m2 = 0.0f;
+#pragma unroll 4
+    for (int c = t; c < p.k; c += nt) s += to_f32(row[c]);
+    s = warp_sum(s);
+    float mean = s * inv_own;
+#pragma unroll 4
+    for (int c = t; c < p.k; c += nt) {
+      const float d = to_f32(row[c]) - mean;
+      m2 = fmaf(d, d, m2);
+    }
+    m2 = warp_sum(m2);
+    if (gw > 1) {
+      if (lane == 0) red[parity][warp] = make_float2(s, m2);
+      group_sync(g, nt);
+      const float2 w = lane < gw ? red[parity][w0 + lane] : make_float2(0.0f, 0.0f);
+      parity ^= 1;
+      mean = warp_sum(w.x) * inv_k;
+      const float d = fmaf(w.x, inv_lane, -mean);
+      m2 = warp_sum(n_lane > 0.0f ? fmaf(n_lane * d, d, w.y) : 0.0f);
+    }
+    const float rstd = __frsqrt_rn(fmaf(m2, inv_k, p.eps));
+    float* yf = static_cast<float*>(p.y) + r * p.ldy;
+    __nv_bfloat16* yh = static_cast<__nv_bfloat16*>(p.y) + r * p.ldy;
+#pragma unroll 4
+    for (int c = t; c < p.k; c += nt) {
+      const float gm = p.gamma ? load_param(p.gamma, p.param_f32, c) : 1.0f;
+      const float bt = p.beta ? load_param(p.beta, p.param_f32, c) : 0.0f;
+      const float v = fmaf((to_f32(row[c]) - mean) * rstd, gm, bt);
+      if (p.y_f32) {
+        yf[c] = v;
+        mag = max(mag, mag_bits(v));
+      } else {
+        yh[c] = __float2bfloat16_rn(v);
+        mag = max(mag, mag_bits(yh[c]));
+      }
+    }
+    if (t == 0) {
+      if (p.mean) p.mean[r] = mean;
+      if (p.rstd) p.rstd[r] = rstd;
     }
   }
+  cp_async_wait<0>();
+  if (p.amax) {
+    mag = block_max(mag, mags);
+    if (threadIdx.x == 0) atomicMax(reinterpret_cast<unsigned int*>(p.amax), mag);
+  }
+}
+
+// Backward: the column sums of a group live in shared memory, each column
+// touched by one thread only.
+template <typename TX, typename TDY>
+__global__ void __launch_bounds__(LO_THREADS, 1) ln_backward_odd_kernel(const LnBwdParams p, int nt, uint32_t* mag_out) {
+  constexpr int S = LO_STAGES;
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float2 red[2][LO_THREADS / 32];
+  __shared__ uint32_t mags[LO_THREADS / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int groups = blockDim.x / nt, g = threadIdx.x / nt, t = threadIdx.x - g * nt;
+  const int gw = nt >> 5, w0 = g * gw;
+  const int dy_bytes = odd_row_bytes(p.k, sizeof(TDY)), x_bytes = odd_row_bytes(p.k, sizeof(TX));
+  const int stage_bytes = dy_bytes + x_bytes * (p.res ? 2 : 1);
+  float* acc = reinterpret_cast<float*>(ring);            // [groups][2][k]
+  float* dg = acc + 2 * g * p.k;
+  float* db = dg + p.k;
+  uint8_t* own = ring + static_cast<size_t>(groups) * 2 * p.k * 4 / 16 * 16 + 16 + static_cast<size_t>(g) * S * stage_bytes;
+  const float inv_k = 1.0f / static_cast<float>(p.k);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * groups + g;
+  auto issue = [&](int64_t r, int stage) {
+    if (r < p.rows) {
+      uint8_t* b = own + stage * stage_bytes;
+      odd_in(b, static_cast<const TDY*>(p.dy) + r * p.lddy, t, nt, p.k);
+      odd_in(b + dy_bytes, static_cast<const TX*>(p.x) + r * p.ldx, t, nt, p.k);
+      if (p.res) odd_in(b + dy_bytes + x_bytes, static_cast<const TX*>(p.res) + r * p.ldr, t, nt, p.k);
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) issue(r0 + i * step, i);
+  for (int c = t; c < p.k; c += nt) dg[c] = db[c] = 0.0f;
+  uint32_t mag = 0;
+  int parity = 0, stage = 0;
+  float mean_next = r0 < p.rows ? p.mean[r0] : 0.0f, rstd_next = r0 < p.rows ? p.rstd[r0] : 0.0f;
+  for (int64_t r = r0; r < p.rows; r += step) {
+    const float mean = mean_next, rstd = rstd_next;
+    if (r + step < p.rows) {
+      mean_next = p.mean[r + step];
+      rstd_next = p.rstd[r + step];
+    }
+    cp_async_wait<S - 2>();
+    if (gw > 1) group_sync(g, nt); else __syncwarp();
+    issue(r + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);
+    const uint8_t* b = own + stage * stage_bytes;
+    if (++stage == S) stage = 0;
+    const TDY* dy = reinterpret_cast<const TDY*>(b) + row_shift(static_cast<const TDY*>(p.dy) + r * p.lddy);
+    const TX* x = reinterpret_cast<const TX*>(b + dy_bytes) + row_shift(static_cast<const TX*>(p.x) + r * p.ldx);
+    const TX* res = reinterpret_cast<const TX*>(b + dy_bytes + x_bytes) +
+                    (p.res ? row_shift(static_cast<const TX*>(p.res) + r * p.ldr) : 0);
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll 4
+    for (int c = t; c < p.k; c += nt) {
+      const float d = to_f32(dy[c]), xh = (to_f32(x[c]) - mean) * rstd;
+      const float a = p.gamma ? d * load_param(p.gamma, p.param_f32, c) : d;
+      s1 += a;
+      s2 = fmaf(a, xh, s2);
+      dg[c] = fmaf(d, xh, dg[c]);
+      db[c] += d;
+    }
+    s1 = warp_sum(s1);
+    s2 = warp_sum(s2);
+    if (gw > 1) {
+      if (lane == 0) red[parity][warp] = make_float2(s1, s2);
+      group_sync(g, nt);
+      const float2 w = lane < gw ? red[parity][w0 + lane] : make_float2(0.0f, 0.0f);
+      parity ^= 1;
+      s1 = warp_sum(w.x);
+      s2 = warp_sum(w.y);
+    }
+    const float c1 = s1 * inv_k, c2 = s2 * inv_k;
+    TX* dx = static_cast<TX*>(p.dx) + r * p.lddx;
+#pragma unroll 4
+    for (int c = t; c < p.k; c += nt) {
+      const float d = to_f32(dy[c]), xh = (to_f32(x[c]) - mean) * rstd;
+      const float a = p.gamma ? d * load_param(p.gamma, p.param_f32, c) : d;
+      float v = rstd * (a - fmaf(xh, c2, c1));
+      if (p.res) v += to_f32(res[c]);
+      const TX o = from_f32<TX>(v);
+      dx[c] = o;
+      mag = max(mag, mag_bits(o));
+    }
+  }
+  cp_async_wait<0>();
+  mag = block_max(mag, mags);
+  if (p.partial) write_partial(p, acc, groups);
+  publish_block(p, mag, mag_out);
 }
 
 // First n0 columns of the blocks' partials [blocks][stride] to out0, the next
@@ -647,24 +835,50 @@ __global__ void __launch_bounds__(256) sum_partials_kernel(const float* partial,
 constexpr int LN_CHUNKS = 64;
 constexpr int LB_MAX_BLOCKS = 160;     // of the one-pass backward kernel; a workspace is sized for it
 
-template <typename TX, bool kVec, int WARPS, int NV>
+template <typename TX, int NV>
 cudaError_t run_forward(const LnParams& p, cudaStream_t s) {
-  constexpr int ROWS = WARPS == 1 ? 8 : 1;
-  constexpr int THREADS = WARPS == 1 ? 256 : 32 * WARPS;
-  const int64_t need = (p.rows + ROWS - 1) / ROWS;
-  const int64_t most = static_cast<int64_t>(device_sm_count()) * (2048 / THREADS);
-  ln_forward_rows_kernel<TX, kVec, WARPS, NV><<<static_cast<int>(need < most ? need : most), THREADS, 0, s>>>(p);
+  const int per_warp = 32 * 8 * NV;
+  const int nt = (p.k + per_warp - 1) / per_warp * 32;
+  int groups = LF_THREADS / nt;
+  if (groups > p.rows) groups = static_cast<int>(p.rows);
+  const int64_t need = (p.rows + groups - 1) / groups;
+  const int64_t most = static_cast<int64_t>(device_sm_count()) * lf_blocks<NV>();
+  const int smem = lf_stages<TX, NV>() * groups * nt * 8 * NV * static_cast<int>(sizeof(TX));
+  auto kern = ln_forward_rows_kernel<TX, NV>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<static_cast<int>(need < most ? need : most), groups * nt, smem, s>>>(p, nt);
   return cudaGetLastError();
 }
 
-template <typename TX, bool kVec>
-cudaError_t dispatch_forward(const LnParams& p, cudaStream_t s) {
-  if (p.k <= 256) return run_forward<TX, kVec, 1, 1>(p, s);
-  if (p.k <= 1024) return run_forward<TX, kVec, 1, 4>(p, s);
-  if (p.k <= 4096) return run_forward<TX, kVec, 4, 4>(p, s);
-  if (p.k <= 8192) return run_forward<TX, kVec, 8, 4>(p, s);
-  if (p.k <= 16384) return run_forward<TX, kVec, 16, 4>(p, s);
-  if (p.k <= 32768) return run_forward<TX, kVec, 32, 4>(p, s);
+// Threads per row of the kernels for rows that start anywhere: about 16
+// elements each.
+int odd_threads(int k) {
+  const int nt = (k + 511) / 512 * 32;
+  return nt < LO_THREADS ? nt : LO_THREADS;
+}
+
+template <typename TX>
+cudaError_t dispatch_forward(const LnParams& p, bool vec, cudaStream_t s) {
+  if (vec && p.k <= LF_THREADS * 16) return run_forward<TX, 2>(p, s);
+  if (vec && p.k <= LF_THREADS * 32) return run_forward<TX, 4>(p, s);
+  if (vec && p.k <= LF_MAX_K) return run_forward<TX, 8>(p, s);
+  const int64_t ring = static_cast<int64_t>(LO_STAGES) * odd_row_bytes(p.k < LF_MAX_K ? p.k : LF_MAX_K, sizeof(TX));
+  if (!vec && p.k <= LF_MAX_K && ring <= LO_SMEM) {
+    const int nt = odd_threads(p.k);
+    const int64_t half = LO_SMEM / 2;                     // two blocks per SM where a row's ring allows it
+    int64_t groups = LO_THREADS / nt;
+    if (groups > half / ring) groups = half / ring > 0 ? half / ring : 1;
+    if (groups > p.rows) groups = p.rows;
+    const int64_t need = (p.rows + groups - 1) / groups;
+    const int64_t most = static_cast<int64_t>(device_sm_count()) * (groups * ring <= half ? 2 : 1);
+    const int smem = static_cast<int>(groups * ring);
+    auto kern = ln_forward_odd_kernel<TX>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kern<<<static_cast<int>(need < most ? need : most), static_cast<int>(groups) * nt, smem, s>>>(p, nt);
+    return cudaGetLastError();
+  }
   const int grid = static_cast<int>(p.rows < 8 * device_sm_count() ? p.rows : 8 * device_sm_count());
   ln_forward_long_kernel<TX><<<grid, LN_THREADS, 0, s>>>(p);
   return cudaGetLastError();
@@ -673,31 +887,33 @@ cudaError_t dispatch_forward(const LnParams& p, cudaStream_t s) {
 // Every row of the operand starts on a 16-byte boundary.
 bool rows_aligned16(const void* p, int64_t ld, bool f32) { return aligned16(p) && (ld * (f32 ? 4 : 2)) % 16 == 0; }
 
-template <typename TX, typename TDY, bool kVec>
-cudaError_t run_backward_rows(LnBwdParams p, float* dgamma, float* dbeta, uint32_t* mags, cudaStream_t s) {
-  const int per_warp = 32 * 8 * LB_NV;
-  const int nt = (p.k + per_warp - 1) / per_warp * 32;
-  // as many groups as the block holds (named barriers 1..15 for groups of several warps)
-  int groups = LB_THREADS / nt;
-  if (groups > p.rows) groups = static_cast<int>(p.rows);
+// Blocks of a one-pass backward kernel, each with `groups` groups of nt
+// threads and smem bytes of shared memory, and the sum over them.
+template <typename Kernel>
+cudaError_t run_backward_blocks(Kernel kern, const LnBwdParams& p, int nt, int groups, size_t smem, float* dgamma,
+                                float* dbeta, uint32_t* mags, cudaStream_t s) {
   const int sms = device_sm_count() < LB_MAX_BLOCKS ? device_sm_count() : LB_MAX_BLOCKS;
   const int64_t need = (p.rows + groups - 1) / groups;
   const int blocks = static_cast<int>(need < sms ? need : sms);
-  const int elem = static_cast<int>(sizeof(TDY) + sizeof(TX) * (p.res ? 2 : 1));
-  size_t smem = static_cast<size_t>(lb_stages<TX, TDY>()) * groups * nt * 8 * LB_NV * elem;
-  const size_t sums = static_cast<size_t>(groups) * 2 * p.k * sizeof(float);
-  if (sums > smem) smem = sums;
-  auto kern = ln_backward_rows_kernel<TX, TDY, kVec>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  // the sum over blocks also joins their maxima: only without it has *amax to be cleared
+  if (e == cudaSuccess && p.amax && !p.partial) e = cudaMemsetAsync(p.amax, 0, sizeof(float), s);
   if (e != cudaSuccess) return e;
   kern<<<blocks, groups * nt, smem, s>>>(p, nt, mags);
   e = cudaGetLastError();
   if (e != cudaSuccess || !p.partial) return e;
-  return launch_sum_partials(p.partial, blocks, 2 * p.k, p.k, p.k, dgamma, dbeta, mags, p.amax, s);
+  return launch_sum_partials(p.partial, blocks, 2 * static_cast<int64_t>(p.k), p.k, p.k, dgamma, dbeta, mags, p.amax, s);
 }
 
 template <typename TX, typename TDY>
+constexpr int64_t lb_elem(bool res) { return static_cast<int64_t>(sizeof(TDY) + sizeof(TX) * (res ? 2 : 1)); }
+
+template <typename TX, typename TDY>
 cudaError_t run_backward_long(const LnBwdParams& p, float* dgamma, float* dbeta, cudaStream_t s) {
+  if (p.amax) {
+    const cudaError_t e = cudaMemsetAsync(p.amax, 0, sizeof(float), s);
+    if (e != cudaSuccess) return e;
+  }
   const int grid = static_cast<int>(p.rows < 8 * device_sm_count() ? p.rows : 8 * device_sm_count());
   ln_backward_dx_long_kernel<TX><<<grid, LN_THREADS, 0, s>>>(p);
   if (p.partial) {
@@ -712,11 +928,38 @@ cudaError_t run_backward_long(const LnBwdParams& p, float* dgamma, float* dbeta,
   return cudaGetLastError();
 }
 
+// Shared memory per group of the odd kernel, 0 where a row is too long for it.
+template <typename TX, typename TDY>
+int64_t odd_backward_bytes(int64_t k, bool res) {
+  if (k > LB_MAX_K) return 0;
+  const int64_t stage = odd_row_bytes(static_cast<int>(k), sizeof(TDY)) +
+                        odd_row_bytes(static_cast<int>(k), sizeof(TX)) * (res ? 2 : 1);
+  const int64_t bytes = LO_STAGES * stage + 8 * k;
+  return bytes + 32 <= LO_SMEM ? bytes : 0;
+}
+
 template <typename TX, typename TDY>
 cudaError_t dispatch_backward(const LnBwdParams& p, bool vec, float* dgamma, float* dbeta, uint32_t* mags, cudaStream_t s) {
-  if (p.k > LB_MAX_K) return run_backward_long<TX, TDY>(p, dgamma, dbeta, s);
-  return vec ? run_backward_rows<TX, TDY, true>(p, dgamma, dbeta, mags, s)
-             : run_backward_rows<TX, TDY, false>(p, dgamma, dbeta, mags, s);
+  if (vec && p.k <= LB_MAX_K) {
+    const int per_warp = 32 * 8 * LB_NV;
+    const int nt = (p.k + per_warp - 1) / per_warp * 32;
+    int groups = LB_THREADS / nt;
+    if (groups > p.rows) groups = static_cast<int>(p.rows);
+    size_t smem = static_cast<size_t>(lb_stages<TX, TDY>() * groups * nt * 8 * LB_NV * lb_elem<TX, TDY>(p.res != nullptr));
+    const size_t sums = static_cast<size_t>(groups) * 2 * p.k * sizeof(float);
+    if (sums > smem) smem = sums;
+    return run_backward_blocks(ln_backward_rows_kernel<TX, TDY>, p, nt, groups, smem, dgamma, dbeta, mags, s);
+  }
+  const int64_t each = vec ? 0 : odd_backward_bytes<TX, TDY>(p.k, p.res != nullptr);
+  if (each > 0) {
+    const int nt = odd_threads(p.k);
+    int64_t groups = LO_THREADS / nt;
+    if (groups > (LO_SMEM - 32) / each) groups = (LO_SMEM - 32) / each;
+    if (groups > p.rows) groups = p.rows;
+    return run_backward_blocks(ln_backward_odd_kernel<TX, TDY>, p, nt, static_cast<int>(groups),
+                               static_cast<size_t>(groups * each + 32), dgamma, dbeta, mags, s);
+  }
+  return run_backward_long<TX, TDY>(p, dgamma, dbeta, s);
 }
 
 }  // namespace
@@ -751,21 +994,18 @@ nvfp4_status launch_layernorm(const LayerNorm& a, cudaStream_t s) {
   const LnParams p{a.x, a.ldx, a.gamma, a.beta, a.param_dtype == NVFP4_DTYPE_F32, a.eps, a.y, a.ldy,
                    yf, a.mean, a.rstd, a.amax, a.rows, static_cast<int>(a.k)};
   const bool vec = rows_aligned16(a.x, a.ldx, xf) && rows_aligned16(a.y, a.ldy, yf) && aligned16(a.gamma) && aligned16(a.beta);
-  if (xf) return launch_status(vec ? dispatch_forward<float, true>(p, s) : dispatch_forward<float, false>(p, s));
-  return launch_status(vec ? dispatch_forward<__nv_bfloat16, true>(p, s) : dispatch_forward<__nv_bfloat16, false>(p, s));
+  return launch_status(xf ? dispatch_forward<float>(p, vec, s) : dispatch_forward<__nv_bfloat16>(p, vec, s));
 }
 
 nvfp4_status launch_layernorm_backward(const LayerNormBackward& a, cudaStream_t s) {
   const bool sums = a.dgamma || a.dbeta;
   cudaError_t e = cudaSuccess;
-  // with column sums the last kernel also joins the blocks' maxima: no clearing needed
-  if (a.amax && (a.rows == 0 || !sums || a.k > LB_MAX_K)) e = cudaMemsetAsync(a.amax, 0, sizeof(float), s);
   if (a.rows == 0) {
+    if (a.amax) e = cudaMemsetAsync(a.amax, 0, sizeof(float), s);
     if (e == cudaSuccess && a.dgamma) e = cudaMemsetAsync(a.dgamma, 0, a.k * sizeof(float), s);
     if (e == cudaSuccess && a.dbeta) e = cudaMemsetAsync(a.dbeta, 0, a.k * sizeof(float), s);
     return launch_status(e);
   }
-  if (e != cudaSuccess) return launch_status(e);
   const bool xf = a.x_dtype == NVFP4_DTYPE_F32, df = a.dy_dtype == NVFP4_DTYPE_F32;
   const LnBwdParams p{a.dy, a.lddy, df, a.x, a.ldx, a.mean, a.rstd, a.gamma,
                       a.param_dtype == NVFP4_DTYPE_F32, a.residual, a.ldr, a.dx, a.lddx,
