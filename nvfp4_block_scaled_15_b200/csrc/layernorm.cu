@@ -189,73 +189,120 @@ __global__ void __launch_bounds__(LN_THREADS) ln_backward_params_long_kernel(con
 __device__ __forceinline__ int chunk_col(int t, int nt, int j) { return 8 * (t + nt * j); }
 __device__ __forceinline__ bool whole(int t, int nt, int j, int k) { return chunk_col(t, nt, j) + 8 <= k; }
 
-__device__ __forceinline__ void unpack8(const uint4 w, float (&x)[8]) {
+// Two fp32 lanes per instruction (add / mul / fma.rn.f32x2): the one-pass
+// kernels are bound by instruction issue as much as by memory.
+__device__ __forceinline__ unsigned long long bits2(float2 a) { return *reinterpret_cast<unsigned long long*>(&a); }
+__device__ __forceinline__ float2 pair2(unsigned long long b) { return *reinterpret_cast<float2*>(&b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return pair2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return pair2(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return pair2(r);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// A chunk: 8 elements as 4 pairs.
+struct Chunk {
+  float2 v[4];
+  __device__ __forceinline__ float& at(int e) { return e & 1 ? v[e >> 1].y : v[e >> 1].x; }
+  __device__ __forceinline__ float get(int e) const { return e & 1 ? v[e >> 1].y : v[e >> 1].x; }
+};
+
+__device__ __forceinline__ Chunk unpack_chunk(const uint4 w) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  Chunk c;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i) c.v[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
+  return c;
 }
 
 // Chunk j's columns of gamma or beta (cached: every row reads them).
-__device__ __forceinline__ void load_param_chunk(const void* p, int f32, int t, int nt, int j, int k, float dflt,
-                                                 float (&x)[8]) {
+__device__ __forceinline__ Chunk load_param_chunk(const void* p, int f32, int t, int nt, int j, int k, float dflt) {
+  Chunk x;
   if (!p) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = dflt;
+    for (int i = 0; i < 4; ++i) x.v[i] = both(dflt);
   } else if (whole(t, nt, j, k)) {
     const int c = chunk_col(t, nt, j);
     if (f32) {
       const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c));
       const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c + 4));
-      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+      x.v[0] = make_float2(a.x, a.y), x.v[1] = make_float2(a.z, a.w);
+      x.v[2] = make_float2(b.x, b.y), x.v[3] = make_float2(b.z, b.w);
     } else {
-      unpack8(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + c)), x);
+      x = unpack_chunk(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + c)));
     }
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int c = chunk_col(t, nt, j) + e;
-      x[e] = c < k ? load_param(p, f32, c) : dflt;
+      x.at(e) = c < k ? load_param(p, f32, c) : dflt;
     }
   }
+  return x;
 }
 
-// Stores a chunk rounded to T; returns the largest stored magnitude.
+// Stores a chunk rounded to T and takes it into the running maximum of stored
+// magnitudes (Mag: both halves of a word for bf16, where one instruction takes
+// the larger magnitudes of two pairs and keeps a NaN).
 template <typename T>
-__device__ __forceinline__ uint32_t store_chunk(T* row, int t, int nt, int j, int k, const float (&x)[8]) {
-  uint32_t mag = 0;
+struct Mag {
+  uint32_t m = 0;
+  __device__ __forceinline__ void pair(uint32_t u) {
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(u));
+  }
+  __device__ __forceinline__ uint32_t bits() const {
+    return max((m & 0x7FFFu) << 16, m & 0x7FFF0000u);
+  }
+};
+template <>
+struct Mag<float> {
+  uint32_t m = 0;
+  __device__ __forceinline__ uint32_t bits() const { return m; }
+};
+
+template <typename T>
+__device__ __forceinline__ void store_chunk(T* row, int t, int nt, int j, int k, const Chunk& x, Mag<T>& mag) {
   if (whole(t, nt, j, k)) {
     T* out = row + chunk_col(t, nt, j);
     if constexpr (sizeof(T) == 2) {
       uint32_t u[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x.v[i].x, x.v[i].y);
         u[i] = *reinterpret_cast<const uint32_t*>(&h);
-        mag = __vmaxu2(mag, u[i] & 0x7FFF7FFFu);
+        mag.pair(u[i]);
       }
       *reinterpret_cast<uint4*>(out) = make_uint4(u[0], u[1], u[2], u[3]);
-      mag = max(mag << 16, mag & 0xFFFF0000u);
     } else {
-      *reinterpret_cast<float4*>(out) = make_float4(x[0], x[1], x[2], x[3]);
-      *reinterpret_cast<float4*>(out + 4) = make_float4(x[4], x[5], x[6], x[7]);
+      *reinterpret_cast<float4*>(out) = make_float4(x.v[0].x, x.v[0].y, x.v[1].x, x.v[1].y);
+      *reinterpret_cast<float4*>(out + 4) = make_float4(x.v[2].x, x.v[2].y, x.v[3].x, x.v[3].y);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) mag = max(mag, mag_bits(x[e]));
+      for (int e = 0; e < 8; ++e) mag.m = max(mag.m, mag_bits(x.get(e)));
     }
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int c = chunk_col(t, nt, j) + e;
       if (c < k) {
-        const T o = from_f32<T>(x[e]);
+        const T o = from_f32<T>(x.get(e));
         row[c] = o;
-        mag = max(mag, mag_bits(o));
+        if constexpr (sizeof(T) == 2)
+          mag.pair(__bfloat16_as_ushort(o));
+        else
+          mag.m = max(mag.m, mag_bits(o));
       }
     }
   }
-  return mag;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -303,15 +350,17 @@ __device__ __forceinline__ void stage_in(uint8_t* slots, const T* row, int t, in
 }
 
 template <typename T>
-__device__ __forceinline__ void stage_out(const uint8_t* slots, int t, int nt, int j, float (&x)[8]) {
+__device__ __forceinline__ Chunk stage_out(const uint8_t* slots, int t, int nt, int j) {
   if constexpr (sizeof(T) == 2) {
-    unpack8(*reinterpret_cast<const uint4*>(slots + (j * nt + t) * 16), x);
+    return unpack_chunk(*reinterpret_cast<const uint4*>(slots + (j * nt + t) * 16));
   } else {
+    Chunk c;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const float4 v = *reinterpret_cast<const float4*>(slots + ((j * 2 + h) * nt + t) * 16);
-      x[4 * h] = v.x, x[4 * h + 1] = v.y, x[4 * h + 2] = v.z, x[4 * h + 3] = v.w;
+      c.v[2 * h] = make_float2(v.x, v.y), c.v[2 * h + 1] = make_float2(v.z, v.w);
     }
+    return c;
   }
 }
 
@@ -329,23 +378,29 @@ __device__ __forceinline__ void group_sync(int g, int nt) {
 // own elements; the row's statistics follow from the warps' (sum, deviations) by
 //   mean = sum_w s_w / k,  sum (x - mean)^2 = sum_w (M_w + n_w (s_w / n_w - mean)^2)
 // (no cancellation, as with sum x^2 - k mean^2), so a row needs one barrier.
-constexpr int LF_THREADS = 512;
 constexpr int LF_MAX_NV = 8;
-constexpr int LF_MAX_K = LF_THREADS * 8 * LF_MAX_NV;
 
-// Blocks per SM, and ring stages: what their share of 192 KB holds of the
-// longest rows of the variant.
+// NV = 2 (rows of up to 8192): 1024 threads, so at least two rows are worked
+// on at once, gamma and beta in shared memory in their own type.  NV = 4, 8:
+// 512 threads of 128 registers (a row's turn is long enough alone), gamma and
+// beta from L2.
 template <int NV>
-constexpr int lf_blocks() { return NV <= 2 ? 2 : 1; }
+constexpr int lf_threads() { return NV <= 2 ? 1024 : 512; }
+template <int NV>
+constexpr int lf_max_k() { return 512 * 8 * NV; }
+// Ring stages: what 128 KB (NV = 2) or 192 KB hold of the variant's longest rows.
 template <typename TX, int NV>
-constexpr int lf_stages() { return 196608 / lf_blocks<NV>() / (LF_THREADS * 8 * NV * static_cast<int>(sizeof(TX))); }
+constexpr int lf_stages() {
+  return (NV <= 2 ? 131072 : 196608) / (lf_threads<NV>() * 8 * NV * static_cast<int>(sizeof(TX)));
+}
 
-template <typename TX, int NV>
-__global__ void __launch_bounds__(LF_THREADS, lf_blocks<NV>()) ln_forward_rows_kernel(const LnParams p, int nt) {
+template <typename TX, typename TY, typename TP, int NV>
+__global__ void __launch_bounds__(lf_threads<NV>(), 1) ln_forward_rows_kernel(const LnParams p, int nt) {
   constexpr int S = lf_stages<TX, NV>();
+  constexpr bool kParamsShared = NV <= 2;
   extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ float2 red[2][LF_THREADS / 32];
-  __shared__ uint32_t mags[LF_THREADS / 32];
+  __shared__ float2 red[2][lf_threads<NV>() / 32];
+  __shared__ uint32_t mags[lf_threads<NV>() / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int groups = blockDim.x / nt, g = threadIdx.x / nt, t = threadIdx.x - g * nt;
   const int gw = nt >> 5, w0 = g * gw;                   // warps of a group, its first
@@ -371,32 +426,56 @@ __global__ void __launch_bounds__(LF_THREADS, lf_blocks<NV>()) ln_forward_rows_k
   };
 #pragma unroll
   for (int i = 0; i < S; ++i) issue(r0 + i * step, i);
-  uint32_t mag = 0;
+  // gamma and beta in the slots of a row of their type, the same for every group
+  uint8_t* gslots = ring + static_cast<size_t>(groups) * S * row_bytes;
+  uint8_t* bslots = gslots + nt * 8 * NV * static_cast<int>(sizeof(TP));
+  if constexpr (kParamsShared) {
+    if (g == 0) {
+      if (p.gamma) stage_in<TP, NV>(gslots, static_cast<const TP*>(p.gamma), t, nt, p.k);
+      if (p.beta) stage_in<TP, NV>(bslots, static_cast<const TP*>(p.beta), t, nt, p.k);
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+    __syncthreads();
+  }
+  auto param = [&](const void* src, const uint8_t* slots, int j, float dflt) {
+    if (kParamsShared && src) return stage_out<TP>(slots, t, nt, j);
+    return load_param_chunk(src, sizeof(TP) == 4, t, nt, j, p.k, dflt);
+  };
+  Mag<TY> mag;
   int parity = 0, stage = 0;
   for (int64_t r = r0; r < p.rows; r += step) {
     cp_async_wait<S - 1>();
-    float x[NV][8];
-    float s = 0.0f;
+    Chunk x[NV];
+    float2 s2 = both(0.0f);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) stage_out<TX>(own + stage * row_bytes, t, nt, j, x[j]);
+    for (int j = 0; j < NV; ++j) x[j] = stage_out<TX>(own + stage * row_bytes, t, nt, j);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s += x[j][e];          // 0 past the row's end
+      for (int i = 0; i < 4; ++i) s2 = add2(s2, x[j].v[i]);          // 0 past the row's end
     issue(r + S * step, stage);                          // the slot is read
     if (++stage == S) stage = 0;
-    s = warp_sum(s);
-    float mean = s * inv_own, m2 = 0.0f;
+    const float s = warp_sum(s2.x + s2.y);
+    float mean = s * inv_own;
+    s2 = both(0.0f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const bool all = whole(t, nt, j, p.k);
+      if (whole(t, nt, j, p.k)) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float d = all || chunk_col(t, nt, j) + e < p.k ? x[j][e] - mean : 0.0f;
-        m2 = fmaf(d, d, m2);
+        for (int i = 0; i < 4; ++i) {
+          const float2 d = add2(x[j].v[i], both(-mean));
+          s2 = fma2(d, d, s2);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float d = chunk_col(t, nt, j) + e < p.k ? x[j].get(e) - mean : 0.0f;
+          s2.x = fmaf(d, d, s2.x);
+        }
       }
     }
-    m2 = warp_sum(m2);
+    float m2 = warp_sum(s2.x + s2.y);
     if (gw > 1) {
       if (lane == 0) red[parity][warp] = make_float2(s, m2);
       group_sync(g, nt);
@@ -407,17 +486,14 @@ __global__ void __launch_bounds__(LF_THREADS, lf_blocks<NV>()) ln_forward_rows_k
       m2 = warp_sum(n_lane > 0.0f ? fmaf(n_lane * d, d, w.y) : 0.0f);
     }
     const float rstd = __frsqrt_rn(fmaf(m2, inv_k, p.eps));
+    TY* y = static_cast<TY*>(p.y) + r * p.ldy;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      float gm[8], bt[8], y[8];
-      load_param_chunk(p.gamma, p.param_f32, t, nt, j, p.k, 1.0f, gm);
-      load_param_chunk(p.beta, p.param_f32, t, nt, j, p.k, 0.0f, bt);
+      const Chunk gm = param(p.gamma, gslots, j, 1.0f), bt = param(p.beta, bslots, j, 0.0f);
+      Chunk o;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = fmaf((x[j][e] - mean) * rstd, gm[e], bt[e]);
-      if (p.y_f32)
-        mag = max(mag, store_chunk<float>(static_cast<float*>(p.y) + r * p.ldy, t, nt, j, p.k, y));
-      else
-        mag = max(mag, store_chunk<__nv_bfloat16>(static_cast<__nv_bfloat16*>(p.y) + r * p.ldy, t, nt, j, p.k, y));
+      for (int i = 0; i < 4; ++i) o.v[i] = fma2(mul2(add2(x[j].v[i], both(-mean)), both(rstd)), gm.v[i], bt.v[i]);
+      store_chunk<TY>(y, t, nt, j, p.k, o, mag);
     }
     if (t == 0) {
       if (p.mean) p.mean[r] = mean;
@@ -426,8 +502,8 @@ __global__ void __launch_bounds__(LF_THREADS, lf_blocks<NV>()) ln_forward_rows_k
   }
   cp_async_wait<0>();
   if (p.amax) {
-    mag = block_max(mag, mags);
-    if (threadIdx.x == 0) atomicMax(reinterpret_cast<unsigned int*>(p.amax), mag);
+    const uint32_t m = block_max(mag.bits(), mags);
+    if (threadIdx.x == 0) atomicMax(reinterpret_cast<unsigned int*>(p.amax), m);
   }
 }
 
@@ -504,14 +580,14 @@ __global__ void __launch_bounds__(LB_THREADS, 1) ln_backward_rows_kernel(const L
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) issue(r0 + i * step, i);
 
-  float gam[LB_NV][8], dg[LB_NV][8], db[LB_NV][8];
+  Chunk gam[LB_NV], dg[LB_NV], db[LB_NV];
 #pragma unroll
   for (int j = 0; j < LB_NV; ++j) {
-    load_param_chunk(p.gamma, p.param_f32, t, nt, j, p.k, 1.0f, gam[j]);
+    gam[j] = load_param_chunk(p.gamma, p.param_f32, t, nt, j, p.k, 1.0f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dg[j][e] = db[j][e] = 0.0f;
+    for (int i = 0; i < 4; ++i) dg[j].v[i] = db[j].v[i] = both(0.0f);
   }
-  uint32_t mag = 0;
+  Mag<TX> mag;
   int parity = 0, stage = 0;
   float mean_next = r0 < p.rows ? p.mean[r0] : 0.0f, rstd_next = r0 < p.rows ? p.rstd[r0] : 0.0f;
   for (int64_t r = r0; r < p.rows; r += step) {
@@ -524,25 +600,29 @@ __global__ void __launch_bounds__(LB_THREADS, 1) ln_backward_rows_kernel(const L
     }
     cp_async_wait<S - 1>();
     const uint8_t* b = own + stage * stage_bytes;
-    float dy[LB_NV][8], xh[LB_NV][8];
-    float s1 = 0.0f, s2 = 0.0f;
+    Chunk dy[LB_NV], xh[LB_NV];
+    float2 sa = both(0.0f), sx = both(0.0f);
 #pragma unroll
     for (int j = 0; j < LB_NV; ++j) {
-      stage_out<TDY>(b, t, nt, j, dy[j]);
-      stage_out<TX>(b + dy_bytes, t, nt, j, xh[j]);
-      const bool all = whole(t, nt, j, p.k);
+      dy[j] = stage_out<TDY>(b, t, nt, j);
+      xh[j] = stage_out<TX>(b + dy_bytes, t, nt, j);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        xh[j][e] = all || chunk_col(t, nt, j) + e < p.k ? (xh[j][e] - mean) * rstd : 0.0f;
-        const float a = dy[j][e] * gam[j][e];         // 0 past the row's end, as dy is
-        s1 += a;
-        s2 = fmaf(a, xh[j][e], s2);
-        dg[j][e] = fmaf(dy[j][e], xh[j][e], dg[j][e]);
-        db[j][e] += dy[j][e];
+      for (int i = 0; i < 4; ++i) xh[j].v[i] = mul2(add2(xh[j].v[i], both(-mean)), both(rstd));
+      if (!whole(t, nt, j, p.k)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (chunk_col(t, nt, j) + e >= p.k) xh[j].at(e) = 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 a = mul2(dy[j].v[i], gam[j].v[i]);       // 0 past the row's end, as dy is
+        sa = add2(sa, a);
+        sx = fma2(a, xh[j].v[i], sx);
+        dg[j].v[i] = fma2(dy[j].v[i], xh[j].v[i], dg[j].v[i]);
+        db[j].v[i] = add2(db[j].v[i], dy[j].v[i]);
       }
     }
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
+    float s1 = warp_sum(sa.x + sa.y), s2 = warp_sum(sx.x + sx.y);
     if (gw > 1) {
       if (lane == 0) red[parity][warp] = make_float2(s1, s2);
       group_sync(g, nt);
@@ -551,24 +631,25 @@ __global__ void __launch_bounds__(LB_THREADS, 1) ln_backward_rows_kernel(const L
       s1 = warp_sum(w.x);
       s2 = warp_sum(w.y);
     }
-    const float c1 = s1 * inv_k, c2 = s2 * inv_k;
+    const float2 c1 = both(-rstd * (s1 * inv_k)), c2 = both(-rstd * (s2 * inv_k));
+    TX* dx = static_cast<TX*>(p.dx) + r * p.lddx;
 #pragma unroll
     for (int j = 0; j < LB_NV; ++j) {
-      float v[8];
+      Chunk v;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = rstd * (dy[j][e] * gam[j][e] - fmaf(xh[j][e], c2, c1));
+      for (int i = 0; i < 4; ++i)
+        v.v[i] = fma2(mul2(dy[j].v[i], gam[j].v[i]), both(rstd), fma2(xh[j].v[i], c2, c1));
       if (p.res) {
-        float res[8];
-        stage_out<TX>(b + dy_bytes + x_bytes, t, nt, j, res);
+        const Chunk res = stage_out<TX>(b + dy_bytes + x_bytes, t, nt, j);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += res[e];
+        for (int i = 0; i < 4; ++i) v.v[i] = add2(v.v[i], res.v[i]);
       }
-      mag = max(mag, store_chunk<TX>(static_cast<TX*>(p.dx) + r * p.lddx, t, nt, j, p.k, v));
+      store_chunk<TX>(dx, t, nt, j, p.k, v, mag);
     }
     if (++stage == S) stage = 0;
   }
   cp_async_wait<0>();
-  mag = block_max(mag, mags);                            // its barrier: every group is done with the ring
+  const uint32_t m = block_max(mag.bits(), mags);         // its barrier: every group is done with the ring
   if (p.partial) {
     float* acc = reinterpret_cast<float*>(ring);          // [groups][2][k]
 #pragma unroll
@@ -577,13 +658,13 @@ __global__ void __launch_bounds__(LB_THREADS, 1) ln_backward_rows_kernel(const L
       for (int e = 0; e < 8; ++e) {
         const int c = chunk_col(t, nt, j) + e;
         if (c < p.k) {
-          acc[(2 * g) * p.k + c] = dg[j][e];
-          acc[(2 * g + 1) * p.k + c] = db[j][e];
+          acc[(2 * g) * p.k + c] = dg[j].get(e);
+          acc[(2 * g + 1) * p.k + c] = db[j].get(e);
         }
       }
     write_partial(p, acc, groups);
   }
-  publish_block(p, mag, mag_out);
+  publish_block(p, m, mag_out);
 }
 
 // ---------------------------------------------------------------------------
@@ -835,20 +916,29 @@ __global__ void __launch_bounds__(256) sum_partials_kernel(const float* partial,
 constexpr int LN_CHUNKS = 64;
 constexpr int LB_MAX_BLOCKS = 160;     // of the one-pass backward kernel; a workspace is sized for it
 
-template <typename TX, int NV>
-cudaError_t run_forward(const LnParams& p, cudaStream_t s) {
+template <typename TX, typename TY, typename TP, int NV>
+cudaError_t run_forward_rows(const LnParams& p, cudaStream_t s) {
   const int per_warp = 32 * 8 * NV;
   const int nt = (p.k + per_warp - 1) / per_warp * 32;
-  int groups = LF_THREADS / nt;
+  int groups = lf_threads<NV>() / nt;
+  if (nt > 32 && groups > 15) groups = 15;                // named barriers 1..15
   if (groups > p.rows) groups = static_cast<int>(p.rows);
   const int64_t need = (p.rows + groups - 1) / groups;
-  const int64_t most = static_cast<int64_t>(device_sm_count()) * lf_blocks<NV>();
-  const int smem = lf_stages<TX, NV>() * groups * nt * 8 * NV * static_cast<int>(sizeof(TX));
-  auto kern = ln_forward_rows_kernel<TX, NV>;
+  const int64_t most = device_sm_count();
+  const int smem = nt * 8 * NV * (lf_stages<TX, NV>() * groups * static_cast<int>(sizeof(TX)) +
+                                  (NV <= 2 ? 2 * static_cast<int>(sizeof(TP)) : 0));
+  auto kern = ln_forward_rows_kernel<TX, TY, TP, NV>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   kern<<<static_cast<int>(need < most ? need : most), groups * nt, smem, s>>>(p, nt);
   return cudaGetLastError();
+}
+
+template <typename TX, int NV>
+cudaError_t run_forward(const LnParams& p, cudaStream_t s) {
+  using bf16 = __nv_bfloat16;
+  if (p.y_f32) return p.param_f32 ? run_forward_rows<TX, float, float, NV>(p, s) : run_forward_rows<TX, float, bf16, NV>(p, s);
+  return p.param_f32 ? run_forward_rows<TX, bf16, float, NV>(p, s) : run_forward_rows<TX, bf16, bf16, NV>(p, s);
 }
 
 // Threads per row of the kernels for rows that start anywhere: about 16
@@ -860,11 +950,11 @@ int odd_threads(int k) {
 
 template <typename TX>
 cudaError_t dispatch_forward(const LnParams& p, bool vec, cudaStream_t s) {
-  if (vec && p.k <= LF_THREADS * 16) return run_forward<TX, 2>(p, s);
-  if (vec && p.k <= LF_THREADS * 32) return run_forward<TX, 4>(p, s);
-  if (vec && p.k <= LF_MAX_K) return run_forward<TX, 8>(p, s);
-  const int64_t ring = static_cast<int64_t>(LO_STAGES) * odd_row_bytes(p.k < LF_MAX_K ? p.k : LF_MAX_K, sizeof(TX));
-  if (!vec && p.k <= LF_MAX_K && ring <= LO_SMEM) {
+  if (vec && p.k <= lf_max_k<2>()) return run_forward<TX, 2>(p, s);
+  if (vec && p.k <= lf_max_k<4>()) return run_forward<TX, 4>(p, s);
+  if (vec && p.k <= lf_max_k<LF_MAX_NV>()) return run_forward<TX, 8>(p, s);
+  const int64_t ring = static_cast<int64_t>(LO_STAGES) * odd_row_bytes(p.k < lf_max_k<LF_MAX_NV>() ? p.k : lf_max_k<LF_MAX_NV>(), sizeof(TX));
+  if (!vec && p.k <= lf_max_k<LF_MAX_NV>() && ring <= LO_SMEM) {
     const int nt = odd_threads(p.k);
     const int64_t half = LO_SMEM / 2;                     // two blocks per SM where a row's ring allows it
     int64_t groups = LO_THREADS / nt;
