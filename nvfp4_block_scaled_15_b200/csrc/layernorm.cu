@@ -183,11 +183,12 @@ __global__ void __launch_bounds__(LN_THREADS) ln_backward_params_long_kernel(con
 // ---------------------------------------------------------------------------
 // Rows held in registers
 // ---------------------------------------------------------------------------
-// Rows that all start on 16-byte boundaries are cut into chunks of 8 elements;
-// thread t of the nt threads that share a row holds chunks t, t + nt, ...
-// (16-byte accesses; the chunk at the row's end element by element).
+// Rows of whole 8-element chunks that all start on 16-byte boundaries: thread
+// t of the nt threads that share a row holds chunks t, t + nt, ...  (Other rows
+// have kernels of their own below: chunks cut by the row's end cost these
+// kernels twice their instructions, as the compiler keeps the elementwise
+// path's bounds in registers.)
 __device__ __forceinline__ int chunk_col(int t, int nt, int j) { return 8 * (t + nt * j); }
-__device__ __forceinline__ bool whole(int t, int nt, int j, int k) { return chunk_col(t, nt, j) + 8 <= k; }
 
 // Two fp32 lanes per instruction (add / mul / fma.rn.f32x2): the one-pass
 // kernels are bound by instruction issue as much as by memory.
@@ -213,7 +214,6 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 // A chunk: 8 elements as 4 pairs.
 struct Chunk {
   float2 v[4];
-  __device__ __forceinline__ float& at(int e) { return e & 1 ? v[e >> 1].y : v[e >> 1].x; }
   __device__ __forceinline__ float get(int e) const { return e & 1 ? v[e >> 1].y : v[e >> 1].x; }
 };
 
@@ -225,28 +225,20 @@ __device__ __forceinline__ Chunk unpack_chunk(const uint4 w) {
   return c;
 }
 
-// Chunk j's columns of gamma or beta (cached: every row reads them).
-__device__ __forceinline__ Chunk load_param_chunk(const void* p, int f32, int t, int nt, int j, int k, float dflt) {
+// Columns c .. c+7 of gamma or beta (cached: every row reads them).
+template <typename TP>
+__device__ __forceinline__ Chunk load_param_chunk(const void* p, int c, int k, float dflt) {
   Chunk x;
-  if (!p) {
+  if (!p || c >= k) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) x.v[i] = both(dflt);
-  } else if (whole(t, nt, j, k)) {
-    const int c = chunk_col(t, nt, j);
-    if (f32) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c));
-      const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c + 4));
-      x.v[0] = make_float2(a.x, a.y), x.v[1] = make_float2(a.z, a.w);
-      x.v[2] = make_float2(b.x, b.y), x.v[3] = make_float2(b.z, b.w);
-    } else {
-      x = unpack_chunk(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + c)));
-    }
+  } else if constexpr (sizeof(TP) == 4) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c + 4));
+    x.v[0] = make_float2(a.x, a.y), x.v[1] = make_float2(a.z, a.w);
+    x.v[2] = make_float2(b.x, b.y), x.v[3] = make_float2(b.z, b.w);
   } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = chunk_col(t, nt, j) + e;
-      x.at(e) = c < k ? load_param(p, f32, c) : dflt;
-    }
+    x = unpack_chunk(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + c)));
   }
   return x;
 }
@@ -271,37 +263,21 @@ struct Mag<float> {
 };
 
 template <typename T>
-__device__ __forceinline__ void store_chunk(T* row, int t, int nt, int j, int k, const Chunk& x, Mag<T>& mag) {
-  if (whole(t, nt, j, k)) {
-    T* out = row + chunk_col(t, nt, j);
-    if constexpr (sizeof(T) == 2) {
-      uint32_t u[4];
+__device__ __forceinline__ void store_chunk(T* out, const Chunk& x, Mag<T>& mag) {
+  if constexpr (sizeof(T) == 2) {
+    uint32_t u[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x.v[i].x, x.v[i].y);
-        u[i] = *reinterpret_cast<const uint32_t*>(&h);
-        mag.pair(u[i]);
-      }
-      *reinterpret_cast<uint4*>(out) = make_uint4(u[0], u[1], u[2], u[3]);
-    } else {
-      *reinterpret_cast<float4*>(out) = make_float4(x.v[0].x, x.v[0].y, x.v[1].x, x.v[1].y);
-      *reinterpret_cast<float4*>(out + 4) = make_float4(x.v[2].x, x.v[2].y, x.v[3].x, x.v[3].y);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) mag.m = max(mag.m, mag_bits(x.get(e)));
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x.v[i].x, x.v[i].y);
+      u[i] = *reinterpret_cast<const uint32_t*>(&h);
+      mag.pair(u[i]);
     }
+    *reinterpret_cast<uint4*>(out) = make_uint4(u[0], u[1], u[2], u[3]);
   } else {
+    *reinterpret_cast<float4*>(out) = make_float4(x.v[0].x, x.v[0].y, x.v[1].x, x.v[1].y);
+    *reinterpret_cast<float4*>(out + 4) = make_float4(x.v[2].x, x.v[2].y, x.v[3].x, x.v[3].y);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = chunk_col(t, nt, j) + e;
-      if (c < k) {
-        const T o = from_f32<T>(x.get(e));
-        row[c] = o;
-        if constexpr (sizeof(T) == 2)
-          mag.pair(__bfloat16_as_ushort(o));
-        else
-          mag.m = max(mag.m, mag_bits(o));
-      }
-    }
+    for (int e = 0; e < 8; ++e) mag.m = max(mag.m, mag_bits(x.get(e)));
   }
 }
 
@@ -337,14 +313,13 @@ __device__ __forceinline__ void stage_in(uint8_t* slots, const T* row, int t, in
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = chunk_col(t, nt, j);
-    if (c + 8 <= k) {
 #pragma unroll
-      for (int h = 0; h < PARTS; ++h) cp_async16(slots + ((j * PARTS + h) * nt + t) * 16, row + c + h * PER);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        reinterpret_cast<T*>(slots + ((j * PARTS + e / PER) * nt + t) * 16)[e % PER] =
-            c + e < k ? row[c + e] : from_f32<T>(0.0f);
+    for (int h = 0; h < PARTS; ++h) {
+      uint8_t* slot = slots + ((j * PARTS + h) * nt + t) * 16;
+      if (c < k)
+        cp_async16(slot, row + c + h * PER);
+      else
+        *reinterpret_cast<uint4*>(slot) = make_uint4(0u, 0u, 0u, 0u);     // past the row's end: zeros
     }
   }
 }
@@ -364,6 +339,33 @@ __device__ __forceinline__ Chunk stage_out(const uint8_t* slots, int t, int nt, 
   }
 }
 
+// Sums of a and b over the warp at the price of one: after the first step the
+// lower half-warp carries a's partial sums and the upper half b's.  The result
+// (sum a, sum b) is on every lane.
+__device__ __forceinline__ float2 warp_sum2(float a, float b) {
+  const bool upper = threadIdx.x & 16;
+  float v = (upper ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, upper ? a : b, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return make_float2(__shfl_sync(0xFFFFFFFFu, v, 0), __shfl_sync(0xFFFFFFFFu, v, 16));
+}
+
+// Mean and squared deviations of a union, from each part's (n, mean, M): with
+// a pivot c and d = mean - c, sum n d and sum (M + n d^2) give
+//   mean = c + sum n d / N,   M = sum (M + n d^2) - (sum n d)^2 / N.
+// The pivot is the first part's mean; then N d^2 is at most M N / n_first, so
+// the last difference loses a factor of at most the number of parts (32),
+// whatever the row's mean.  Parts are the lanes of a warp.
+struct Stats {
+  float mean, m2;
+};
+__device__ __forceinline__ Stats join_lanes(float n, float mean, float m2, float inv_total) {
+  const float pivot = __shfl_sync(0xFFFFFFFFu, mean, 0);
+  const float d = n > 0.0f ? mean - pivot : 0.0f;
+  const float2 s = warp_sum2(n * d, n > 0.0f ? fmaf(n * d, d, m2) : 0.0f);
+  return {fmaf(s.x, inv_total, pivot), fmaf(-s.x * inv_total, s.x, s.y)};
+}
+
 // Named barrier of the nt threads of group g (its warps only).
 __device__ __forceinline__ void group_sync(int g, int nt) {
   asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(nt) : "memory");
@@ -372,135 +374,130 @@ __device__ __forceinline__ void group_sync(int g, int nt) {
 // ---------------------------------------------------------------------------
 // Forward in one pass
 // ---------------------------------------------------------------------------
-// A block has G groups of nt threads; a group takes one row at a time, NV
-// chunks per thread, and S rows ahead are on their way into a ring in shared
-// memory.  Each warp takes the mean and the squared deviations about it of its
-// own elements; the row's statistics follow from the warps' (sum, deviations) by
-//   mean = sum_w s_w / k,  sum (x - mean)^2 = sum_w (M_w + n_w (s_w / n_w - mean)^2)
-// (no cancellation, as with sum x^2 - k mean^2), so a row needs one barrier.
-constexpr int LF_MAX_NV = 8;
-
-// NV = 2 (rows of up to 8192): 1024 threads, so at least two rows are worked
-// on at once, gamma and beta in shared memory in their own type.  NV = 4, 8:
-// 512 threads of 128 registers (a row's turn is long enough alone), gamma and
-// beta from L2.
-template <int NV>
-constexpr int lf_threads() { return NV <= 2 ? 1024 : 512; }
+// A block has G groups of nt threads; a group takes one row at a time, held in
+// registers as it lies in memory, NV chunks per thread.  A thread takes the
+// mean and squared deviations of its own elements; lanes and then warps are
+// joined (join_lanes), so a row needs one barrier and no sum of squares cancels
+// against the mean.  A row's loads, its reductions and its stores alternate, so
+// the memory is kept busy by the other blocks of the SM: registers are held to
+// what allows LF_BLOCKS of them.
+constexpr int LF_THREADS = 256;        // of a block, up to rows of LF_THREADS * 32; 512 beyond
+template <typename TX, int NV>
+constexpr int lf_blocks(int threads) {  // blocks per SM
+  return (NV <= 4 ? (sizeof(TX) == 2 ? 1024 : 768) : (sizeof(TX) == 2 ? 512 : 512)) / threads;
+}
 template <int NV>
 constexpr int lf_max_k() { return 512 * 8 * NV; }
-// Ring stages: what 128 KB (NV = 2) or 192 KB hold of the variant's longest rows.
-template <typename TX, int NV>
-constexpr int lf_stages() {
-  return (NV <= 2 ? 131072 : 196608) / (lf_threads<NV>() * 8 * NV * static_cast<int>(sizeof(TX)));
+constexpr int LF_MAX_K = lf_max_k<8>();
+
+// A chunk as it lies in memory.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16> {
+  uint4 w;
+  __device__ __forceinline__ Chunk get() const { return unpack_chunk(w); }
+};
+template <>
+struct Raw<float> {
+  Chunk c;
+  __device__ __forceinline__ Chunk get() const { return c; }
+};
+
+// Streaming 16-byte load (read once, not kept in L1).
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
 }
 
-template <typename TX, typename TY, typename TP, int NV>
-__global__ void __launch_bounds__(lf_threads<NV>(), 1) ln_forward_rows_kernel(const LnParams p, int nt) {
-  constexpr int S = lf_stages<TX, NV>();
-  constexpr bool kParamsShared = NV <= 2;
-  extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ float2 red[2][lf_threads<NV>() / 32];
-  __shared__ uint32_t mags[lf_threads<NV>() / 32];
+__device__ __forceinline__ void load_raw(Raw<__nv_bfloat16>& x, const __nv_bfloat16* row, int c, int k) {
+  x.w = c < k ? ld_stream(row + c) : make_uint4(0u, 0u, 0u, 0u);
+}
+__device__ __forceinline__ void load_raw(Raw<float>& x, const float* row, int c, int k) {
+  uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+  if (c < k) a = ld_stream(row + c), b = ld_stream(row + c + 4);
+  x.c.v[0] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
+  x.c.v[1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
+  x.c.v[2] = make_float2(__uint_as_float(b.x), __uint_as_float(b.y));
+  x.c.v[3] = make_float2(__uint_as_float(b.z), __uint_as_float(b.w));
+}
+
+template <typename TX, typename TY, typename TP, int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS, lf_blocks<TX, NV>(THREADS)) ln_forward_rows_kernel(const LnParams p, int nt) {
+  __shared__ float2 red[2][THREADS / 32];
+  __shared__ uint32_t mags[THREADS / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int groups = blockDim.x / nt, g = threadIdx.x / nt, t = threadIdx.x - g * nt;
   const int gw = nt >> 5, w0 = g * gw;                   // warps of a group, its first
-  const int row_bytes = nt * 8 * NV * static_cast<int>(sizeof(TX));
-  uint8_t* own = ring + static_cast<size_t>(g) * S * row_bytes;
   const float inv_k = 1.0f / static_cast<float>(p.k);
-  // elements that warp w of a group holds
-  auto count = [&](int w) {
+  // elements of this thread, of its warp, of warp `lane` of the group
+  auto count = [&](int first, int lanes) {
     int n = 0;
-    for (int j = 0; j < NV; ++j) n += min(max(p.k - 8 * (32 * w + nt * j), 0), 256);
+    for (int j = 0; j < NV; ++j) n += min(max(p.k - 8 * (first + nt * j), 0), 8 * lanes);
     return static_cast<float>(n);
   };
-  const float n_own = count(warp - w0);
-  const float inv_own = n_own > 0.0f ? 1.0f / n_own : 0.0f;
-  const float n_lane = lane < gw ? count(lane) : 0.0f;
-  const float inv_lane = n_lane > 0.0f ? 1.0f / n_lane : 0.0f;
+  auto inverse = [](float n) { return n > 0.0f ? 1.0f / n : 0.0f; };
+  const float n_thread = count(t, 1), inv_thread = inverse(n_thread);
+  const float inv_warp = inverse(count(t - lane, 32));
+  const float n_lane = lane < gw ? count(32 * lane, 32) : 0.0f;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * groups + g;
-  auto issue = [&](int64_t r, int stage) {
-    if (r < p.rows)
-      stage_in<TX, NV>(own + stage * row_bytes, static_cast<const TX*>(p.x) + r * p.ldx, t, nt, p.k);
-    cp_async_commit();
-  };
-#pragma unroll
-  for (int i = 0; i < S; ++i) issue(r0 + i * step, i);
-  // gamma and beta in the slots of a row of their type, the same for every group
-  uint8_t* gslots = ring + static_cast<size_t>(groups) * S * row_bytes;
-  uint8_t* bslots = gslots + nt * 8 * NV * static_cast<int>(sizeof(TP));
-  if constexpr (kParamsShared) {
-    if (g == 0) {
-      if (p.gamma) stage_in<TP, NV>(gslots, static_cast<const TP*>(p.gamma), t, nt, p.k);
-      if (p.beta) stage_in<TP, NV>(bslots, static_cast<const TP*>(p.beta), t, nt, p.k);
-    }
-    cp_async_commit();
-    cp_async_wait<0>();
-    __syncthreads();
-  }
-  auto param = [&](const void* src, const uint8_t* slots, int j, float dflt) {
-    if (kParamsShared && src) return stage_out<TP>(slots, t, nt, j);
-    return load_param_chunk(src, sizeof(TP) == 4, t, nt, j, p.k, dflt);
-  };
   Mag<TY> mag;
-  int parity = 0, stage = 0;
-  for (int64_t r = r0; r < p.rows; r += step) {
-    cp_async_wait<S - 1>();
-    Chunk x[NV];
+  int parity = 0;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * groups + g; r < p.rows; r += step) {
+    const TX* row = static_cast<const TX*>(p.x) + r * p.ldx;
+    Raw<TX> x[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) load_raw(x[j], row, chunk_col(t, nt, j), p.k);
     float2 s2 = both(0.0f);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) x[j] = stage_out<TX>(own + stage * row_bytes, t, nt, j);
+    for (int j = 0; j < NV; ++j) {
+      const Chunk c = x[j].get();
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s2 = add2(s2, x[j].v[i]);          // 0 past the row's end
-    issue(r + S * step, stage);                          // the slot is read
-    if (++stage == S) stage = 0;
-    const float s = warp_sum(s2.x + s2.y);
-    float mean = s * inv_own;
+      for (int i = 0; i < 4; ++i) s2 = add2(s2, c.v[i]);             // 0 past the row's end
+    }
+    const float own_mean = (s2.x + s2.y) * inv_thread;
     s2 = both(0.0f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (whole(t, nt, j, p.k)) {
+      if (chunk_col(t, nt, j) < p.k) {
+        const Chunk c = x[j].get();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 d = add2(x[j].v[i], both(-mean));
+          const float2 d = add2(c.v[i], both(-own_mean));
           s2 = fma2(d, d, s2);
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float d = chunk_col(t, nt, j) + e < p.k ? x[j].get(e) - mean : 0.0f;
-          s2.x = fmaf(d, d, s2.x);
         }
       }
     }
-    float m2 = warp_sum(s2.x + s2.y);
+    Stats st = join_lanes(n_thread, own_mean, s2.x + s2.y, inv_warp);
     if (gw > 1) {
-      if (lane == 0) red[parity][warp] = make_float2(s, m2);
+      if (lane == 0) red[parity][warp] = make_float2(st.mean, st.m2);
       group_sync(g, nt);
       const float2 w = lane < gw ? red[parity][w0 + lane] : make_float2(0.0f, 0.0f);
       parity ^= 1;
-      mean = warp_sum(w.x) * inv_k;
-      const float d = fmaf(w.x, inv_lane, -mean);
-      m2 = warp_sum(n_lane > 0.0f ? fmaf(n_lane * d, d, w.y) : 0.0f);
+      st = join_lanes(n_lane, w.x, w.y, inv_k);
     }
-    const float rstd = __frsqrt_rn(fmaf(m2, inv_k, p.eps));
+    const float mean = st.mean;
+    const float rstd = __frsqrt_rn(fmaf(st.m2 < 0.0f ? 0.0f : st.m2, inv_k, p.eps));   // a NaN stays one
     TY* y = static_cast<TY*>(p.y) + r * p.ldy;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const Chunk gm = param(p.gamma, gslots, j, 1.0f), bt = param(p.beta, bslots, j, 0.0f);
-      Chunk o;
+      const int col = chunk_col(t, nt, j);
+      if (col < p.k) {
+        const Chunk gm = load_param_chunk<TP>(p.gamma, col, p.k, 1.0f), bt = load_param_chunk<TP>(p.beta, col, p.k, 0.0f);
+        Chunk c = x[j].get();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o.v[i] = fma2(mul2(add2(x[j].v[i], both(-mean)), both(rstd)), gm.v[i], bt.v[i]);
-      store_chunk<TY>(y, t, nt, j, p.k, o, mag);
+        for (int i = 0; i < 4; ++i) c.v[i] = fma2(mul2(add2(c.v[i], both(-mean)), both(rstd)), gm.v[i], bt.v[i]);
+        store_chunk<TY>(y + col, c, mag);
+      }
     }
     if (t == 0) {
       if (p.mean) p.mean[r] = mean;
       if (p.rstd) p.rstd[r] = rstd;
     }
   }
-  cp_async_wait<0>();
   if (p.amax) {
     const uint32_t m = block_max(mag.bits(), mags);
     if (threadIdx.x == 0) atomicMax(reinterpret_cast<unsigned int*>(p.amax), m);
@@ -583,7 +580,8 @@ __global__ void __launch_bounds__(LB_THREADS, 1) ln_backward_rows_kernel(const L
   Chunk gam[LB_NV], dg[LB_NV], db[LB_NV];
 #pragma unroll
   for (int j = 0; j < LB_NV; ++j) {
-    gam[j] = load_param_chunk(p.gamma, p.param_f32, t, nt, j, p.k, 1.0f);
+    gam[j] = p.param_f32 ? load_param_chunk<float>(p.gamma, chunk_col(t, nt, j), p.k, 1.0f)
+                         : load_param_chunk<__nv_bfloat16>(p.gamma, chunk_col(t, nt, j), p.k, 1.0f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) dg[j].v[i] = db[j].v[i] = both(0.0f);
   }
@@ -608,33 +606,30 @@ __global__ void __launch_bounds__(LB_THREADS, 1) ln_backward_rows_kernel(const L
       xh[j] = stage_out<TX>(b + dy_bytes, t, nt, j);
 #pragma unroll
       for (int i = 0; i < 4; ++i) xh[j].v[i] = mul2(add2(xh[j].v[i], both(-mean)), both(rstd));
-      if (!whole(t, nt, j, p.k)) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (chunk_col(t, nt, j) + e >= p.k) xh[j].at(e) = 0.0f;
-      }
+      if (chunk_col(t, nt, j) >= p.k) continue;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 a = mul2(dy[j].v[i], gam[j].v[i]);       // 0 past the row's end, as dy is
+        const float2 a = mul2(dy[j].v[i], gam[j].v[i]);
         sa = add2(sa, a);
         sx = fma2(a, xh[j].v[i], sx);
         dg[j].v[i] = fma2(dy[j].v[i], xh[j].v[i], dg[j].v[i]);
         db[j].v[i] = add2(db[j].v[i], dy[j].v[i]);
       }
     }
-    float s1 = warp_sum(sa.x + sa.y), s2 = warp_sum(sx.x + sx.y);
+    float2 sum = warp_sum2(sa.x + sa.y, sx.x + sx.y);
     if (gw > 1) {
-      if (lane == 0) red[parity][warp] = make_float2(s1, s2);
+      if (lane == 0) red[parity][warp] = sum;
       group_sync(g, nt);
       const float2 w = lane < gw ? red[parity][w0 + lane] : make_float2(0.0f, 0.0f);
       parity ^= 1;
-      s1 = warp_sum(w.x);
-      s2 = warp_sum(w.y);
+      sum = warp_sum2(w.x, w.y);
     }
-    const float2 c1 = both(-rstd * (s1 * inv_k)), c2 = both(-rstd * (s2 * inv_k));
+    const float2 c1 = both(-rstd * (sum.x * inv_k)), c2 = both(-rstd * (sum.y * inv_k));
     TX* dx = static_cast<TX*>(p.dx) + r * p.lddx;
 #pragma unroll
     for (int j = 0; j < LB_NV; ++j) {
+      const int col = chunk_col(t, nt, j);
+      if (col >= p.k) continue;
       Chunk v;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -644,7 +639,7 @@ __global__ void __launch_bounds__(LB_THREADS, 1) ln_backward_rows_kernel(const L
 #pragma unroll
         for (int i = 0; i < 4; ++i) v.v[i] = add2(v.v[i], res.v[i]);
       }
-      store_chunk<TX>(dx, t, nt, j, p.k, v, mag);
+      store_chunk<TX>(dx + col, v, mag);
     }
     if (++stage == S) stage = 0;
   }
@@ -653,15 +648,15 @@ __global__ void __launch_bounds__(LB_THREADS, 1) ln_backward_rows_kernel(const L
   if (p.partial) {
     float* acc = reinterpret_cast<float*>(ring);          // [groups][2][k]
 #pragma unroll
-    for (int j = 0; j < LB_NV; ++j)
+    for (int j = 0; j < LB_NV; ++j) {
+      const int c = chunk_col(t, nt, j);
+      if (c >= p.k) continue;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int c = chunk_col(t, nt, j) + e;
-        if (c < p.k) {
-          acc[(2 * g) * p.k + c] = dg[j].get(e);
-          acc[(2 * g + 1) * p.k + c] = db[j].get(e);
-        }
+        acc[(2 * g) * p.k + c + e] = dg[j].get(e);
+        acc[(2 * g + 1) * p.k + c + e] = db[j].get(e);
       }
+    }
     write_partial(p, acc, groups);
   }
   publish_block(p, m, mag_out);
@@ -916,29 +911,27 @@ __global__ void __launch_bounds__(256) sum_partials_kernel(const float* partial,
 constexpr int LN_CHUNKS = 64;
 constexpr int LB_MAX_BLOCKS = 160;     // of the one-pass backward kernel; a workspace is sized for it
 
-template <typename TX, typename TY, typename TP, int NV>
+template <typename TX, typename TY, typename TP, int NV, int THREADS>
 cudaError_t run_forward_rows(const LnParams& p, cudaStream_t s) {
   const int per_warp = 32 * 8 * NV;
   const int nt = (p.k + per_warp - 1) / per_warp * 32;
-  int groups = lf_threads<NV>() / nt;
-  if (nt > 32 && groups > 15) groups = 15;                // named barriers 1..15
+  int groups = THREADS / nt;
   if (groups > p.rows) groups = static_cast<int>(p.rows);
   const int64_t need = (p.rows + groups - 1) / groups;
-  const int64_t most = device_sm_count();
-  const int smem = nt * 8 * NV * (lf_stages<TX, NV>() * groups * static_cast<int>(sizeof(TX)) +
-                                  (NV <= 2 ? 2 * static_cast<int>(sizeof(TP)) : 0));
-  auto kern = ln_forward_rows_kernel<TX, TY, TP, NV>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  kern<<<static_cast<int>(need < most ? need : most), groups * nt, smem, s>>>(p, nt);
+  const int64_t most = static_cast<int64_t>(device_sm_count()) * lf_blocks<TX, NV>(THREADS);
+  ln_forward_rows_kernel<TX, TY, TP, NV, THREADS>
+      <<<static_cast<int>(need < most ? need : most), groups * nt, 0, s>>>(p, nt);
   return cudaGetLastError();
 }
 
-template <typename TX, int NV>
+template <typename TX, int NV, int THREADS>
 cudaError_t run_forward(const LnParams& p, cudaStream_t s) {
   using bf16 = __nv_bfloat16;
-  if (p.y_f32) return p.param_f32 ? run_forward_rows<TX, float, float, NV>(p, s) : run_forward_rows<TX, float, bf16, NV>(p, s);
-  return p.param_f32 ? run_forward_rows<TX, bf16, float, NV>(p, s) : run_forward_rows<TX, bf16, bf16, NV>(p, s);
+  if (p.y_f32)
+    return p.param_f32 ? run_forward_rows<TX, float, float, NV, THREADS>(p, s)
+                       : run_forward_rows<TX, float, bf16, NV, THREADS>(p, s);
+  return p.param_f32 ? run_forward_rows<TX, bf16, float, NV, THREADS>(p, s)
+                     : run_forward_rows<TX, bf16, bf16, NV, THREADS>(p, s);
 }
 
 // Threads per row of the kernels for rows that start anywhere: about 16
@@ -950,11 +943,11 @@ int odd_threads(int k) {
 
 template <typename TX>
 cudaError_t dispatch_forward(const LnParams& p, bool vec, cudaStream_t s) {
-  if (vec && p.k <= lf_max_k<2>()) return run_forward<TX, 2>(p, s);
-  if (vec && p.k <= lf_max_k<4>()) return run_forward<TX, 4>(p, s);
-  if (vec && p.k <= lf_max_k<LF_MAX_NV>()) return run_forward<TX, 8>(p, s);
-  const int64_t ring = static_cast<int64_t>(LO_STAGES) * odd_row_bytes(p.k < lf_max_k<LF_MAX_NV>() ? p.k : lf_max_k<LF_MAX_NV>(), sizeof(TX));
-  if (!vec && p.k <= lf_max_k<LF_MAX_NV>() && ring <= LO_SMEM) {
+  if (vec && p.k <= LF_THREADS * 32) return run_forward<TX, 4, LF_THREADS>(p, s);
+  if (vec && p.k <= lf_max_k<4>()) return run_forward<TX, 4, 512>(p, s);
+  if (vec && p.k <= LF_MAX_K) return run_forward<TX, 8, 512>(p, s);
+  const int64_t ring = static_cast<int64_t>(LO_STAGES) * odd_row_bytes(p.k < LF_MAX_K ? p.k : LF_MAX_K, sizeof(TX));
+  if (!vec && p.k <= LF_MAX_K && ring <= LO_SMEM) {
     const int nt = odd_threads(p.k);
     const int64_t half = LO_SMEM / 2;                     // two blocks per SM where a row's ring allows it
     int64_t groups = LO_THREADS / nt;
@@ -1083,7 +1076,7 @@ nvfp4_status launch_layernorm(const LayerNorm& a, cudaStream_t s) {
   const bool xf = a.x_dtype == NVFP4_DTYPE_F32, yf = a.y_dtype == NVFP4_DTYPE_F32;
   const LnParams p{a.x, a.ldx, a.gamma, a.beta, a.param_dtype == NVFP4_DTYPE_F32, a.eps, a.y, a.ldy,
                    yf, a.mean, a.rstd, a.amax, a.rows, static_cast<int>(a.k)};
-  const bool vec = rows_aligned16(a.x, a.ldx, xf) && rows_aligned16(a.y, a.ldy, yf) && aligned16(a.gamma) && aligned16(a.beta);
+  const bool vec = a.k % 8 == 0 && rows_aligned16(a.x, a.ldx, xf) && rows_aligned16(a.y, a.ldy, yf) && aligned16(a.gamma) && aligned16(a.beta);
   return launch_status(xf ? dispatch_forward<float>(p, vec, s) : dispatch_forward<__nv_bfloat16>(p, vec, s));
 }
 
@@ -1100,7 +1093,7 @@ nvfp4_status launch_layernorm_backward(const LayerNormBackward& a, cudaStream_t 
   const LnBwdParams p{a.dy, a.lddy, df, a.x, a.ldx, a.mean, a.rstd, a.gamma,
                       a.param_dtype == NVFP4_DTYPE_F32, a.residual, a.ldr, a.dx, a.lddx,
                       sums ? static_cast<float*>(a.workspace) : nullptr, a.amax, a.rows, static_cast<int>(a.k)};
-  const bool vec = rows_aligned16(a.dy, a.lddy, df) && rows_aligned16(a.x, a.ldx, xf) && rows_aligned16(a.dx, a.lddx, xf) &&
+  const bool vec = a.k % 8 == 0 && rows_aligned16(a.dy, a.lddy, df) && rows_aligned16(a.x, a.ldx, xf) && rows_aligned16(a.dx, a.lddx, xf) &&
                    aligned16(a.gamma) && (!a.residual || rows_aligned16(a.residual, a.ldr, xf));
   uint32_t* mags = sums ? reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.workspace) +
                                                       layernorm_backward_workspace_bytes(a.rows, a.k) -
