@@ -36,6 +36,30 @@ __device__ __forceinline__ float act_value(float v, int act) {
   }
 }
 
+// The same for an array, with one branch on the activation.
+template <int N>
+__device__ __forceinline__ void act_values(float (&x)[N], int act) {
+  switch (act) {
+    case NVFP4_ACT_RELU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = act_value(x[i], NVFP4_ACT_RELU);
+      break;
+    case NVFP4_ACT_GELU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = act_value(x[i], NVFP4_ACT_GELU);
+      break;
+    case NVFP4_ACT_GELU_TANH:
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = act_value(x[i], NVFP4_ACT_GELU_TANH);
+      break;
+    case NVFP4_ACT_SILU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = act_value(x[i], NVFP4_ACT_SILU);
+      break;
+    default: break;
+  }
+}
+
 // act'(v).  The logistic forms are written on e = e^{-|.|} <= 1, so neither
 // p (1 - p) nor the tails cancel or overflow; past |v| = 16 (gelu) or 128
 // (silu) the second term is below the smallest normal number and left out, so

@@ -22,6 +22,8 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <type_traits>
+
 #include "epilogue.cuh"
 #include "internal.h"
 #include "ptx.cuh"
@@ -61,11 +63,12 @@ namespace {
 // ---------------------------------------------------------------------------
 // GEMM configuration
 // ---------------------------------------------------------------------------
-template <int BN_, bool kMx>
+template <int BN_, bool kMx, bool kE = false>
 struct GemmCfg {
   using F = ScaleFmt<kMx>;
   static constexpr int BN = BN_;
-  static constexpr int STAGES = (BN == 256) ? 4 : 6;
+  // kE: one stage makes room for the epilogue's boxes (4 KB per epilogue warp)
+  static constexpr int STAGES = ((BN == 256) ? 4 : 6) - (kE ? 1 : 0);
   static constexpr int A_BYTES = BM * BK_BYTES;
   static constexpr int B_BYTES = BN * BK_BYTES;
   static constexpr int SFA_BYTES = F::ATOMS_PER_STAGE * SF_ATOM;
@@ -78,7 +81,8 @@ struct GemmCfg {
   static constexpr int EPI_WARPS = 8;
   static constexpr int THREADS = (2 + EPI_WARPS) * 32;
   static constexpr int BAR_BYTES = 256;
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + BAR_BYTES + 1024;
+  static constexpr int BOX_BYTES = kE ? EPI_WARPS * 32 * 32 * 4 : 0;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + BOX_BYTES + BAR_BYTES + 1024;
   static_assert(TMEM_SF_BASE + STAGES * SF_COLS_PER_STAGE <= (int)TMEM_COLS, "TMEM budget");
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
@@ -106,17 +110,14 @@ struct GemmParams {
   const float* g_d;
   float* amax_d;    // max |alpha acc| over D, or null (with an epilogue: max |D| as stored)
   // Epilogue kernels only: D = act(alpha acc + bias) + residual, pre the value
-  // before act; residual and pre have D's type (vec_res / vec_pre: 16-byte
-  // aligned rows).
+  // before act; residual and pre have D's type.
   const void* bias;
   int bias_f32;
   int act;
   const void* res;
   int64_t ldr;
-  int vec_res;
   void* pre;
   int64_t ldp;
-  int vec_pre;
   uint64_t wait_limit_ns;
   int* status;
   // Quantize-and-GEMM kernel only: A arrives as bf16 rows (qa_x, pitch
@@ -293,90 +294,144 @@ __device__ __forceinline__ void store_row(const GemmParams& p, int row, int col0
   }
 }
 
-// Eight values of row `row`, columns c .. c+7, as T: one or two 16-byte
-// accesses when the row is aligned (vec) and whole, else the n_valid elements
-// one by one.
+// ---------------------------------------------------------------------------
+// Epilogue with bias, activation and residual: v = alpha acc + bias, pre = v,
+// D = act(v) + residual, each rounded once to its type.
+// ---------------------------------------------------------------------------
+// An epilogue thread holds a row of 32 columns (a box: 32 rows x 32 columns per
+// warp).  Stored from there, a warp's store would touch 32 rows; so boxes pass
+// through shared memory, rows of 32 elements whose 16-byte chunks are permuted
+// by row so that neither side meets bank conflicts (for bf16 the 64-byte
+// swizzle of the tensor maps).
+constexpr int EPI_BOX = 32;
+constexpr int EPI_ROWS_BYTES = EPI_BOX * EPI_BOX * 4;      // a box of fp32
+
 template <typename T>
-__device__ __forceinline__ void load8(const void* base, int64_t ld, int row, int c, int n_valid, bool vec, float (&x)[8]) {
-  const T* in = static_cast<const T*>(base) + static_cast<int64_t>(row) * ld + c;
-  if (vec && n_valid >= 8) {
-    if constexpr (sizeof(T) == 2) {
-      const uint4 w = *reinterpret_cast<const uint4*>(in);
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ int box_chunk(int row, int q) {
+  return sizeof(T) == 2 ? row * 64 + ((q ^ ((row >> 1) & 3)) << 4) : row * 128 + ((q ^ (row & 7)) << 4);
+}
+
+// This thread's row of a box from / to registers.
+template <typename T>
+__device__ __forceinline__ void box_put(uint8_t* box, int row, const float (&x)[EPI_BOX]) {
+  constexpr int PER = 16 / sizeof(T);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(u[i] << 16);
-        x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+  for (int q = 0; q < EPI_BOX / PER; ++q) {
+    uint4 w;
+    if constexpr (sizeof(T) == 2)
+      w = make_uint4(pack_bf16x2(x[8 * q], x[8 * q + 1]), pack_bf16x2(x[8 * q + 2], x[8 * q + 3]),
+                     pack_bf16x2(x[8 * q + 4], x[8 * q + 5]), pack_bf16x2(x[8 * q + 6], x[8 * q + 7]));
+    else
+      w = make_uint4(__float_as_uint(x[4 * q]), __float_as_uint(x[4 * q + 1]), __float_as_uint(x[4 * q + 2]),
+                     __float_as_uint(x[4 * q + 3]));
+    *reinterpret_cast<uint4*>(box + box_chunk<T>(row, q)) = w;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void box_add(const uint8_t* box, int row, float (&x)[EPI_BOX]) {
+  constexpr int PER = 16 / sizeof(T);
+#pragma unroll
+  for (int q = 0; q < EPI_BOX / PER; ++q) {
+    const uint4 w = *reinterpret_cast<const uint4*>(box + box_chunk<T>(row, q));
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 2) {
+        x[8 * q + 2 * i] += __uint_as_float(u[i] << 16);
+        x[8 * q + 2 * i + 1] += __uint_as_float(u[i] & 0xFFFF0000u);
+      } else {
+        x[4 * q + i] += __uint_as_float(u[i]);
       }
-    } else {
-      const float4 a = *reinterpret_cast<const float4*>(in), b = *reinterpret_cast<const float4*>(in + 4);
-      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = i < n_valid ? to_f32(in[i]) : 0.0f;
   }
 }
 
+// A box between shared memory and the rows row0 .. of a matrix, lane l at
+// column col + l: one coalesced access per row, any alignment.
 template <typename T>
-__device__ __forceinline__ void store8(void* base, int64_t ld, int row, int c, int n_valid, bool vec, const float (&x)[8]) {
-  T* out = static_cast<T*>(base) + static_cast<int64_t>(row) * ld + c;
-  if (vec && n_valid >= 8) {
-    if constexpr (sizeof(T) == 2) {
-      *reinterpret_cast<uint4*>(out) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                  pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-    } else {
-      *reinterpret_cast<float4*>(out) = make_float4(x[0], x[1], x[2], x[3]);
-      *reinterpret_cast<float4*>(out + 4) = make_float4(x[4], x[5], x[6], x[7]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n_valid) out[i] = from_f32<T>(x[i]);
-  }
+__device__ __forceinline__ T* box_elem(uint8_t* box, int row, int lane) {
+  constexpr int PER = 16 / sizeof(T);
+  return reinterpret_cast<T*>(box + box_chunk<T>(row, lane / PER)) + lane % PER;
+}
+template <typename T>
+__device__ __forceinline__ void box_rows_out(uint8_t* box, void* base, int64_t ld, int row0, int rows, int col, bool in) {
+  const int lane = threadIdx.x & 31;
+  T* out = static_cast<T*>(base) + static_cast<int64_t>(row0) * ld + col + lane;
+  if (!in) return;
+#pragma unroll 8
+  for (int r = 0; r < rows; ++r) out[r * ld] = *box_elem<T>(box, r, lane);
+}
+template <typename T>
+__device__ __forceinline__ void box_rows_in(uint8_t* box, const void* base, int64_t ld, int row0, int rows, int col, bool in) {
+  const int lane = threadIdx.x & 31;
+  const T* src = static_cast<const T*>(base) + static_cast<int64_t>(row0) * ld + col + lane;
+  if (!in) return;
+#pragma unroll 16
+  for (int r = 0; r < rows; ++r) *box_elem<T>(box, r, lane) = src[r * ld];
 }
 
-// Epilogue of NV columns of one row held in v (the accumulator): v = alpha
-// acc + bias, pre = v, D = act(v) + residual, each rounded once to T; mag is
-// the running maximum of |D| as stored.
-template <typename T, int NV>
-__device__ __forceinline__ void store_row_epi(const GemmParams& p, int row, int col0, const uint32_t (&v)[NV],
-                                              float alpha, uint32_t& mag) {
-  if (row >= p.M) return;
+// x = alpha acc + bias of a box; lane l holds the bias of column col + l.
+__device__ __forceinline__ void box_values(const uint32_t* v, float alpha, float bias, float (&x)[EPI_BOX]) {
 #pragma unroll
-  for (int g = 0; g < NV / 8; ++g) {
-    const int c = col0 + 8 * g;
-    const int n_valid = p.N - c;
-    if (n_valid <= 0) break;
-    float x[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float b = p.bias && i < n_valid ? load_param(p.bias, p.bias_f32, c + i) : 0.0f;
-      x[i] = fmaf(__uint_as_float(v[8 * g + i]), alpha, b);
-    }
-    if (p.pre) store8<T>(p.pre, p.ldp, row, c, n_valid, p.vec_pre, x);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = act_value(x[i], p.act);
-    if (p.res) {
-      float r[8];
-      load8<T>(p.res, p.ldr, row, c, n_valid, p.vec_res, r);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] += r[i];
-    }
-    store8<T>(p.d, p.ldd, row, c, n_valid, p.vec_store, x);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n_valid) mag = max(mag, mag_bits(from_f32<T>(x[i])));
-  }
+  for (int i = 0; i < EPI_BOX; ++i) x[i] = fmaf(__uint_as_float(v[i]), alpha, __shfl_sync(0xFFFFFFFFu, bias, i));
+}
+__device__ __forceinline__ float box_bias(const GemmParams& p, int col) {
+  const int c = col + static_cast<int>(threadIdx.x & 31);
+  return p.bias && c < p.N ? load_param(p.bias, p.bias_f32, c) : 0.0f;
 }
 
+// Largest stored magnitude of this thread's row, columns below n_valid.
+template <typename T>
+__device__ __forceinline__ void box_mag(const float (&x)[EPI_BOX], int n_valid, uint32_t& mag) {
+#pragma unroll
+  for (int i = 0; i < EPI_BOX; ++i)
+    if (i < n_valid) mag = max(mag, mag_bits(from_f32<T>(x[i])));
+}
+
+// One box of any type and alignment; `box`: EPI_ROWS_BYTES of this warp.
+template <typename T>
+__device__ __forceinline__ void store_box_rows(const GemmParams& p, uint8_t* box, int row0, int col, const uint32_t* v,
+                                               float alpha, float bias, uint32_t& mag) {
+  const int lane = threadIdx.x & 31;
+  const int rows = min(EPI_BOX, p.M - row0);
+  const bool in = col + lane < p.N;
+  float x[EPI_BOX];
+  box_values(v, alpha, bias, x);
+  if (p.pre) {
+    box_put<T>(box, lane, x);
+    __syncwarp();
+    box_rows_out<T>(box, p.pre, p.ldp, row0, rows, col, in);
+    __syncwarp();
+  }
+  act_values(x, p.act);
+  if (p.res) {
+    box_rows_in<T>(box, p.res, p.ldr, row0, rows, col, in);
+    __syncwarp();
+    box_add<T>(box, lane, x);
+    __syncwarp();
+  }
+  box_put<T>(box, lane, x);
+  __syncwarp();
+  box_rows_out<T>(box, p.d, p.ldd, row0, rows, col, in);
+  __syncwarp();
+  if (lane < rows) box_mag<T>(x, p.N - col, mag);
+}
+
+// NV columns (held in v, a row per thread) from column col0, box by box.
 template <int NV>
-__device__ __forceinline__ void store_row_epi(const GemmParams& p, int row, int col0, const uint32_t (&v)[NV],
-                                              float alpha, uint32_t& mag) {
-  if (p.out_f32)
-    store_row_epi<float, NV>(p, row, col0, v, alpha, mag);
-  else
-    store_row_epi<__nv_bfloat16, NV>(p, row, col0, v, alpha, mag);
+__device__ __forceinline__ void store_rows_epi(const GemmParams& p, uint8_t* box, int row0, int col0,
+                                               const uint32_t (&v)[NV], float alpha, uint32_t& mag) {
+  if (row0 >= p.M) return;
+#pragma unroll
+  for (int c = 0; c < NV / EPI_BOX; ++c) {
+    const int col = col0 + c * EPI_BOX;
+    if (col >= p.N) break;
+    const float bias = box_bias(p, col);
+    if (p.out_f32)
+      store_box_rows<float>(p, box, row0, col, v + c * EPI_BOX, alpha, bias, mag);
+    else
+      store_box_rows<__nv_bfloat16>(p, box, row0, col, v + c * EPI_BOX, alpha, bias, mag);
+  }
 }
 
 __device__ __forceinline__ void publish_mag(const GemmParams& p, uint32_t mag) {
@@ -390,11 +445,11 @@ template <int BN, bool kMx, bool kE>
 __global__ void __launch_bounds__(GemmCfg<BN, kMx>::THREADS, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const GemmParams p) {
-  using C = GemmCfg<BN, kMx>;
+  using C = GemmCfg<BN, kMx, kE>;
   using F = typename C::F;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::STAGE_BYTES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::STAGE_BYTES + C::BOX_BYTES);
   uint64_t* empty = full + C::STAGES;
   uint64_t* acc_full = empty + C::STAGES;
   uint64_t* acc_empty = acc_full + C::ACC_BUFS;
@@ -577,7 +632,7 @@ __global__ void __launch_bounds__(GemmCfg<BN, kMx>::THREADS, 1)
       const int col0 = tn * BN + half * HALF;
       if (col0 < p.N) {
         if constexpr (kE)
-          store_row_epi<HALF>(p, row, col0, v, alpha, mag);
+          store_rows_epi<HALF>(p, smem + C::STAGES * C::STAGE_BYTES + ew * EPI_ROWS_BYTES, row - lane, col0, v, alpha, mag);
         else if (p.out_q)
           store_row_q<HALF>(p, row, col0, v, alpha, gd, amax_run);
         else
@@ -614,11 +669,11 @@ constexpr int QA_WARPS = 4;
 constexpr int QA_BLOCKS = 8;
 constexpr int QA_UNIT_BLOCKS = 32 * QA_BLOCKS;
 
-template <bool kMx>
+template <bool kMx, bool kE = false>
 struct PairCfg {
   using F = ScaleFmt<kMx>;
   static constexpr int BN = 256;                       // N per tile (both CTAs)
-  static constexpr int STAGES = 5;
+  static constexpr int STAGES = kE ? 4 : 5;            // kE: one stage makes room for two more boxes per warp
   static constexpr int A_BYTES = BM * BK_BYTES;        // this CTA's 128 rows of A
   static constexpr int B_BYTES = 128 * BK_BYTES;       // this CTA's half of B
   static constexpr int SFA_BYTES = F::ATOMS_PER_STAGE * SF_ATOM;
@@ -640,15 +695,18 @@ struct PairCfg {
   // (64-B rows, 64-B swizzle) written to global memory by TMA stores.
   static constexpr int EPI_BOX_COLS = 32;
   static constexpr int EPI_BOX_BYTES = 32 * EPI_BOX_COLS * 2;
-  static constexpr int EPI_BYTES = EPI_WARPS * 2 * EPI_BOX_BYTES;
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_BYTES + 256 + 1024;
+  static constexpr int EPI_BOXES = kE ? 4 : 2;         // per warp (kE: residual in and D out, pre; or two fp32 boxes)
+  static constexpr int EPI_BYTES = EPI_WARPS * EPI_BOXES * EPI_BOX_BYTES;
+  static constexpr int RES_BAR_BYTES = kE ? EPI_WARPS * EPI_BOXES * 8 : 0;   // one mbarrier per residual box
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_BYTES + 256 + RES_BAR_BYTES + 1024;
   // Quantize-and-GEMM kernel: QA_WARPS more warps quantize A's rows; the
   // E4M3 scale table takes 1 KB more.
+  static_assert(SMEM_BYTES <= 232448, "shared memory budget");
   static constexpr int THREADS_QA = THREADS + QA_WARPS * 32;
   static constexpr int SMEM_BYTES_QA = SMEM_BYTES + 128 * 8;
   static_assert(STAGE_BYTES % 1024 == 0, "stages stay 1024-B aligned");
   static_assert(TMEM_SF_BASE + SF_COLS <= (int)TMEM_COLS, "TMEM budget");
-  static_assert(SMEM_BYTES_QA <= 232448, "shared memory budget");
+  static_assert(kE || SMEM_BYTES_QA <= 232448, "shared memory budget");
 };
 
 // Wait (bounded) until chunk c of every row of 256-row block tm of A is
@@ -761,6 +819,112 @@ __device__ __forceinline__ void qa_quantize_store(const GemmParams& p, int r, in
   }
 }
 
+// Tensor maps of the residual and of pre (kE).
+struct EpiMaps {
+  CUtensorMap res, pre;
+};
+struct NoMaps {};
+
+// One epilogue warp's way out of the CTA-pair kernel for bf16 D, residual and
+// pre that TMA can address (16-byte aligned rows of whole 16-byte chunks).  A
+// tile gives a warp four boxes of 32 x 32 (steps 0..3: the 64 columns shared
+// with the other accumulator first).  The residual's boxes are fetched before
+// the accumulator is waited for, added in place, and leave from where they
+// arrived; pre leaves from boxes of its own:
+//   no residual: D in boxes 0, 1 in turn;  residual without pre: all four
+//   steps' boxes fetched at once;  residual and pre: boxes 0, 1, the later two
+//   steps' fetched when the store that reads the box is done.  pre: boxes 2, 3.
+struct EpiWriter {
+  uint8_t* boxes;
+  uint64_t* bars;            // arrivals of residual boxes
+  uint32_t mag = 0;          // |D|, fp32 bits
+  uint32_t mag2 = 0;         // |D|, two bf16
+  uint32_t parity = 0;       // of bars[0..3]
+  uint32_t pending = 0;      // residual boxes fetched and not waited for
+  int row0 = 0, col0 = 0, first = 0;
+
+  static constexpr uint32_t BYTES = EPI_BOX * EPI_BOX * 2;
+
+  __device__ __forceinline__ int col(int s) const { return col0 + (s < 2 ? first : 64 - first) + (s & 1) * EPI_BOX; }
+
+  __device__ __forceinline__ void fetch(const GemmParams& p, const EpiMaps& m, int s, int buf) {
+    if (col(s) >= p.N) return;
+    pending |= 1u << buf;
+    if ((threadIdx.x & 31) == 0) {
+      mbar_arrive_expect_tx(&bars[buf], BYTES);
+      tma_load_2d(boxes + buf * BYTES, &m.res, &bars[buf], col(s), row0);
+    }
+  }
+
+  __device__ __forceinline__ void start(const GemmParams& p, const EpiMaps& m, int row, int column, int shared_first,
+                                        float (&bias)[4]) {
+    row0 = row, col0 = column, first = shared_first;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) bias[s] = box_bias(p, col(s));
+    if (p.tma_store && p.res && row0 < p.M) {
+      if ((threadIdx.x & 31) == 0) bulk_wait_group_read<0>();     // the last tile's boxes have left
+      fetch(p, m, 0, 0);
+      fetch(p, m, 1, 1);
+      if (!p.pre) {
+        fetch(p, m, 2, 2);
+        fetch(p, m, 3, 3);
+      }
+    }
+  }
+
+  __device__ __forceinline__ void box(const GemmParams& p, const CUtensorMap& d, const EpiMaps& m, int s, const uint32_t* v,
+                                      float alpha, float bias, volatile int* abort_flag) {
+    const int lane = threadIdx.x & 31;
+    const int c = col(s);
+    if (row0 >= p.M || c >= p.N) return;
+    const int buf = p.res && !p.pre ? s : s & 1, pre_buf = 2 + (s & 1);
+    float x[EPI_BOX];
+    box_values(v, alpha, bias, x);
+    if (!p.res) {
+      if (lane == 0) bulk_wait_group_read<1>();                   // the step before last has left its boxes
+      __syncwarp();
+    }
+    if (p.pre) box_put<__nv_bfloat16>(boxes + pre_buf * BYTES, lane, x);
+    act_values(x, p.act);
+    if (p.res) {
+      // a wait that gives up has set the abort flag: the sums are garbage and D is not used
+      (void)mbar_wait_bounded(&bars[buf], (parity >> buf) & 1u, abort_flag, p.wait_limit_ns, p.status);
+      parity ^= 1u << buf;
+      pending &= ~(1u << buf);
+      box_add<__nv_bfloat16>(boxes + buf * BYTES, lane, x);
+    }
+    box_put<__nv_bfloat16>(boxes + buf * BYTES, lane, x);
+    if (row0 + lane < p.M) {
+#pragma unroll
+      for (int i = 0; i < EPI_BOX / 2; ++i)
+        if (c + 2 * i < p.N)
+          asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(mag2) : "r"(pack_bf16x2(x[2 * i], x[2 * i + 1])));
+    }
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      if (p.pre) tma_store_2d(&m.pre, boxes + pre_buf * BYTES, c, row0);
+      tma_store_2d(&d, boxes + buf * BYTES, c, row0);
+      bulk_commit_group();
+    }
+    if (p.res && p.pre && s < 2) {
+      if (lane == 0) bulk_wait_group_read<0>();
+      fetch(p, m, s + 2, buf);
+    }
+  }
+
+  // Nothing may still land in or leave this warp's boxes when the block ends.
+  __device__ __forceinline__ void finish(const GemmParams& p) {
+    for (int b = 0; b < 4; ++b)
+      if (pending & (1u << b)) {
+        volatile int no_abort = 0;
+        (void)mbar_wait_bounded(&bars[b], (parity >> b) & 1u, &no_abort, p.wait_limit_ns, p.status);
+      }
+    if (p.tma_store && (threadIdx.x & 31) == 0) bulk_wait_group<0>();
+    mag = max(mag, max((mag2 & 0x7FFFu) << 16, mag2 & 0x7FFF0000u));
+  }
+};
+
 // kQ: the epilogue writes the quantized output (FP8 or NVFP4 under g_d)
 // instead of bf16 / fp32 D; a separate instantiation keeps the TMA-store
 // path's registers out of it.
@@ -771,8 +935,9 @@ template <bool kMx, bool kQ, bool kQA = false, bool kE = false>
 __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>::THREADS, 1)
     gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmSFA, const __grid_constant__ CUtensorMap tmSFB,
-                     const __grid_constant__ CUtensorMap tmD, const GemmParams p) {
-  using C = PairCfg<kMx>;
+                     const __grid_constant__ CUtensorMap tmD,
+                     const __grid_constant__ std::conditional_t<kE, EpiMaps, NoMaps> tmE, const GemmParams p) {
+  using C = PairCfg<kMx, kE>;
   using F = typename C::F;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
@@ -787,6 +952,7 @@ __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>:
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float2* qa_table = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(full) + 256);   // kQA only
   int* qa_start = reinterpret_cast<int*>(tmem_slot + 2);       // kQA: first ticket of this CTA's start-up batch
+  uint64_t* res_bar = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(full) + 256);       // kE: [warp][box]
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -806,6 +972,8 @@ __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>:
     mbar_init(&acc_empty[1], 2 * C::EPI_WARPS);
     mbar_init(ovl_free, 2 * 4);                // the 4 warps per CTA that hold the shared columns
     mbar_init(mma_done, 1);
+    if constexpr (kE)
+      for (int b = 0; b < C::EPI_WARPS * C::EPI_BOXES; ++b) mbar_init(&res_bar[b], 1);
     *abort_flag = 0;
     // One ticket batch for the CTA's first units (one per quantizer and
     // epilogue warp): one atomic per CTA instead of one per warp at the start.
@@ -1024,7 +1192,7 @@ __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>:
     }
     const float gd = kQ ? *p.g_d : 0.0f;
     float amax_run = 0.0f;
-    uint32_t mag = 0;
+    [[maybe_unused]] EpiWriter ep{epi_smem + ew * C::EPI_BOXES * C::EPI_BOX_BYTES, res_bar + ew * C::EPI_BOXES};
     const uint32_t acc_empty_leader = mapa_shared(smem_u32(acc_empty), 0);
     const uint32_t ovl_free_leader = mapa_shared(smem_u32(ovl_free), 0);
     int j = 0;
@@ -1037,16 +1205,44 @@ __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>:
         tm = t % tiles_m;
         tn = t / tiles_m;
       }
+      [[maybe_unused]] float bias[4];
+      if constexpr (kE) ep.start(p, tmE, tm * 256 + static_cast<int>(rank) * 128 + quad * 32, tn * C::BN + half * HALF,
+                                 b == 0 && half == 1 ? 64 : 0, bias);
       if (!mbar_wait_bounded(acc_full, static_cast<uint32_t>(j & 1), abort_flag, p.wait_limit_ns, p.status)) break;
       tc_fence_after();
       uint32_t v[HALF];
       const uint32_t taddr =
           tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + (b ? C::ACC1_COL : 0) + half * HALF;
-      if constexpr (kQA || kE) {
+      if constexpr (kE) {
+        // 64 columns at a time, the columns shared with the other accumulator first
+        const bool shared_cols = (b == 0 && half == 1) || (b == 1 && half == 0);
+        const int first = (b == 0 && half == 1) ? 64 : 0;
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {
+          const int c_off = part == 0 ? first : 64 - first;
+          uint32_t w[64];
+          tmem_ld_32x32b_x32(taddr + c_off, w);
+          tmem_ld_32x32b_x32(taddr + c_off + 32, w + 32);
+          tmem_ld_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (part == 0 && shared_cols) mbar_arrive_cluster_relaxed(ovl_free_leader);
+            if (part == 1) mbar_arrive_cluster_relaxed(acc_empty_leader + 8u * b);
+          }
+          if (p.tma_store) {
+            ep.box(p, tmD, tmE, 2 * part, w, alpha, part ? bias[2] : bias[0], abort_flag);
+            ep.box(p, tmD, tmE, 2 * part + 1, w + 32, alpha, part ? bias[3] : bias[1], abort_flag);
+          } else {
+            store_rows_epi<64>(p, ep.boxes, ep.row0, tn * C::BN + half * HALF + c_off, w, alpha, ep.mag);
+          }
+        }
+        continue;
+      }
+      if constexpr (kQA) {
         // 64 columns at a time (the quantizer warps take the registers a
-        // 128-column drain would hold; the epilogue's code stays half as
-        // long), the columns shared with the other accumulator first; bf16 or
-        // fp32 D, no quantized output.
+        // 128-column drain would hold), the columns shared with the other
+        // accumulator first; bf16 or fp32 D, no quantized output.
         const bool shared_cols = (b == 0 && half == 1) || (b == 1 && half == 0);
         const int first = (b == 0 && half == 1) ? 64 : 0;
         const int row0 = tm * 256 + static_cast<int>(rank) * 128 + quad * 32;
@@ -1064,9 +1260,7 @@ __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>:
             if (part == 1) mbar_arrive_cluster_relaxed(acc_empty_leader + 8u * b);
           }
           const int col0 = tn * C::BN + half * HALF + c_off;
-          if constexpr (kE) {
-            if (col0 < p.N) store_row_epi<64>(p, row0 + lane, col0, v, alpha, mag);
-          } else if (p.tma_store) {
+          if (p.tma_store) {
             if (row0 < p.M) {
 #pragma unroll
               for (int cc = 0; cc < 2; ++cc) {
@@ -1167,7 +1361,10 @@ __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>:
     }
     if (!kQ && !kE && p.tma_store && lane == 0) bulk_wait_group<0>();
     if constexpr (kQ) publish_amax(p, amax_run);
-    if constexpr (kE) publish_mag(p, mag);
+    if constexpr (kE) {
+      ep.finish(p);
+      publish_mag(p, ep.mag);
+    }
   } else if constexpr (kQA) {
     // ------------------- A quantizers (quantize-and-GEMM) -------------------
     // Units taken in ticket order (qa_unit maps a ticket to a row and a K
@@ -1288,16 +1485,13 @@ void set_quant_out(GemmParams& p, const QuantOut* q, int64_t N) {
 // Epilogue fields of the parameters (none when e is null).
 void set_epilogue(GemmParams& p, const Epilogue* e) {
   if (!e) return;
-  const int64_t size = p.out_f32 ? 4 : 2;
   p.bias = e->bias;
   p.bias_f32 = e->bias_f32;
   p.act = e->act;
   p.res = e->residual;
   p.ldr = e->ldr;
-  p.vec_res = aligned16(e->residual) && (e->ldr * size) % 16 == 0;
   p.pre = e->pre;
   p.ldp = e->ldp;
-  p.vec_pre = aligned16(e->pre) && (e->ldp * size) % 16 == 0;
   p.amax_d = e->amax_d;
 }
 
@@ -1327,9 +1521,17 @@ nvfp4_status run_gemm_pair(const void* a_codes, const void* a_sf, const float* g
   // 16-B chunks, so a row end inside a chunk would be overrun: such D takes
   // the direct-store path.
   const bool tma_store =
-      !(q && q->mode) && !epi && out == NVFP4_OUT_BF16 && aligned16(d) && (ldd * 2) % 16 == 0 && N % 8 == 0;
+      !(q && q->mode) && out == NVFP4_OUT_BF16 && aligned16(d) && (ldd * 2) % 16 == 0 && N % 8 == 0 &&
+      (!epi || ((!epi->residual || (aligned16(epi->residual) && epi->ldr % 8 == 0)) &&
+                (!epi->pre || (aligned16(epi->pre) && epi->ldp % 8 == 0))));
   memset(&tmD, 0, sizeof(tmD));
   if (tma_store && !make_out_map(&tmD, d, M, N, ldd)) return NVFP4_ERR_CUDA;
+  EpiMaps tmE;
+  memset(&tmE, 0, sizeof(tmE));
+  if (tma_store && epi) {
+    if (epi->residual && !make_out_map(&tmE.res, const_cast<void*>(epi->residual), M, N, epi->ldr)) return NVFP4_ERR_CUDA;
+    if (epi->pre && !make_out_map(&tmE.pre, epi->pre, M, N, epi->ldp)) return NVFP4_ERR_CUDA;
+  }
   GemmParams p{};
   p.sfa = static_cast<const uint8_t*>(a_sf);
   p.sfb = static_cast<const uint8_t*>(b_sf);
@@ -1352,12 +1554,12 @@ nvfp4_status run_gemm_pair(const void* a_codes, const void* a_sf, const float* g
   p.wait_limit_ns = wait_limit_ns();
   p.status = device_status_ptr();
   if (!p.status) return NVFP4_ERR_CUDA;
-  void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, GemmParams) =
+  void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, NoMaps, GemmParams) =
       gemm_pair_kernel<kMx, false>;
   int threads = C::THREADS, smem = C::SMEM_BYTES;
   if constexpr (!kMx) {
     if (p.out_q) kern = gemm_pair_kernel<false, true>;
-    if (epi) kern = gemm_pair_kernel<false, false, false, true>;
+    if (epi) smem = PairCfg<false, true>::SMEM_BYTES;
     if (qa) {
       if (p.out_q) return NVFP4_ERR_INVALID_ARG;
       kern = gemm_pair_kernel<false, false, true>;
@@ -1376,7 +1578,9 @@ nvfp4_status run_gemm_pair(const void* a_codes, const void* a_sf, const float* g
       p.qa_group = qa->group;
     }
   }
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  auto kern_epi = gemm_pair_kernel<false, false, false, true>;
+  const void* func = epi ? reinterpret_cast<const void*>(kern_epi) : reinterpret_cast<const void*>(kern);
+  cudaError_t e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return launch_status(e);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
@@ -1400,14 +1604,15 @@ nvfp4_status run_gemm_pair(const void* a_codes, const void* a_sf, const float* g
   if (dev >= 64 || *mp == 0) {
     cfg.gridDim = dim3(2 * (device_sm_count() / 2));
     int clusters = 0;
-    e = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&clusters, func, &cfg);
     if (e != cudaSuccess || clusters < 1) return launch_status(e != cudaSuccess ? e : cudaErrorInvalidConfiguration);
     *mp = clusters;
   }
   const int tiles = p.tiles_m * p.tiles_n;
   const int pairs = tiles < *mp ? tiles : *mp;
   cfg.gridDim = dim3(2 * pairs);
-  e = cudaLaunchKernelEx(&cfg, kern, tmA, tmB, tmSFA, tmSFB, tmD, p);
+  e = epi ? cudaLaunchKernelEx(&cfg, kern_epi, tmA, tmB, tmSFA, tmSFB, tmD, tmE, p)
+          : cudaLaunchKernelEx(&cfg, kern, tmA, tmB, tmSFA, tmSFB, tmD, NoMaps{}, p);
   return launch_status(e);
 }
 
@@ -1415,7 +1620,6 @@ template <int BN, bool kMx>
 nvfp4_status run_gemm(const void* a_codes, const void* a_sf, const float* g_a, const void* b_codes,
                       const void* b_sf, const float* g_b, int64_t M, int64_t N, int64_t K, void* d, int64_t ldd,
                       nvfp4_out_dtype out, const QuantOut* q, cudaStream_t s, const Epilogue* epi) {
-  using C = GemmCfg<BN, kMx>;
   CUtensorMap tmA, tmB;
   if (!make_code_map(&tmA, a_codes, M, K, BM) || !make_code_map(&tmB, b_codes, N, K, BN)) return NVFP4_ERR_CUDA;
   GemmParams p{};
@@ -1428,7 +1632,7 @@ nvfp4_status run_gemm(const void* a_codes, const void* a_sf, const float* g_a, c
   p.M = static_cast<int>(M);
   p.N = static_cast<int>(N);
   p.K = static_cast<int>(K);
-  p.kb4 = static_cast<int>(K / C::F::K_PER_ATOM);
+  p.kb4 = static_cast<int>(K / ScaleFmt<kMx>::K_PER_ATOM);
   p.tiles_m = static_cast<int>((M + BM - 1) / BM);
   p.tiles_n = static_cast<int>((N + BN - 1) / BN);
   p.out_f32 = out == NVFP4_OUT_F32;
@@ -1440,14 +1644,18 @@ nvfp4_status run_gemm(const void* a_codes, const void* a_sf, const float* g_a, c
   p.status = device_status_ptr();
   if (!p.status) return NVFP4_ERR_CUDA;
   auto kern = gemm_kernel<BN, kMx, false>;
+  int smem = GemmCfg<BN, kMx>::SMEM_BYTES;
   if constexpr (!kMx) {
-    if (epi) kern = gemm_kernel<BN, false, true>;
+    if (epi) {
+      kern = gemm_kernel<BN, false, true>;
+      smem = GemmCfg<BN, false, true>::SMEM_BYTES;
+    }
   }
   const int tiles = p.tiles_m * p.tiles_n;
   const int grid = tiles < device_sm_count() ? tiles : device_sm_count();
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return launch_status(e);
-  kern<<<grid, C::THREADS, C::SMEM_BYTES, s>>>(tmA, tmB, p);
+  kern<<<grid, GemmCfg<BN, kMx>::THREADS, smem, s>>>(tmA, tmB, p);
   return launch_status(cudaGetLastError());
 }
 
