@@ -944,8 +944,12 @@ __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>:
   uint8_t* epi_smem = smem + C::STAGES * C::STAGE_BYTES;
   uint64_t* full = reinterpret_cast<uint64_t*>(epi_smem + C::EPI_BYTES);
   uint64_t* empty = full + C::STAGES;
-  uint64_t* acc_full = empty + C::STAGES;      // MMA -> epilogue, one phase per tile
-  uint64_t* acc_empty = acc_full + 1;          // [2] accumulator b fully drained
+  // MMA -> epilogue, one barrier per accumulator: the MMAs into accumulator b
+  // start once every epilogue warp has drained its previous tile, so no warp is
+  // ever two phases behind.  (One barrier for both would alias: the warps that
+  // do not hold the shared columns may lag a tile while the next one completes.)
+  uint64_t* acc_full = empty + C::STAGES;
+  uint64_t* acc_empty = acc_full + 2;          // [2] accumulator b fully drained
   uint64_t* ovl_free = acc_empty + 2;          // shared columns drained, one phase per tile
   uint64_t* mma_done = ovl_free + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
@@ -967,7 +971,8 @@ __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>:
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    mbar_init(acc_full, 1);
+    mbar_init(&acc_full[0], 1);
+    mbar_init(&acc_full[1], 1);
     mbar_init(&acc_empty[0], 2 * C::EPI_WARPS);
     mbar_init(&acc_empty[1], 2 * C::EPI_WARPS);
     mbar_init(ovl_free, 2 * 4);                // the 4 warps per CTA that hold the shared columns
@@ -1153,7 +1158,7 @@ __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>:
           }
         }
         if (!ok) break;
-        tc_commit_pair_mc(acc_full, 0x3);
+        tc_commit_pair_mc(&acc_full[b], 0x3);
       }
       tc_commit_pair_mc(mma_done, 0x1);
       volatile int no_abort = 0;
@@ -1208,7 +1213,7 @@ __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>:
       [[maybe_unused]] float bias[4];
       if constexpr (kE) ep.start(p, tmE, tm * 256 + static_cast<int>(rank) * 128 + quad * 32, tn * C::BN + half * HALF,
                                  b == 0 && half == 1 ? 64 : 0, bias);
-      if (!mbar_wait_bounded(acc_full, static_cast<uint32_t>(j & 1), abort_flag, p.wait_limit_ns, p.status)) break;
+      if (!mbar_wait_bounded(&acc_full[b], static_cast<uint32_t>(j >> 1) & 1u, abort_flag, p.wait_limit_ns, p.status)) break;
       tc_fence_after();
       uint32_t v[HALF];
       const uint32_t taddr =

@@ -101,6 +101,25 @@ def test_gemm_many_tiles_per_block(lib):
     R.check(pre, *ref["pre"], "pre")
 
 
+@pytest.mark.parametrize("n,k,res,pre", [(4352, 64, False, False), (4352, 1024, True, False), (4352, 64, True, False), (4352, 64, True, True),
+                                         (4354, 64, True, False)], ids=str)
+def test_gemm_epilogue_slower_than_the_product(lib, n, k, res, pre):
+    """Short K and several tiles per CTA pair: the products run ahead of the epilogue warps, which then differ in how far
+    they are (the warps of one half release the shared columns and go on, those of the other may be a tile behind)."""
+    m = 2304
+    a, w, _, (d_ref, s_ref, alpha) = product(lib, m, n, k)
+    bias = randn(1, n).bfloat16().cuda()
+    r = randn(2, m, n).bfloat16().cuda() if res else None
+    p = torch.empty(m, n, dtype=BF16, device="cuda") if pre else None
+    for _ in range(3):
+        d = lib.gemm_epilogue(a, w, bias, "gelu", r, pre=p if pre else False)
+    assert lib.nvfp4_check_device_status() == lib.OK
+    ref = R.epilogue(d_ref, s_ref, alpha, bias, "gelu", r)
+    R.check(d, *ref["d"], "d")
+    if pre:
+        R.check(p, *ref["pre"], "pre")
+
+
 def test_gemm_nonfinite_bias_and_residual(lib):
     a, w, _, _ = product(lib, 300, 520, 1088)
     bias = torch.zeros(520, device="cuda")
