@@ -16,11 +16,58 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "nvfp4.h"
 
 namespace nvfp4 {
 
+// Two fp32 lanes per instruction (add / mul / fma.rn.f32x2): these kernels are
+// bound by instruction issue as much as by memory.
+__device__ __forceinline__ unsigned long long bits2(float2 a) { return *reinterpret_cast<unsigned long long*>(&a); }
+__device__ __forceinline__ float2 pair2(unsigned long long b) { return *reinterpret_cast<float2*>(&b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return pair2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return pair2(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return pair2(r);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// 2^x and 1 / x to 2 ulps (results below 2^-126 are 0), and the minimum and
+// maximum that keep a NaN.
+__device__ __forceinline__ float2 exp2_2(float2 x) {
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x.x));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x.y));
+  return x;
+}
+__device__ __forceinline__ float2 rcp2(float2 x) {
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x.x));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x.y));
+  return x;
+}
+__device__ __forceinline__ float2 min2(float2 x, float c) {
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(x.x) : "f"(c));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(x.y) : "f"(c));
+  return x;
+}
+__device__ __forceinline__ float2 max2(float2 x, float c) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.x) : "f"(c));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.y) : "f"(c));
+  return x;
+}
+__device__ __forceinline__ float2 abs2(float2 x) { return make_float2(fabsf(x.x), fabsf(x.y)); }
+
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGeluC2 = 1.5957691216057308f;      // 2 sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
@@ -28,93 +75,118 @@ constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 // g = erfc(a / sqrt 2) / 2 = e^{-a^2 / 2} t Q(t) / 2, t = 1 / (1 + 0.425 a /
 // sqrt 2), for a >= 0; also e = e^{-a^2 / 2}.  Q: polynomial of degree 7 fitted
 // to e^{x^2} erfc(x) / t for 0 <= x <= 9.3 with the least largest relative
-// error (1.1e-7; 4e-7 with its evaluation in fp32): a GEMM with this gelu at
-// K = 1024, where its epilogue is what takes the time, runs 2.1 times as fast as
-// with erfcf (78 against 162 us, 4096 x 8192).  Past a = 16, e is 0.
-__device__ __forceinline__ float normal_tail(float a, float& e) {
-  const float t = __fdividef(1.0f, fmaf(0.3005203820f, a, 1.0f));
-  float q = 0.0724736005f;
-  q = fmaf(q, t, -0.3173076808f);
-  q = fmaf(q, t, 0.4147784114f);
-  q = fmaf(q, t, -0.1098528951f);
-  q = fmaf(q, t, 0.2585873306f);
-  q = fmaf(q, t, 0.1996419132f);
-  q = fmaf(q, t, 0.2420118004f);
-  q = fmaf(q, t, 0.2396674007f);
-  e = __expf(-0.5f * a * a);
-  return 0.5f * e * (t * q);
+// error (1.1e-7; 4e-7 with its evaluation in fp32), the half taken into its
+// coefficients: a GEMM with this gelu at K = 1024, where its epilogue is what
+// takes the time, ran 2.1 times as fast as with erfcf (78 against 162 us, 4096
+// x 8192).  Past a = 16, e is 0.
+__device__ __forceinline__ float2 normal_tail2(float2 a, float2& e) {
+  const float2 t = rcp2(fma2(both(0.3005203820f), a, both(1.0f)));
+  float2 q = both(0.5f * 0.0724736005f);
+  q = fma2(q, t, both(0.5f * -0.3173076808f));
+  q = fma2(q, t, both(0.5f * 0.4147784114f));
+  q = fma2(q, t, both(0.5f * -0.1098528951f));
+  q = fma2(q, t, both(0.5f * 0.2585873306f));
+  q = fma2(q, t, both(0.5f * 0.1996419132f));
+  q = fma2(q, t, both(0.5f * 0.2420118004f));
+  q = fma2(q, t, both(0.5f * 0.2396674007f));
+  e = exp2_2(mul2(mul2(a, both(-0.5f * kLog2e)), a));
+  return mul2(e, mul2(t, q));
+}
+
+// act(v) of two values.  A NaN stays one; an infinite v gives the limit where
+// that is finite or v, except silu and gelu_tanh at -infinity (NaN, as
+// v / (1 + e^{-v}) has there).
+template <int kAct>
+__device__ __forceinline__ float2 act_pair(float2 v) {
+  if constexpr (kAct == NVFP4_ACT_RELU) {
+    return max2(v, 0.0f);
+  } else if constexpr (kAct == NVFP4_ACT_GELU) {
+    float2 e;
+    const float2 a = min2(abs2(v), 16.0f);
+    return fma2(both(-1.0f), mul2(a, normal_tail2(a, e)), max2(v, 0.0f));
+  } else if constexpr (kAct == NVFP4_ACT_GELU_TANH) {
+    const float2 m = mul2(v, both(-kGeluC2 * kLog2e));
+    const float2 w = fma2(mul2(v, both(kGeluA)), v, both(1.0f));
+    return mul2(v, rcp2(add2(exp2_2(mul2(m, w)), both(1.0f))));
+  } else if constexpr (kAct == NVFP4_ACT_SILU) {
+    return mul2(v, rcp2(add2(exp2_2(mul2(v, both(-kLog2e))), both(1.0f))));
+  } else {
+    return v;
+  }
+}
+
+// act'(v) of two values.  The logistic forms are written on e = e^{-|.|} <= 1,
+// so neither p (1 - p) nor the tails cancel or overflow, and on v held to the
+// range outside which act' is 0 or 1 to the last bit (|v| <= 16, silu 128), so
+// an infinite v gives the limit; a NaN stays one.
+template <int kAct>
+__device__ __forceinline__ float2 slope_pair(float2 v) {
+  if constexpr (kAct == NVFP4_ACT_RELU) {
+    const auto one = [](float x) { return x > 0.0f ? 1.0f : (x <= 0.0f ? 0.0f : x); };
+    return make_float2(one(v.x), one(v.y));
+  } else if constexpr (kAct == NVFP4_ACT_GELU) {
+    float2 e;
+    v = max2(min2(v, 16.0f), -16.0f);
+    const float2 g = normal_tail2(abs2(v), e);
+    const float2 p = make_float2(v.x < 0.0f ? g.x : 1.0f - g.x, v.y < 0.0f ? g.y : 1.0f - g.y);
+    return fma2(mul2(e, both(kInvSqrt2Pi)), v, p);
+  } else if constexpr (kAct == NVFP4_ACT_GELU_TANH || kAct == NVFP4_ACT_SILU) {
+    constexpr bool kGelu = kAct == NVFP4_ACT_GELU_TANH;
+    v = max2(min2(v, kGelu ? 16.0f : 128.0f), kGelu ? -16.0f : -128.0f);
+    // logistic argument u = w v, slope p + v u'(v) p (1 - p)
+    float2 u = v, du = v;                       // u, v u'(v)
+    if constexpr (kGelu) {
+      const float2 v2 = mul2(v, v), m = mul2(v, both(kGeluC2));
+      u = mul2(m, fma2(v2, both(kGeluA), both(1.0f)));
+      du = mul2(m, fma2(v2, both(3.0f * kGeluA), both(1.0f)));
+    }
+    const float2 e = exp2_2(mul2(abs2(u), both(-kLog2e)));
+    const float2 r = rcp2(add2(e, both(1.0f))), q = mul2(e, r);
+    const float2 p = make_float2(v.x < 0.0f ? q.x : r.x, v.y < 0.0f ? q.y : r.y);
+    return fma2(du, mul2(q, r), p);
+  } else {
+    return both(1.0f);
+  }
+}
+
+// Calls f with the activation as a compile-time constant.
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
+  switch (act) {
+    case NVFP4_ACT_RELU: f(std::integral_constant<int, NVFP4_ACT_RELU>{}); break;
+    case NVFP4_ACT_GELU: f(std::integral_constant<int, NVFP4_ACT_GELU>{}); break;
+    case NVFP4_ACT_GELU_TANH: f(std::integral_constant<int, NVFP4_ACT_GELU_TANH>{}); break;
+    case NVFP4_ACT_SILU: f(std::integral_constant<int, NVFP4_ACT_SILU>{}); break;
+    default: f(std::integral_constant<int, NVFP4_ACT_NONE>{}); break;
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void act_values(float2 (&x)[N], int act) {
+  with_act(act, [&](auto a) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = act_pair<decltype(a)::value>(x[i]);
+  });
 }
 
 __device__ __forceinline__ float act_value(float v, int act) {
-  switch (act) {
-    case NVFP4_ACT_RELU: return v < 0.0f ? 0.0f : v;
-    case NVFP4_ACT_GELU: {
-      float e;
-      const float a = fminf(fabsf(v), 16.0f);
-      return (v < 0.0f ? 0.0f : v) - a * normal_tail(a, e);          // a NaN stays one
-    }
-    case NVFP4_ACT_GELU_TANH: return __fdividef(v, 1.0f + __expf(-kGeluC2 * v * fmaf(kGeluA * v, v, 1.0f)));
-    case NVFP4_ACT_SILU: return __fdividef(v, 1.0f + __expf(-v));
-    default: return v;
-  }
+  float2 x[1] = {both(v)};
+  act_values(x, act);
+  return x[0].x;
 }
 
-// The same for an array, with one branch on the activation.
-template <int N>
-__device__ __forceinline__ void act_values(float (&x)[N], int act) {
-  switch (act) {
-    case NVFP4_ACT_RELU:
-#pragma unroll
-      for (int i = 0; i < N; ++i) x[i] = act_value(x[i], NVFP4_ACT_RELU);
-      break;
-    case NVFP4_ACT_GELU:
-#pragma unroll
-      for (int i = 0; i < N; ++i) x[i] = act_value(x[i], NVFP4_ACT_GELU);
-      break;
-    case NVFP4_ACT_GELU_TANH:
-#pragma unroll
-      for (int i = 0; i < N; ++i) x[i] = act_value(x[i], NVFP4_ACT_GELU_TANH);
-      break;
-    case NVFP4_ACT_SILU:
-#pragma unroll
-      for (int i = 0; i < N; ++i) x[i] = act_value(x[i], NVFP4_ACT_SILU);
-      break;
-    default: break;
-  }
-}
+// A chunk: 8 elements as 4 pairs.
+struct Chunk {
+  float2 v[4];
+  __device__ __forceinline__ float get(int e) const { return e & 1 ? v[e >> 1].y : v[e >> 1].x; }
+};
 
-// act'(v).  The logistic forms are written on e = e^{-|.|} <= 1, so neither
-// p (1 - p) nor the tails cancel or overflow; past |v| = 16 (gelu) or 128
-// (silu) the second term is below the smallest normal number and left out, so
-// an infinite v gives the limit (0 or 1) instead of inf * 0.
-__device__ __forceinline__ float act_slope(float v, int act) {
-  switch (act) {
-    case NVFP4_ACT_RELU: return v > 0.0f ? 1.0f : (v <= 0.0f ? 0.0f : v);
-    case NVFP4_ACT_GELU: {
-      float e;
-      const float a = fminf(fabsf(v), 16.0f);
-      const float g = normal_tail(a, e);
-      const float p = v < 0.0f ? g : 1.0f - g;
-      return v == v ? fmaf(kInvSqrt2Pi * e, copysignf(a, v), p) : v;
-    }
-    case NVFP4_ACT_GELU_TANH: {
-      const float v2 = v * v;
-      const float u2 = kGeluC2 * v * fmaf(kGeluA, v2, 1.0f);
-      const float e = __expf(-fabsf(u2));
-      const float r = __fdividef(1.0f, 1.0f + e);
-      const float q = e * r;
-      const float p = v < 0.0f ? q : r;
-      return fabsf(v) < 16.0f ? fmaf(kGeluC2 * v * (q * r), fmaf(3.0f * kGeluA, v2, 1.0f), p) : (v == v ? p : v);
-    }
-    case NVFP4_ACT_SILU: {
-      const float e = __expf(-fabsf(v));
-      const float r = __fdividef(1.0f, 1.0f + e);
-      const float q = e * r;
-      const float p = v < 0.0f ? q : r;
-      return fabsf(v) < 128.0f ? fmaf(v, q * r, p) : (v == v ? p : v);
-    }
-    default: return 1.0f;
-  }
+__device__ __forceinline__ Chunk unpack_chunk(const uint4 w) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  Chunk c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c.v[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
+  return c;
 }
 
 // Typed element access (T: __nv_bfloat16 or float).
@@ -138,6 +210,46 @@ __device__ __forceinline__ uint32_t mag_bits(__nv_bfloat16 v) {
 __device__ __forceinline__ float load_param(const void* p, int f32, int64_t i) {
   return f32 ? __ldg(static_cast<const float*>(p) + i)
              : __bfloat162float(__ushort_as_bfloat16(__ldg(static_cast<const unsigned short*>(p) + i)));
+}
+
+// Stores a chunk rounded to T (unless out is null) and takes it into the running maximum of stored
+// magnitudes (Mag: both halves of a word for bf16, where one instruction takes
+// the larger magnitudes of two pairs and keeps a NaN).
+template <typename T>
+struct Mag {
+  uint32_t m = 0;
+  __device__ __forceinline__ void pair(uint32_t u) {
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(u));
+  }
+  __device__ __forceinline__ uint32_t bits() const {
+    return max((m & 0x7FFFu) << 16, m & 0x7FFF0000u);
+  }
+};
+template <>
+struct Mag<float> {
+  uint32_t m = 0;
+  __device__ __forceinline__ uint32_t bits() const { return m; }
+};
+
+template <typename T>
+__device__ __forceinline__ void store_chunk(T* out, const Chunk& x, Mag<T>& mag) {
+  if constexpr (sizeof(T) == 2) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x.v[i].x, x.v[i].y);
+      u[i] = *reinterpret_cast<const uint32_t*>(&h);
+      mag.pair(u[i]);
+    }
+    if (out) *reinterpret_cast<uint4*>(out) = make_uint4(u[0], u[1], u[2], u[3]);
+  } else {
+    if (out) {
+      *reinterpret_cast<float4*>(out) = make_float4(x.v[0].x, x.v[0].y, x.v[1].x, x.v[1].y);
+      *reinterpret_cast<float4*>(out + 4) = make_float4(x.v[2].x, x.v[2].y, x.v[3].x, x.v[3].y);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) mag.m = max(mag.m, mag_bits(x.get(e)));
+  }
 }
 
 }  // namespace nvfp4

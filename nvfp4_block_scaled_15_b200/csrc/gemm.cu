@@ -311,37 +311,34 @@ __device__ __forceinline__ int box_chunk(int row, int q) {
   return sizeof(T) == 2 ? row * 64 + ((q ^ ((row >> 1) & 3)) << 4) : row * 128 + ((q ^ (row & 7)) << 4);
 }
 
-// This thread's row of a box from / to registers.
+// This thread's row of a box, 16 pairs, from / to registers.
+using BoxRow = float2[EPI_BOX / 2];
 template <typename T>
-__device__ __forceinline__ void box_put(uint8_t* box, int row, const float (&x)[EPI_BOX]) {
-  constexpr int PER = 16 / sizeof(T);
+__device__ __forceinline__ void box_put(uint8_t* box, int row, const BoxRow& x) {
 #pragma unroll
-  for (int q = 0; q < EPI_BOX / PER; ++q) {
+  for (int q = 0; q < EPI_BOX * static_cast<int>(sizeof(T)) / 16; ++q) {
     uint4 w;
     if constexpr (sizeof(T) == 2)
-      w = make_uint4(pack_bf16x2(x[8 * q], x[8 * q + 1]), pack_bf16x2(x[8 * q + 2], x[8 * q + 3]),
-                     pack_bf16x2(x[8 * q + 4], x[8 * q + 5]), pack_bf16x2(x[8 * q + 6], x[8 * q + 7]));
+      w = make_uint4(pack_bf16x2(x[4 * q].x, x[4 * q].y), pack_bf16x2(x[4 * q + 1].x, x[4 * q + 1].y),
+                     pack_bf16x2(x[4 * q + 2].x, x[4 * q + 2].y), pack_bf16x2(x[4 * q + 3].x, x[4 * q + 3].y));
     else
-      w = make_uint4(__float_as_uint(x[4 * q]), __float_as_uint(x[4 * q + 1]), __float_as_uint(x[4 * q + 2]),
-                     __float_as_uint(x[4 * q + 3]));
+      w = make_uint4(__float_as_uint(x[2 * q].x), __float_as_uint(x[2 * q].y), __float_as_uint(x[2 * q + 1].x),
+                     __float_as_uint(x[2 * q + 1].y));
     *reinterpret_cast<uint4*>(box + box_chunk<T>(row, q)) = w;
   }
 }
 template <typename T>
-__device__ __forceinline__ void box_add(const uint8_t* box, int row, float (&x)[EPI_BOX]) {
-  constexpr int PER = 16 / sizeof(T);
+__device__ __forceinline__ void box_add(const uint8_t* box, int row, BoxRow& x) {
 #pragma unroll
-  for (int q = 0; q < EPI_BOX / PER; ++q) {
+  for (int q = 0; q < EPI_BOX * static_cast<int>(sizeof(T)) / 16; ++q) {
     const uint4 w = *reinterpret_cast<const uint4*>(box + box_chunk<T>(row, q));
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    if constexpr (sizeof(T) == 2) {
+      const Chunk c = unpack_chunk(w);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (sizeof(T) == 2) {
-        x[8 * q + 2 * i] += __uint_as_float(u[i] << 16);
-        x[8 * q + 2 * i + 1] += __uint_as_float(u[i] & 0xFFFF0000u);
-      } else {
-        x[4 * q + i] += __uint_as_float(u[i]);
-      }
+      for (int i = 0; i < 4; ++i) x[4 * q + i] = add2(x[4 * q + i], c.v[i]);
+    } else {
+      x[2 * q] = add2(x[2 * q], make_float2(__uint_as_float(w.x), __uint_as_float(w.y)));
+      x[2 * q + 1] = add2(x[2 * q + 1], make_float2(__uint_as_float(w.z), __uint_as_float(w.w)));
     }
   }
 }
@@ -371,9 +368,16 @@ __device__ __forceinline__ void box_rows_in(uint8_t* box, const void* base, int6
 }
 
 // x = alpha acc + bias of a box; lane l holds the bias of column col + l.
-__device__ __forceinline__ void box_values(const uint32_t* v, float alpha, float bias, float (&x)[EPI_BOX]) {
+__device__ __forceinline__ void box_values(const uint32_t* v, float alpha, bool has_bias, float bias, BoxRow& x) {
 #pragma unroll
-  for (int i = 0; i < EPI_BOX; ++i) x[i] = fmaf(__uint_as_float(v[i]), alpha, __shfl_sync(0xFFFFFFFFu, bias, i));
+  for (int i = 0; i < EPI_BOX / 2; ++i) {
+    x[i] = make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+    if (has_bias)
+      x[i] = fma2(x[i], both(alpha),
+                  make_float2(__shfl_sync(0xFFFFFFFFu, bias, 2 * i), __shfl_sync(0xFFFFFFFFu, bias, 2 * i + 1)));
+    else
+      x[i] = mul2(x[i], both(alpha));
+  }
 }
 __device__ __forceinline__ float box_bias(const GemmParams& p, int col) {
   const int c = col + static_cast<int>(threadIdx.x & 31);
@@ -382,10 +386,10 @@ __device__ __forceinline__ float box_bias(const GemmParams& p, int col) {
 
 // Largest stored magnitude of this thread's row, columns below n_valid.
 template <typename T>
-__device__ __forceinline__ void box_mag(const float (&x)[EPI_BOX], int n_valid, uint32_t& mag) {
+__device__ __forceinline__ void box_mag(const BoxRow& x, int n_valid, uint32_t& mag) {
 #pragma unroll
   for (int i = 0; i < EPI_BOX; ++i)
-    if (i < n_valid) mag = max(mag, mag_bits(from_f32<T>(x[i])));
+    if (i < n_valid) mag = max(mag, mag_bits(from_f32<T>(i & 1 ? x[i / 2].y : x[i / 2].x)));
 }
 
 // One box of any type and alignment; `box`: EPI_ROWS_BYTES of this warp.
@@ -395,8 +399,8 @@ __device__ __forceinline__ void store_box_rows(const GemmParams& p, uint8_t* box
   const int lane = threadIdx.x & 31;
   const int rows = min(EPI_BOX, p.M - row0);
   const bool in = col + lane < p.N;
-  float x[EPI_BOX];
-  box_values(v, alpha, bias, x);
+  BoxRow x;
+  box_values(v, alpha, p.bias != nullptr, bias, x);
   if (p.pre) {
     box_put<T>(box, lane, x);
     __syncwarp();
@@ -837,8 +841,8 @@ struct NoMaps {};
 struct EpiWriter {
   uint8_t* boxes;
   uint64_t* bars;            // arrivals of residual boxes
-  uint32_t mag = 0;          // |D|, fp32 bits
-  uint32_t mag2 = 0;         // |D|, two bf16
+  Mag<__nv_bfloat16> mag;    // |D| of box()
+  uint32_t mag_rows = 0;     // |D| of store_rows_epi()
   uint32_t parity = 0;       // of bars[0..3]
   uint32_t pending = 0;      // residual boxes fetched and not waited for
   int row0 = 0, col0 = 0, first = 0;
@@ -878,8 +882,8 @@ struct EpiWriter {
     const int c = col(s);
     if (row0 >= p.M || c >= p.N) return;
     const int buf = p.res && !p.pre ? s : s & 1, pre_buf = 2 + (s & 1);
-    float x[EPI_BOX];
-    box_values(v, alpha, bias, x);
+    BoxRow x;
+    box_values(v, alpha, p.bias != nullptr, bias, x);
     if (!p.res) {
       if (lane == 0) bulk_wait_group_read<1>();                   // the step before last has left its boxes
       __syncwarp();
@@ -894,11 +898,13 @@ struct EpiWriter {
       box_add<__nv_bfloat16>(boxes + buf * BYTES, lane, x);
     }
     box_put<__nv_bfloat16>(boxes + buf * BYTES, lane, x);
-    if (row0 + lane < p.M) {
+    if (p.amax_d && row0 + lane < p.M) {
 #pragma unroll
-      for (int i = 0; i < EPI_BOX / 2; ++i)
-        if (c + 2 * i < p.N)
-          asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(mag2) : "r"(pack_bf16x2(x[2 * i], x[2 * i + 1])));
+      for (int q = 0; q < EPI_BOX / 8; ++q)
+        if (c + 8 * q < p.N) {                                    // N is a multiple of 8 here
+#pragma unroll
+          for (int i = 4 * q; i < 4 * q + 4; ++i) mag.pair(pack_bf16x2(x[i].x, x[i].y));
+        }
     }
     fence_proxy_async_shared();
     __syncwarp();
@@ -921,7 +927,6 @@ struct EpiWriter {
         (void)mbar_wait_bounded(&bars[b], (parity >> b) & 1u, &no_abort, p.wait_limit_ns, p.status);
       }
     if (p.tma_store && (threadIdx.x & 31) == 0) bulk_wait_group<0>();
-    mag = max(mag, max((mag2 & 0x7FFFu) << 16, mag2 & 0x7FFF0000u));
   }
 };
 
@@ -1239,7 +1244,7 @@ __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>:
             ep.box(p, tmD, tmE, 2 * part, w, alpha, part ? bias[2] : bias[0], abort_flag);
             ep.box(p, tmD, tmE, 2 * part + 1, w + 32, alpha, part ? bias[3] : bias[1], abort_flag);
           } else {
-            store_rows_epi<64>(p, ep.boxes, ep.row0, tn * C::BN + half * HALF + c_off, w, alpha, ep.mag);
+            store_rows_epi<64>(p, ep.boxes, ep.row0, tn * C::BN + half * HALF + c_off, w, alpha, ep.mag_rows);
           }
         }
         continue;
@@ -1368,7 +1373,7 @@ __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>:
     if constexpr (kQ) publish_amax(p, amax_run);
     if constexpr (kE) {
       ep.finish(p);
-      publish_mag(p, ep.mag);
+      publish_mag(p, max(ep.mag_rows, ep.mag.bits()));
     }
   } else if constexpr (kQA) {
     // ------------------- A quantizers (quantize-and-GEMM) -------------------

@@ -162,10 +162,10 @@ nvfp4_status launch_epilogue_backward(const EpilogueBackward& a, cudaStream_t s)
 size_t epilogue_backward_workspace_bytes(int64_t M, int64_t N);
 // Joins the blocks' partials [blocks][stride] of an earlier kernel on the
 // stream: the sums of the first n0 columns to out0, of the next n1 to out1
-// (either may be null), and max over mags[blocks] (fp32 bits) to *amax (may be
+// (either may be null), and max over mags[n_mags] (fp32 bits) to *amax (may be
 // null).
 cudaError_t launch_sum_partials(const float* partial, int blocks, int64_t stride, int n0, int n1, float* out0, float* out1,
-                                const uint32_t* mags, float* amax, cudaStream_t s);
+                                const uint32_t* mags, int n_mags, float* amax, cudaStream_t s);
 // Per-launch 48-bit tag of workspace counters (never 0).
 unsigned long long next_launch_tag();
 

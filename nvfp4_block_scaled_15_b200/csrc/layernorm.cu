@@ -190,41 +190,6 @@ __global__ void __launch_bounds__(LN_THREADS) ln_backward_params_long_kernel(con
 // path's bounds in registers.)
 __device__ __forceinline__ int chunk_col(int t, int nt, int j) { return 8 * (t + nt * j); }
 
-// Two fp32 lanes per instruction (add / mul / fma.rn.f32x2): the one-pass
-// kernels are bound by instruction issue as much as by memory.
-__device__ __forceinline__ unsigned long long bits2(float2 a) { return *reinterpret_cast<unsigned long long*>(&a); }
-__device__ __forceinline__ float2 pair2(unsigned long long b) { return *reinterpret_cast<float2*>(&b); }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  unsigned long long r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
-  return pair2(r);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  unsigned long long r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
-  return pair2(r);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  unsigned long long r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
-  return pair2(r);
-}
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
-
-// A chunk: 8 elements as 4 pairs.
-struct Chunk {
-  float2 v[4];
-  __device__ __forceinline__ float get(int e) const { return e & 1 ? v[e >> 1].y : v[e >> 1].x; }
-};
-
-__device__ __forceinline__ Chunk unpack_chunk(const uint4 w) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-  Chunk c;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) c.v[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
-  return c;
-}
-
 // Columns c .. c+7 of gamma or beta (cached: every row reads them).
 template <typename TP>
 __device__ __forceinline__ Chunk load_param_chunk(const void* p, int c, int k, float dflt) {
@@ -241,44 +206,6 @@ __device__ __forceinline__ Chunk load_param_chunk(const void* p, int c, int k, f
     x = unpack_chunk(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + c)));
   }
   return x;
-}
-
-// Stores a chunk rounded to T and takes it into the running maximum of stored
-// magnitudes (Mag: both halves of a word for bf16, where one instruction takes
-// the larger magnitudes of two pairs and keeps a NaN).
-template <typename T>
-struct Mag {
-  uint32_t m = 0;
-  __device__ __forceinline__ void pair(uint32_t u) {
-    asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(u));
-  }
-  __device__ __forceinline__ uint32_t bits() const {
-    return max((m & 0x7FFFu) << 16, m & 0x7FFF0000u);
-  }
-};
-template <>
-struct Mag<float> {
-  uint32_t m = 0;
-  __device__ __forceinline__ uint32_t bits() const { return m; }
-};
-
-template <typename T>
-__device__ __forceinline__ void store_chunk(T* out, const Chunk& x, Mag<T>& mag) {
-  if constexpr (sizeof(T) == 2) {
-    uint32_t u[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(x.v[i].x, x.v[i].y);
-      u[i] = *reinterpret_cast<const uint32_t*>(&h);
-      mag.pair(u[i]);
-    }
-    *reinterpret_cast<uint4*>(out) = make_uint4(u[0], u[1], u[2], u[3]);
-  } else {
-    *reinterpret_cast<float4*>(out) = make_float4(x.v[0].x, x.v[0].y, x.v[1].x, x.v[1].y);
-    *reinterpret_cast<float4*>(out + 4) = make_float4(x.v[2].x, x.v[2].y, x.v[3].x, x.v[3].y);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) mag.m = max(mag.m, mag_bits(x.get(e)));
-  }
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -879,7 +806,8 @@ __global__ void __launch_bounds__(LO_THREADS, 1) ln_backward_odd_kernel(const Ln
 // amax.  A block of 8 warps takes 32 columns; warp w sums the partials w, w +
 // 8, ..., and the warps' sums are added in order.
 __global__ void __launch_bounds__(256) sum_partials_kernel(const float* partial, int blocks, int64_t stride, int n0, int n1,
-                                                           float* out0, float* out1, const uint32_t* mags, float* amax) {
+                                                           float* out0, float* out1, const uint32_t* mags, int n_mags,
+                                                           float* amax) {
   __shared__ float part[8][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");      // launched as a programmatic dependent of the rows' kernel
@@ -902,7 +830,7 @@ __global__ void __launch_bounds__(256) sum_partials_kernel(const float* partial,
   }
   if (blockIdx.x == 0 && warp == 1 && amax) {
     uint32_t m = 0;
-    for (int b = lane; b < blocks; b += 32) m = max(m, __ldcg(mags + b));
+    for (int b = lane; b < n_mags; b += 32) m = max(m, __ldcg(mags + b));
     m = __reduce_max_sync(0xFFFFFFFFu, m);
     if (lane == 0) *amax = __uint_as_float(m);
   }
@@ -985,7 +913,7 @@ cudaError_t run_backward_blocks(Kernel kern, const LnBwdParams& p, int nt, int g
   kern<<<blocks, groups * nt, smem, s>>>(p, nt, mags);
   e = cudaGetLastError();
   if (e != cudaSuccess || !p.partial) return e;
-  return launch_sum_partials(p.partial, blocks, 2 * static_cast<int64_t>(p.k), p.k, p.k, dgamma, dbeta, mags, p.amax, s);
+  return launch_sum_partials(p.partial, blocks, 2 * static_cast<int64_t>(p.k), p.k, p.k, dgamma, dbeta, mags, blocks, p.amax, s);
 }
 
 template <typename TX, typename TDY>
@@ -1006,7 +934,7 @@ cudaError_t run_backward_long(const LnBwdParams& p, float* dgamma, float* dbeta,
     ln_backward_params_long_kernel<TX><<<dim3(cols, chunks), LN_THREADS, 0, s>>>(p, per);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_sum_partials(p.partial, chunks, 2 * static_cast<int64_t>(p.k), p.k, p.k, dgamma, dbeta, nullptr, nullptr, s);
+    return launch_sum_partials(p.partial, chunks, 2 * static_cast<int64_t>(p.k), p.k, p.k, dgamma, dbeta, nullptr, 0, nullptr, s);
   }
   return cudaGetLastError();
 }
@@ -1048,7 +976,7 @@ cudaError_t dispatch_backward(const LnBwdParams& p, bool vec, float* dgamma, flo
 }  // namespace
 
 cudaError_t launch_sum_partials(const float* partial, int blocks, int64_t stride, int n0, int n1, float* out0, float* out1,
-                                const uint32_t* mags, float* amax, cudaStream_t s) {
+                                const uint32_t* mags, int n_mags, float* amax, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1058,7 +986,7 @@ cudaError_t launch_sum_partials(const float* partial, int blocks, int64_t stride
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sum_partials_kernel, partial, blocks, stride, n0, n1, out0, out1, mags, amax);
+  return cudaLaunchKernelEx(&cfg, sum_partials_kernel, partial, blocks, stride, n0, n1, out0, out1, mags, n_mags, amax);
 }
 
 // [blocks][2][k] partials, then one magnitude per block.
