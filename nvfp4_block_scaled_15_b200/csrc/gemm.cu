@@ -350,21 +350,35 @@ __device__ __forceinline__ T* box_elem(uint8_t* box, int row, int lane) {
   constexpr int PER = 16 / sizeof(T);
   return reinterpret_cast<T*>(box + box_chunk<T>(row, lane / PER)) + lane % PER;
 }
+// (Eight rows' accesses are issued before the first is used.)
 template <typename T>
 __device__ __forceinline__ void box_rows_out(uint8_t* box, void* base, int64_t ld, int row0, int rows, int col, bool in) {
   const int lane = threadIdx.x & 31;
   T* out = static_cast<T*>(base) + static_cast<int64_t>(row0) * ld + col + lane;
   if (!in) return;
-#pragma unroll 8
-  for (int r = 0; r < rows; ++r) out[r * ld] = *box_elem<T>(box, r, lane);
+#pragma unroll
+  for (int r = 0; r < EPI_BOX; r += 8) {
+    T x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = *box_elem<T>(box, r + i, lane);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (r + i < rows) out[(r + i) * ld] = x[i];
+  }
 }
 template <typename T>
 __device__ __forceinline__ void box_rows_in(uint8_t* box, const void* base, int64_t ld, int row0, int rows, int col, bool in) {
   const int lane = threadIdx.x & 31;
   const T* src = static_cast<const T*>(base) + static_cast<int64_t>(row0) * ld + col + lane;
   if (!in) return;
-#pragma unroll 16
-  for (int r = 0; r < rows; ++r) *box_elem<T>(box, r, lane) = src[r * ld];
+#pragma unroll
+  for (int r = 0; r < EPI_BOX; r += 16) {
+    T x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = r + i < rows ? src[(r + i) * ld] : from_f32<T>(0.0f);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) *box_elem<T>(box, r + i, lane) = x[i];
+  }
 }
 
 // x = alpha acc + bias of a box; lane l holds the bias of column col + l.
@@ -1671,12 +1685,19 @@ nvfp4_status run_gemm(const void* a_codes, const void* a_sf, const float* g_a, c
 
 }  // namespace
 
+// Most 128 x 128 tiles of an epilogue GEMM that takes one tile per SM instead of
+// a 256 x 256 tile per CTA pair.
+constexpr int64_t EPI_SMALL_TILES = 148;
+
 template <bool kMx>
 nvfp4_status dispatch_gemm(const void* a_codes, const void* a_sf, const float* g_a, const void* b_codes,
                            const void* b_sf, const float* g_b, int64_t M, int64_t N, int64_t K, void* d, int64_t ldd,
                            nvfp4_out_dtype out, const QuantOut* q, cudaStream_t s, const Epilogue* epi = nullptr) {
   if (N <= 128) return run_gemm<128, kMx>(a_codes, a_sf, g_a, b_codes, b_sf, g_b, M, N, K, d, ldd, out, q, s, epi);
   if (M <= 128) return run_gemm<256, kMx>(a_codes, a_sf, g_a, b_codes, b_sf, g_b, M, N, K, d, ldd, out, q, s, epi);
+  // few tiles: four times as many smaller ones, one SM each
+  if (epi && ((M + 127) / 128) * ((N + 127) / 128) <= EPI_SMALL_TILES)
+    return run_gemm<128, kMx>(a_codes, a_sf, g_a, b_codes, b_sf, g_b, M, N, K, d, ldd, out, q, s, epi);
   return run_gemm_pair<kMx>(a_codes, a_sf, g_a, b_codes, b_sf, g_b, M, N, K, d, ldd, out, q, s, nullptr, epi);
 }
 

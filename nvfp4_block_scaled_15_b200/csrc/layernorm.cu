@@ -628,8 +628,15 @@ constexpr int LO_THREADS = 512;
 constexpr int LO_STAGES = 3;
 constexpr int LO_SMEM = 220 * 1024;
 
+// gamma or beta as fp32 in shared memory, each element by the thread that uses
+// it in some group; the rows' first copies are on their way meanwhile.
+__device__ __forceinline__ void odd_params(float* dst, const void* src, int f32, int k, float dflt) {
+#pragma unroll 4
+  for (int c = threadIdx.x; c < k; c += blockDim.x) dst[c] = src ? load_param(src, f32, c) : dflt;
+}
+
 template <typename TX>
-__global__ void __launch_bounds__(LO_THREADS, 2) ln_forward_odd_kernel(const LnParams p, int nt) {
+__global__ void __launch_bounds__(LO_THREADS, 2) ln_forward_odd_kernel(const LnParams p, int nt, int params_shared) {
   constexpr int S = LO_STAGES;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float2 red[2][LO_THREADS / 32];
@@ -656,6 +663,13 @@ __global__ void __launch_bounds__(LO_THREADS, 2) ln_forward_odd_kernel(const LnP
   };
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) issue(r0 + i * step, i);
+  float* gamma = reinterpret_cast<float*>(ring + static_cast<size_t>(groups) * S * row_bytes);
+  float* beta = gamma + p.k;
+  if (params_shared) {
+    odd_params(gamma, p.gamma, p.param_f32, p.k, 1.0f);
+    odd_params(beta, p.beta, p.param_f32, p.k, 0.0f);
+    __syncthreads();
+  }
   uint32_t mag = 0;
   int parity = 0, stage = 0;
   for (int64_t r = r0; r < p.rows; r += step) {
@@ -689,15 +703,16 @@ __global__ void __launch_bounds__(LO_THREADS, 2) ln_forward_odd_kernel(const LnP
     __nv_bfloat16* yh = static_cast<__nv_bfloat16*>(p.y) + r * p.ldy;
 #pragma unroll 4
     for (int c = t; c < p.k; c += nt) {
-      const float gm = p.gamma ? load_param(p.gamma, p.param_f32, c) : 1.0f;
-      const float bt = p.beta ? load_param(p.beta, p.param_f32, c) : 0.0f;
+      const float gm = params_shared ? gamma[c] : p.gamma ? load_param(p.gamma, p.param_f32, c) : 1.0f;
+      const float bt = params_shared ? beta[c] : p.beta ? load_param(p.beta, p.param_f32, c) : 0.0f;
       const float v = fmaf((to_f32(row[c]) - mean) * rstd, gm, bt);
       if (p.y_f32) {
         yf[c] = v;
         mag = max(mag, mag_bits(v));
       } else {
-        yh[c] = __float2bfloat16_rn(v);
-        mag = max(mag, mag_bits(yh[c]));
+        const __nv_bfloat16 o = __float2bfloat16_rn(v);
+        yh[c] = o;
+        mag = max(mag, mag_bits(o));
       }
     }
     if (t == 0) {
@@ -728,7 +743,8 @@ __global__ void __launch_bounds__(LO_THREADS, 1) ln_backward_odd_kernel(const Ln
   float* acc = reinterpret_cast<float*>(ring);            // [groups][2][k]
   float* dg = acc + 2 * g * p.k;
   float* db = dg + p.k;
-  uint8_t* own = ring + static_cast<size_t>(groups) * 2 * p.k * 4 / 16 * 16 + 16 + static_cast<size_t>(g) * S * stage_bytes;
+  float* gamma = acc + static_cast<size_t>(groups) * 2 * p.k;
+  uint8_t* own = ring + (static_cast<size_t>(groups) * 2 + 1) * p.k * 4 / 16 * 16 + 16 + static_cast<size_t>(g) * S * stage_bytes;
   const float inv_k = 1.0f / static_cast<float>(p.k);
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * groups + g;
@@ -743,7 +759,9 @@ __global__ void __launch_bounds__(LO_THREADS, 1) ln_backward_odd_kernel(const Ln
   };
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) issue(r0 + i * step, i);
+  odd_params(gamma, p.gamma, p.param_f32, p.k, 1.0f);
   for (int c = t; c < p.k; c += nt) dg[c] = db[c] = 0.0f;
+  __syncthreads();
   uint32_t mag = 0;
   int parity = 0, stage = 0;
   float mean_next = r0 < p.rows ? p.mean[r0] : 0.0f, rstd_next = r0 < p.rows ? p.rstd[r0] : 0.0f;
@@ -766,7 +784,7 @@ __global__ void __launch_bounds__(LO_THREADS, 1) ln_backward_odd_kernel(const Ln
 #pragma unroll 4
     for (int c = t; c < p.k; c += nt) {
       const float d = to_f32(dy[c]), xh = (to_f32(x[c]) - mean) * rstd;
-      const float a = p.gamma ? d * load_param(p.gamma, p.param_f32, c) : d;
+      const float a = d * gamma[c];
       s1 += a;
       s2 = fmaf(a, xh, s2);
       dg[c] = fmaf(d, xh, dg[c]);
@@ -787,7 +805,7 @@ __global__ void __launch_bounds__(LO_THREADS, 1) ln_backward_odd_kernel(const Ln
 #pragma unroll 4
     for (int c = t; c < p.k; c += nt) {
       const float d = to_f32(dy[c]), xh = (to_f32(x[c]) - mean) * rstd;
-      const float a = p.gamma ? d * load_param(p.gamma, p.param_f32, c) : d;
+      const float a = d * gamma[c];
       float v = rstd * (a - fmaf(xh, c2, c1));
       if (p.res) v += to_f32(res[c]);
       const TX o = from_f32<TX>(v);
@@ -877,17 +895,20 @@ cudaError_t dispatch_forward(const LnParams& p, bool vec, cudaStream_t s) {
   const int64_t ring = static_cast<int64_t>(LO_STAGES) * odd_row_bytes(p.k < LF_MAX_K ? p.k : LF_MAX_K, sizeof(TX));
   if (!vec && p.k <= LF_MAX_K && ring <= LO_SMEM) {
     const int nt = odd_threads(p.k);
-    const int64_t half = LO_SMEM / 2;                     // two blocks per SM where a row's ring allows it
+    // gamma and beta in shared memory, and two blocks per SM, where they leave room for a row's ring
+    const int64_t half = LO_SMEM / 2;
+    int64_t params = 8 * static_cast<int64_t>(p.k);
+    if (ring + params > LO_SMEM) params = 0;
     int64_t groups = LO_THREADS / nt;
-    if (groups > half / ring) groups = half / ring > 0 ? half / ring : 1;
+    if (groups * ring + params > half) groups = ring + params <= half ? (half - params) / ring : 1;
     if (groups > p.rows) groups = p.rows;
     const int64_t need = (p.rows + groups - 1) / groups;
-    const int64_t most = static_cast<int64_t>(device_sm_count()) * (groups * ring <= half ? 2 : 1);
-    const int smem = static_cast<int>(groups * ring);
+    const int64_t most = static_cast<int64_t>(device_sm_count()) * (groups * ring + params <= half ? 2 : 1);
+    const int smem = static_cast<int>(groups * ring + params);
     auto kern = ln_forward_odd_kernel<TX>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<static_cast<int>(need < most ? need : most), static_cast<int>(groups) * nt, smem, s>>>(p, nt);
+    kern<<<static_cast<int>(need < most ? need : most), static_cast<int>(groups) * nt, smem, s>>>(p, nt, params > 0);
     return cudaGetLastError();
   }
   const int grid = static_cast<int>(p.rows < 8 * device_sm_count() ? p.rows : 8 * device_sm_count());
@@ -939,14 +960,14 @@ cudaError_t run_backward_long(const LnBwdParams& p, float* dgamma, float* dbeta,
   return cudaGetLastError();
 }
 
-// Shared memory per group of the odd kernel, 0 where a row is too long for it.
+// Shared memory per group of the odd kernel (beside gamma), 0 where a row is too long for it.
 template <typename TX, typename TDY>
 int64_t odd_backward_bytes(int64_t k, bool res) {
   if (k > LB_MAX_K) return 0;
   const int64_t stage = odd_row_bytes(static_cast<int>(k), sizeof(TDY)) +
                         odd_row_bytes(static_cast<int>(k), sizeof(TX)) * (res ? 2 : 1);
   const int64_t bytes = LO_STAGES * stage + 8 * k;
-  return bytes + 32 <= LO_SMEM ? bytes : 0;
+  return bytes + 4 * k + 32 <= LO_SMEM ? bytes : 0;
 }
 
 template <typename TX, typename TDY>
@@ -965,10 +986,11 @@ cudaError_t dispatch_backward(const LnBwdParams& p, bool vec, float* dgamma, flo
   if (each > 0) {
     const int nt = odd_threads(p.k);
     int64_t groups = LO_THREADS / nt;
-    if (groups > (LO_SMEM - 32) / each) groups = (LO_SMEM - 32) / each;
+    const int64_t gamma = 4 * static_cast<int64_t>(p.k) + 32;
+    if (groups > (LO_SMEM - gamma) / each) groups = (LO_SMEM - gamma) / each;
     if (groups > p.rows) groups = p.rows;
     return run_backward_blocks(ln_backward_odd_kernel<TX, TDY>, p, nt, static_cast<int>(groups),
-                               static_cast<size_t>(groups * each + 32), dgamma, dbeta, mags, s);
+                               static_cast<size_t>(groups * each + gamma), dgamma, dbeta, mags, s);
   }
   return run_backward_long<TX, TDY>(p, dgamma, dbeta, s);
 }
