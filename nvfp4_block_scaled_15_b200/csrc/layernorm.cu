@@ -10,6 +10,7 @@
 
 #include "epilogue.cuh"
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace nvfp4 {
 
@@ -192,9 +193,9 @@ __device__ __forceinline__ int chunk_col(int t, int nt, int j) { return 8 * (t +
 
 // Columns c .. c+7 of gamma or beta (cached: every row reads them).
 template <typename TP>
-__device__ __forceinline__ Chunk load_param_chunk(const void* p, int c, int k, float dflt) {
+__device__ __forceinline__ Chunk load_param_chunk(const void* p, int c, float dflt) {
   Chunk x;
-  if (!p || c >= k) {
+  if (!p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) x.v[i] = both(dflt);
   } else if constexpr (sizeof(TP) == 4) {
@@ -206,12 +207,6 @@ __device__ __forceinline__ Chunk load_param_chunk(const void* p, int c, int k, f
     x = unpack_chunk(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + c)));
   }
   return x;
-}
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  return v;
 }
 
 // cp.async copies into this thread's own slots of shared memory: nobody else
@@ -296,6 +291,131 @@ __device__ __forceinline__ Stats join_lanes(float n, float mean, float m2, float
 // Named barrier of the nt threads of group g (its warps only).
 __device__ __forceinline__ void group_sync(int g, int nt) {
   asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(nt) : "memory");
+}
+
+// A group's barrier, whatever its size.
+__device__ __forceinline__ void group_or_warp_sync(int g, int nt) {
+  if (nt > 32)
+    group_sync(g, nt);
+  else
+    __syncwarp();
+}
+
+// ---------------------------------------------------------------------------
+// Rows that start anywhere (an odd pitch or width, a view into a buffer)
+// ---------------------------------------------------------------------------
+// Such a row comes into shared memory as it lies in memory, copied in 4-byte
+// words (cp.async has no smaller ones): its element c is at slot c + shift,
+// shift = 1 where a bf16 row starts in the middle of a word, and zeros follow
+// the row's end.  Threads take the same 8-element chunks as above, out of five
+// words and a funnel shift, and results go back through shared memory in the
+// same way.  Any thread may have copied a thread's words, so a row takes two
+// barriers more than an aligned one.
+template <typename T>
+__device__ __forceinline__ int row_shift(const T* row) {
+  return sizeof(T) == 2 ? static_cast<int>((reinterpret_cast<uintptr_t>(row) >> 1) & 1) : 0;
+}
+
+// Bytes of a row's image: whole chunks, the word behind them and the shift.
+__host__ __device__ constexpr int odd_bytes(int k, int size) { return (k + 7) / 8 * 8 * size + 16; }
+
+template <typename T>
+__device__ __forceinline__ void odd_in(uint8_t* image, const T* row, int t, int nt, int k) {
+  T* dst = reinterpret_cast<T*>(image);
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll 4
+    for (int c = t; c < k; c += nt) cp_async4(dst + c, row + c);
+  } else {
+    const int shift = row_shift(row);
+    const int words = (k + shift) >> 1;                  // up to the last whole one
+#pragma unroll 4
+    for (int w = t + shift; w < words; w += nt) cp_async4(dst + 2 * w, row + (2 * w - shift));
+    // the ends, and zeros up to where a row with the other shift reaches
+    if (t == 0 && shift) dst[1] = row[0];
+    if (t == nt - 1) {
+      if ((k + shift) & 1 && k > shift) dst[k + shift - 1] = row[k - 1];
+      dst[k + shift] = from_f32<T>(0.0f);
+      if (shift == 0) dst[k + 1] = from_f32<T>(0.0f);
+    }
+  }
+}
+
+// Zeros behind the rows of an image, which copies leave alone.
+template <typename T>
+__device__ __forceinline__ void odd_clear(uint8_t* image, int t, int nt, int k) {
+  for (int c = k + t; c < odd_bytes(k, sizeof(T)) / static_cast<int>(sizeof(T)); c += nt)
+    reinterpret_cast<T*>(image)[c] = from_f32<T>(0.0f);
+}
+
+template <typename T>
+__device__ __forceinline__ Chunk odd_chunk(const uint8_t* image, int c, int shift) {
+  if constexpr (sizeof(T) == 2) {
+    const uint4 w = *reinterpret_cast<const uint4*>(image + 2 * c);
+    const uint32_t next = *reinterpret_cast<const uint32_t*>(image + 2 * c + 16);
+    const int bits = 16 * shift;
+    return unpack_chunk(make_uint4(__funnelshift_r(w.x, w.y, bits), __funnelshift_r(w.y, w.z, bits),
+                                   __funnelshift_r(w.z, w.w, bits), __funnelshift_r(w.w, next, bits)));
+  } else {
+    Chunk x;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float4 v = *reinterpret_cast<const float4*>(image + 4 * c + 16 * h);
+      x.v[2 * h] = make_float2(v.x, v.y), x.v[2 * h + 1] = make_float2(v.z, v.w);
+    }
+    return x;
+  }
+}
+
+// Elements of a chunk at or past the row's end become v.
+__device__ __forceinline__ void cut_chunk(Chunk& x, int valid, float v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (2 * i >= valid) x.v[i].x = v;
+    if (2 * i + 1 >= valid) x.v[i].y = v;
+  }
+}
+
+// A result row in shared memory (element c at slot c) to a row that starts
+// anywhere, in words where the row has whole ones.
+template <typename T>
+__device__ __forceinline__ void odd_out(const uint8_t* image, T* row, int t, int nt, int k) {
+  const T* src = reinterpret_cast<const T*>(image);
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll 4
+    for (int c = t; c < k; c += nt) row[c] = src[c];
+  } else {
+    const int shift = row_shift(row);
+    const int words = (k + shift) >> 1;
+    const uint32_t* in = reinterpret_cast<const uint32_t*>(image);
+#pragma unroll 4
+    for (int w = t + shift; w < words; w += nt)          // columns 2 w - shift and the next
+      *reinterpret_cast<uint32_t*>(row + (2 * w - shift)) = shift ? __funnelshift_r(in[w - 1], in[w], 16) : in[w];
+    if (t == 0 && shift) row[0] = src[0];
+    if (t == nt - 1 && ((k + shift) & 1) && k > shift) row[k - 1] = src[k - 1];
+  }
+}
+
+// gamma and beta as fp32 in shared memory, whole chunks; a thread's loads of
+// both are issued before the first is stored.
+__device__ __forceinline__ void params_in(float* gamma, float* beta, const LnParams& p) {
+  const int k8 = (p.k + 7) / 8 * 8;
+  for (int c = threadIdx.x; c < k8; c += 4 * blockDim.x) {
+    float g[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int col = min(c + i * static_cast<int>(blockDim.x), p.k - 1);
+      g[i] = p.gamma ? load_param(p.gamma, p.param_f32, col) : 1.0f;
+      b[i] = p.beta ? load_param(p.beta, p.param_f32, col) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int col = c + i * static_cast<int>(blockDim.x);
+      if (col < k8) gamma[col] = g[i], beta[col] = b[i];
+    }
+  }
+}
+__device__ __forceinline__ Chunk param_chunk(const float* p, int c) {
+  return odd_chunk<float>(reinterpret_cast<const uint8_t*>(p), c, 0);
 }
 
 // ---------------------------------------------------------------------------
@@ -389,6 +509,7 @@ __global__ void __launch_bounds__(THREADS, lf_blocks<TX, NV>(THREADS)) ln_forwar
     s2 = both(0.0f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      // branches: selects instead of them took registers that spilled (107 -> 139 us at 16384 x 8192)
       if (chunk_col(t, nt, j) < p.k) {
         const Chunk c = x[j].get();
 #pragma unroll
@@ -413,7 +534,7 @@ __global__ void __launch_bounds__(THREADS, lf_blocks<TX, NV>(THREADS)) ln_forwar
     for (int j = 0; j < NV; ++j) {
       const int col = chunk_col(t, nt, j);
       if (col < p.k) {
-        const Chunk gm = load_param_chunk<TP>(p.gamma, col, p.k, 1.0f), bt = load_param_chunk<TP>(p.beta, col, p.k, 0.0f);
+        const Chunk gm = load_param_chunk<TP>(p.gamma, col, 1.0f), bt = load_param_chunk<TP>(p.beta, col, 0.0f);
         Chunk c = x[j].get();
 #pragma unroll
         for (int i = 0; i < 4; ++i) c.v[i] = fma2(mul2(add2(c.v[i], both(-mean)), both(rstd)), gm.v[i], bt.v[i]);
@@ -431,31 +552,128 @@ __global__ void __launch_bounds__(THREADS, lf_blocks<TX, NV>(THREADS)) ln_forwar
   }
 }
 
+// Forward of rows that start anywhere, of up to LF_MAX_K elements: the chunks
+// of the kernel above out of the row's image in shared memory, where gamma and
+// beta lie too.  A thread holds its chunks in registers, so the next row's image
+// is on its way once every thread has read this one's; more images ahead leave
+// room for fewer groups and measured slower (16384 x 4095 bf16: one 123 us, two
+// 149, three 198).
+constexpr int LO_THREADS = 512;
+constexpr int LO_SMEM = 216 * 1024;
+
+template <typename TX, typename TY, int NV>
+__global__ void __launch_bounds__(LO_THREADS, NV <= 4 ? 2 : 1) ln_forward_odd_kernel(const LnParams p, int nt) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float2 red[2][LO_THREADS / 32];
+  __shared__ uint32_t mags[LO_THREADS / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int groups = blockDim.x / nt, g = threadIdx.x / nt, t = threadIdx.x - g * nt;
+  const int gw = nt >> 5, w0 = g * gw;
+  const int k8 = (p.k + 7) / 8 * 8;
+  const int row_bytes = odd_bytes(p.k, sizeof(TX)), out_bytes = k8 * static_cast<int>(sizeof(TY));
+  float* gamma = reinterpret_cast<float*>(smem);
+  float* beta = gamma + k8;
+  uint8_t* own = smem + 8 * k8 + static_cast<size_t>(g) * (row_bytes + out_bytes);
+  uint8_t* out = own + row_bytes;
+  const float inv_k = 1.0f / static_cast<float>(p.k);
+  auto count = [&](int first, int lanes) {
+    int n = 0;
+    for (int j = 0; j < NV; ++j) n += min(max(p.k - 8 * (first + nt * j), 0), 8 * lanes);
+    return static_cast<float>(n);
+  };
+  auto inverse = [](float n) { return n > 0.0f ? 1.0f / n : 0.0f; };
+  const float n_thread = count(t, 1), inv_thread = inverse(n_thread);
+  const float inv_warp = inverse(count(t - lane, 32));
+  const float n_lane = lane < gw ? count(32 * lane, 32) : 0.0f;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * groups + g;
+  odd_clear<TX>(own, t, nt, p.k);
+  group_or_warp_sync(g, nt);
+  auto issue = [&](int64_t r) {
+    if (r < p.rows) odd_in(own, static_cast<const TX*>(p.x) + r * p.ldx, t, nt, p.k);
+    cp_async_commit();
+  };
+  issue(r0);
+  params_in(gamma, beta, p);
+  __syncthreads();
+  Mag<TY> mag;
+  int parity = 0;
+  for (int64_t r = r0; r < p.rows; r += step) {
+    cp_async_wait<0>();
+    group_or_warp_sync(g, nt);                           // the row is there
+    const int shift = row_shift(static_cast<const TX*>(p.x) + r * p.ldx);
+    Chunk x[NV];
+    float2 s2 = both(0.0f);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = chunk_col(t, nt, j);
+      if (c < p.k) {
+        x[j] = odd_chunk<TX>(own, c, shift);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s2 = add2(s2, x[j].v[i]);        // 0 past the row's end
+      }
+    }
+    const float own_mean = (s2.x + s2.y) * inv_thread;
+    s2 = both(0.0f);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = chunk_col(t, nt, j);
+      if (c < p.k) {
+        Chunk d;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d.v[i] = add2(x[j].v[i], both(-own_mean));
+        if (c + 8 > p.k) cut_chunk(d, p.k - c, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s2 = fma2(d.v[i], d.v[i], s2);
+      }
+    }
+    Stats st = join_lanes(n_thread, own_mean, s2.x + s2.y, inv_warp);
+    if (gw > 1) {
+      if (lane == 0) red[parity][warp] = make_float2(st.mean, st.m2);
+      group_sync(g, nt);
+      const float2 w = lane < gw ? red[parity][w0 + lane] : make_float2(0.0f, 0.0f);
+      parity ^= 1;
+      st = join_lanes(n_lane, w.x, w.y, inv_k);
+    } else {
+      __syncwarp();
+    }
+    issue(r + step);                                     // every thread has read the image
+    const float mean = st.mean;
+    const float rstd = __frsqrt_rn(fmaf(st.m2 < 0.0f ? 0.0f : st.m2, inv_k, p.eps));   // a NaN stays one
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = chunk_col(t, nt, j);
+      if (c < p.k) {
+        const Chunk gm = param_chunk(gamma, c), bt = param_chunk(beta, c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          x[j].v[i] = fma2(mul2(add2(x[j].v[i], both(-mean)), both(rstd)), gm.v[i], bt.v[i]);
+        if (c + 8 > p.k) cut_chunk(x[j], p.k - c, 0.0f);
+        store_chunk<TY>(reinterpret_cast<TY*>(out) + c, x[j], mag);
+      }
+    }
+    group_or_warp_sync(g, nt);
+    odd_out(out, static_cast<TY*>(p.y) + r * p.ldy, t, nt, p.k);
+    if (t == 0) {
+      if (p.mean) p.mean[r] = mean;
+      if (p.rstd) p.rstd[r] = rstd;
+    }
+  }
+  if (p.amax) {
+    const uint32_t m = block_max(mag.bits(), mags);
+    if (threadIdx.x == 0) atomicMax(reinterpret_cast<unsigned int*>(p.amax), m);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Backward in one pass
 // ---------------------------------------------------------------------------
 constexpr int LB_THREADS = 512;        // most threads of a block; 128 registers each
 constexpr int LB_NV = 2;               // chunks of 8 elements per thread
-constexpr int LB_MAX_K = LB_THREADS * 8 * LB_NV;
-
-// Ring stages: what 192 KB hold of the rows in flight, four at most.
-template <typename TX, typename TDY>
-constexpr int lb_stages() {
-  const int bytes = LB_MAX_K * (2 * static_cast<int>(sizeof(TX)) + static_cast<int>(sizeof(TDY)));
-  return 196608 / bytes < 4 ? 196608 / bytes : 4;
-}
-
-// The groups' column sums acc[groups][2][k], added in order, as this block's
-// partial.
-__device__ __forceinline__ void write_partial(const LnBwdParams& p, const float* acc, int groups) {
-  __syncthreads();
-  float* out = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * p.k;
-  for (int i = threadIdx.x; i < 2 * p.k; i += blockDim.x) {
-    float s = 0.0f;
-    for (int h = 0; h < groups; ++h) s += acc[2 * h * p.k + i];
-    out[i] = s;
-  }
-}
+constexpr int LB_MAX_COLS = LB_THREADS * 8 * LB_NV;        // columns of a block
+constexpr int LB_MAX_CLUSTER = 8;
+constexpr int LB_MAX_K = LB_MAX_COLS * LB_MAX_CLUSTER;
+constexpr int LB_SMEM = 216 * 1024;
 
 // The block's largest |dx| (in warp 0): to its slot, for the sum over blocks
 // to join, or straight to the maximum where no such kernel follows.
@@ -467,56 +685,104 @@ __device__ __forceinline__ void publish_block(const LnBwdParams& p, uint32_t mag
     atomicMax(reinterpret_cast<unsigned int*>(p.amax), mag);
 }
 
+// Bytes of one ring stage of a group (vector: slots of nt threads; odd: images).
+template <typename TX, typename TDY, bool kOdd>
+__host__ __device__ constexpr int lb_stage_bytes(int k, int nt, bool res) {
+  return kOdd ? odd_bytes(k, sizeof(TDY)) + odd_bytes(k, sizeof(TX)) * (res ? 2 : 1)
+              : nt * 8 * LB_NV * static_cast<int>(sizeof(TDY) + sizeof(TX) * (res ? 2 : 1));
+}
+// Bytes of a group: its ring, and for odd rows the image of its dx.
+template <typename TX, typename TDY, bool kOdd, int S>
+__host__ __device__ constexpr int lb_group_bytes(int k, int nt, bool res) {
+  return S * lb_stage_bytes<TX, TDY, kOdd>(k, nt, res) + (kOdd ? odd_bytes(k, sizeof(TX)) : 0);
+}
+
 // Backward of rows of up to LB_MAX_K elements.  A block has G groups of nt
 // threads; a group takes one row at a time, a thread the same columns of every
 // row, so dgamma and dbeta are sums in its registers until the end.  The rows
-// ahead are on their way into a ring in shared memory (the accumulators leave
-// no room for a second row in registers).  At the end the groups' sums meet in
-// shared memory and the block writes one partial [2][k]; the sum over blocks
-// (sum_partials_kernel) runs in block order, so results do not depend on
-// timing.
-template <typename TX, typename TDY>
-__global__ void __launch_bounds__(LB_THREADS, 1) ln_backward_rows_kernel(const LnBwdParams p, int nt, uint32_t* mag_out) {
-  constexpr int S = lb_stages<TX, TDY>();
+// ahead are on their way into a ring of S in shared memory (the accumulators
+// leave no room for a second row in registers).  Rows longer than a block's
+// columns are cut between the blocks of a cluster (kc columns each, one group
+// per block), which exchange the row's two sums through each other's shared
+// memory.  At the end the groups' column sums meet in shared memory and the
+// block writes one partial; the sum over blocks (sum_partials_kernel) runs in
+// block order, so results do not depend on timing.
+template <typename TX, typename TDY, bool kOdd, bool kCluster, int S>
+__global__ void __launch_bounds__(LB_THREADS, 1) ln_backward_rows_kernel(const LnBwdParams p, int nt, int kc,
+                                                                          uint32_t* mag_out) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float2 red[2][LB_THREADS / 32];
+  __shared__ float2 peers[2][LB_MAX_CLUSTER];            // the row's sums of each block of the cluster
   __shared__ uint32_t mags[LB_THREADS / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int groups = blockDim.x / nt, g = threadIdx.x / nt, t = threadIdx.x - g * nt;
   const int gw = nt >> 5, w0 = g * gw;                   // warps of a group, its first
-  const int slots = nt * 8 * LB_NV;                      // elements of a group's row slots
-  const int dy_bytes = slots * static_cast<int>(sizeof(TDY)), x_bytes = slots * static_cast<int>(sizeof(TX));
-  const int stage_bytes = dy_bytes + x_bytes * (p.res ? 2 : 1);
-  uint8_t* own = ring + static_cast<size_t>(g) * S * stage_bytes;
+  const int cluster = kCluster ? (p.k + kc - 1) / kc : 1;            // blocks that share a row
+  const int rank = kCluster ? static_cast<int>(cluster_ctarank()) : 0;
+  const int c0 = rank * kc, k = kCluster ? min(kc, p.k - c0) : p.k;  // this block's columns
+  const int dy_bytes = kOdd ? odd_bytes(k, sizeof(TDY)) : nt * 8 * LB_NV * static_cast<int>(sizeof(TDY));
+  const int x_bytes = kOdd ? odd_bytes(k, sizeof(TX)) : nt * 8 * LB_NV * static_cast<int>(sizeof(TX));
+  const int stage_bytes = lb_stage_bytes<TX, TDY, kOdd>(k, nt, p.res != nullptr);
+  uint8_t* own = ring + static_cast<size_t>(g) * lb_group_bytes<TX, TDY, kOdd, S>(k, nt, p.res != nullptr);
+  uint8_t* out = own + S * stage_bytes;                  // odd: the image of dx
   const float inv_k = 1.0f / static_cast<float>(p.k);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * groups + g;
+  const int64_t step = static_cast<int64_t>(gridDim.x / cluster) * groups;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x / cluster) * groups + g;
+  const TDY* dy_base = static_cast<const TDY*>(p.dy) + c0;
+  const TX* x_base = static_cast<const TX*>(p.x) + c0;
+  const TX* res_base = static_cast<const TX*>(p.res) + c0;
 
   auto issue = [&](int64_t r, int stage) {
     if (r < p.rows) {
       uint8_t* b = own + stage * stage_bytes;
-      stage_in<TDY, LB_NV>(b, static_cast<const TDY*>(p.dy) + r * p.lddy, t, nt, p.k);
-      stage_in<TX, LB_NV>(b + dy_bytes, static_cast<const TX*>(p.x) + r * p.ldx, t, nt, p.k);
-      if (p.res) stage_in<TX, LB_NV>(b + dy_bytes + x_bytes, static_cast<const TX*>(p.res) + r * p.ldr, t, nt, p.k);
+      if constexpr (kOdd) {
+        odd_in(b, dy_base + r * p.lddy, t, nt, k);
+        odd_in(b + dy_bytes, x_base + r * p.ldx, t, nt, k);
+        if (p.res) odd_in(b + dy_bytes + x_bytes, res_base + r * p.ldr, t, nt, k);
+      } else {
+        stage_in<TDY, LB_NV>(b, dy_base + r * p.lddy, t, nt, k);
+        stage_in<TX, LB_NV>(b + dy_bytes, x_base + r * p.ldx, t, nt, k);
+        if (p.res) stage_in<TX, LB_NV>(b + dy_bytes + x_bytes, res_base + r * p.ldr, t, nt, k);
+      }
     }
     cp_async_commit();
   };
+  if constexpr (kCluster) cluster_sync_all();             // every block of the cluster has started
+  if constexpr (kOdd) {
+    for (int i = 0; i < S; ++i) {
+      uint8_t* b = own + i * stage_bytes;
+      odd_clear<TDY>(b, t, nt, k);
+      odd_clear<TX>(b + dy_bytes, t, nt, k);
+      if (p.res) odd_clear<TX>(b + dy_bytes + x_bytes, t, nt, k);
+    }
+    group_or_warp_sync(g, nt);
+  }
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) issue(r0 + i * step, i);
 
   Chunk gam[LB_NV], dg[LB_NV], db[LB_NV];
 #pragma unroll
   for (int j = 0; j < LB_NV; ++j) {
-    gam[j] = p.param_f32 ? load_param_chunk<float>(p.gamma, chunk_col(t, nt, j), p.k, 1.0f)
-                         : load_param_chunk<__nv_bfloat16>(p.gamma, chunk_col(t, nt, j), p.k, 1.0f);
+    const int c = chunk_col(t, nt, j);
 #pragma unroll
     for (int i = 0; i < 4; ++i) dg[j].v[i] = db[j].v[i] = both(0.0f);
+    if constexpr (!kOdd) {
+      const int in = c0 + min(c, k - 8);
+      gam[j] = p.param_f32 ? load_param_chunk<float>(p.gamma, in, 1.0f) : load_param_chunk<__nv_bfloat16>(p.gamma, in, 1.0f);
+      continue;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      gam[j].v[i].x = p.gamma && c + 2 * i < k ? load_param(p.gamma, p.param_f32, c0 + c + 2 * i) : 1.0f;
+      gam[j].v[i].y = p.gamma && c + 2 * i + 1 < k ? load_param(p.gamma, p.param_f32, c0 + c + 2 * i + 1) : 1.0f;
+    }
   }
   Mag<TX> mag;
   int parity = 0, stage = 0;
   float mean_next = r0 < p.rows ? p.mean[r0] : 0.0f, rstd_next = r0 < p.rows ? p.rstd[r0] : 0.0f;
   for (int64_t r = r0; r < p.rows; r += step) {
-    // the slot read in the last turn takes the row S - 1 turns ahead
+    // the slot read in the last turn takes the row S - 1 turns ahead (odd: every
+    // thread has read it, by the barrier in front of dx's way out)
     issue(r + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);
     const float mean = mean_next, rstd = rstd_next;
     if (r + step < p.rows) {
@@ -524,19 +790,32 @@ __global__ void __launch_bounds__(LB_THREADS, 1) ln_backward_rows_kernel(const L
       rstd_next = p.rstd[r + step];
     }
     cp_async_wait<S - 1>();
+    if constexpr (kOdd) group_or_warp_sync(g, nt);
     const uint8_t* b = own + stage * stage_bytes;
+    int dy_shift = 0, x_shift = 0;
+    if constexpr (kOdd) {
+      dy_shift = row_shift(dy_base + r * p.lddy);
+      x_shift = row_shift(x_base + r * p.ldx);
+    }
     Chunk dy[LB_NV], xh[LB_NV];
     float2 sa = both(0.0f), sx = both(0.0f);
 #pragma unroll
     for (int j = 0; j < LB_NV; ++j) {
-      dy[j] = stage_out<TDY>(b, t, nt, j);
-      xh[j] = stage_out<TX>(b + dy_bytes, t, nt, j);
+      const int c = chunk_col(t, nt, j);
+      if constexpr (kOdd) {
+        if (c >= k) continue;
+        dy[j] = odd_chunk<TDY>(b, c, dy_shift);
+        xh[j] = odd_chunk<TX>(b + dy_bytes, c, x_shift);
+      } else {
+        dy[j] = stage_out<TDY>(b, t, nt, j);
+        xh[j] = stage_out<TX>(b + dy_bytes, t, nt, j);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) xh[j].v[i] = mul2(add2(xh[j].v[i], both(-mean)), both(rstd));
-      if (chunk_col(t, nt, j) >= p.k) continue;
+      if (c >= k) continue;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 a = mul2(dy[j].v[i], gam[j].v[i]);
+        const float2 a = mul2(dy[j].v[i], gam[j].v[i]);       // 0 past the row's end, as dy is
         sa = add2(sa, a);
         sx = fma2(a, xh[j].v[i], sx);
         dg[j].v[i] = fma2(dy[j].v[i], xh[j].v[i], dg[j].v[i]);
@@ -548,25 +827,51 @@ __global__ void __launch_bounds__(LB_THREADS, 1) ln_backward_rows_kernel(const L
       if (lane == 0) red[parity][warp] = sum;
       group_sync(g, nt);
       const float2 w = lane < gw ? red[parity][w0 + lane] : make_float2(0.0f, 0.0f);
-      parity ^= 1;
       sum = warp_sum2(w.x, w.y);
     }
+    if constexpr (kCluster) {
+      // a peer reads the slots of this parity before it arrives at the next row's barrier
+      if (threadIdx.x < cluster)
+        st_shared_cluster_f32x2(mapa_shared(smem_u32(&peers[parity][rank]), threadIdx.x), sum);
+      cluster_sync_all();
+      sum = make_float2(0.0f, 0.0f);
+      for (int i = 0; i < cluster; ++i) {
+        sum.x += peers[parity][i].x;
+        sum.y += peers[parity][i].y;
+      }
+    }
+    parity ^= 1;
     const float2 c1 = both(-rstd * (sum.x * inv_k)), c2 = both(-rstd * (sum.y * inv_k));
-    TX* dx = static_cast<TX*>(p.dx) + r * p.lddx;
+    TX* dx = static_cast<TX*>(p.dx) + r * p.lddx + c0;
+    int res_shift = 0;
+    if constexpr (kOdd) res_shift = p.res ? row_shift(res_base + r * p.ldr) : 0;
 #pragma unroll
     for (int j = 0; j < LB_NV; ++j) {
-      const int col = chunk_col(t, nt, j);
-      if (col >= p.k) continue;
+      const int c = chunk_col(t, nt, j);
+      if (c >= k) continue;
       Chunk v;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         v.v[i] = fma2(mul2(dy[j].v[i], gam[j].v[i]), both(rstd), fma2(xh[j].v[i], c2, c1));
       if (p.res) {
-        const Chunk res = stage_out<TX>(b + dy_bytes + x_bytes, t, nt, j);
+        Chunk res;
+        if constexpr (kOdd)
+          res = odd_chunk<TX>(b + dy_bytes + x_bytes, c, res_shift);
+        else
+          res = stage_out<TX>(b + dy_bytes + x_bytes, t, nt, j);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v.v[i] = add2(v.v[i], res.v[i]);
       }
-      store_chunk<TX>(dx + col, v, mag);
+      if constexpr (kOdd) {
+        if (c + 8 > k) cut_chunk(v, k - c, 0.0f);
+        store_chunk<TX>(reinterpret_cast<TX*>(out) + c, v, mag);
+      } else {
+        store_chunk<TX>(dx + c, v, mag);
+      }
+    }
+    if constexpr (kOdd) {
+      group_or_warp_sync(g, nt);
+      odd_out(out, dx, t, nt, k);
     }
     if (++stage == S) stage = 0;
   }
@@ -577,246 +882,23 @@ __global__ void __launch_bounds__(LB_THREADS, 1) ln_backward_rows_kernel(const L
 #pragma unroll
     for (int j = 0; j < LB_NV; ++j) {
       const int c = chunk_col(t, nt, j);
-      if (c >= p.k) continue;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        acc[(2 * g) * p.k + c + e] = dg[j].get(e);
-        acc[(2 * g + 1) * p.k + c + e] = db[j].get(e);
-      }
+      for (int e = 0; e < 8; ++e)
+        if (c + e < k) {
+          acc[(2 * g) * k + c + e] = dg[j].get(e);
+          acc[(2 * g + 1) * k + c + e] = db[j].get(e);
+        }
     }
-    write_partial(p, acc, groups);
+    __syncthreads();
+    float* part = p.partial + static_cast<int64_t>(blockIdx.x / cluster) * 2 * p.k + c0;
+    for (int i = threadIdx.x; i < 2 * k; i += blockDim.x) {
+      float s = 0.0f;
+      for (int h = 0; h < groups; ++h) s += acc[2 * h * k + i];
+      part[i < k ? i : i - k + p.k] = s;
+    }
   }
   publish_block(p, m, mag_out);
-}
-
-// ---------------------------------------------------------------------------
-// Rows that start anywhere (an odd pitch, a view into a buffer)
-// ---------------------------------------------------------------------------
-// The same groups and rings, but a ring stage holds the row's bytes as they
-// lie in memory, copied in 4-byte words: a bf16 row may start in the middle of
-// a word, so element c sits at 2-byte slot c + shift, and the words at the
-// row's two ends are copied element by element.  Any thread may have copied a
-// thread's elements: each row has one more barrier than above, after which the
-// copies are visible and the slot read in the turn before is free.  A thread's
-// elements are t, t + nt, ...
-template <typename T>
-__device__ __forceinline__ int row_shift(const T* row) {
-  return sizeof(T) == 2 ? static_cast<int>((reinterpret_cast<uintptr_t>(row) >> 1) & 1) : 0;
-}
-
-template <typename T>
-__device__ __forceinline__ void odd_in(uint8_t* slot, const T* row, int t, int nt, int k) {
-  if constexpr (sizeof(T) == 4) {
-    for (int c = t; c < k; c += nt) cp_async4(slot + 4 * c, row + c);
-  } else {
-    const int shift = row_shift(row);
-    T* dst = reinterpret_cast<T*>(slot);
-    for (int w = t; 2 * w - shift < k; w += nt) {
-      const int c = 2 * w - shift;
-      if (c >= 0 && c + 1 < k)
-        cp_async4(dst + 2 * w, row + c);
-      else
-        dst[2 * w + (c < 0)] = row[c < 0 ? 0 : c];
-    }
-  }
-}
-
-// Bytes of one row in a stage.
-__host__ __device__ constexpr int odd_row_bytes(int k, int size) { return (k * size + 4 + 15) / 16 * 16; }
-
-constexpr int LO_THREADS = 512;
-constexpr int LO_STAGES = 3;
-constexpr int LO_SMEM = 220 * 1024;
-
-// gamma or beta as fp32 in shared memory, each element by the thread that uses
-// it in some group; the rows' first copies are on their way meanwhile.
-__device__ __forceinline__ void odd_params(float* dst, const void* src, int f32, int k, float dflt) {
-#pragma unroll 4
-  for (int c = threadIdx.x; c < k; c += blockDim.x) dst[c] = src ? load_param(src, f32, c) : dflt;
-}
-
-template <typename TX>
-__global__ void __launch_bounds__(LO_THREADS, 2) ln_forward_odd_kernel(const LnParams p, int nt, int params_shared) {
-  constexpr int S = LO_STAGES;
-  extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ float2 red[2][LO_THREADS / 32];
-  __shared__ uint32_t mags[LO_THREADS / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int groups = blockDim.x / nt, g = threadIdx.x / nt, t = threadIdx.x - g * nt;
-  const int gw = nt >> 5, w0 = g * gw;
-  const int row_bytes = odd_row_bytes(p.k, sizeof(TX));
-  uint8_t* own = ring + static_cast<size_t>(g) * S * row_bytes;
-  const float inv_k = 1.0f / static_cast<float>(p.k);
-  auto count = [&](int w) {                              // elements that warp w of a group holds
-    const int full = p.k / nt, rest = min(max(p.k - full * nt - 32 * w, 0), 32);
-    return static_cast<float>(32 * full + rest);
-  };
-  const float n_own = count(warp - w0);
-  const float inv_own = n_own > 0.0f ? 1.0f / n_own : 0.0f;
-  const float n_lane = lane < gw ? count(lane) : 0.0f;
-  const float inv_lane = n_lane > 0.0f ? 1.0f / n_lane : 0.0f;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * groups + g;
-  auto issue = [&](int64_t r, int stage) {
-    if (r < p.rows) odd_in(own + stage * row_bytes, static_cast<const TX*>(p.x) + r * p.ldx, t, nt, p.k);
-    cp_async_commit();
-  };
-#pragma unroll
-  for (int i = 0; i < S - 1; ++i) issue(r0 + i * step, i);
-  float* gamma = reinterpret_cast<float*>(ring + static_cast<size_t>(groups) * S * row_bytes);
-  float* beta = gamma + p.k;
-  if (params_shared) {
-    odd_params(gamma, p.gamma, p.param_f32, p.k, 1.0f);
-    odd_params(beta, p.beta, p.param_f32, p.k, 0.0f);
-    __syncthreads();
-  }
-  uint32_t mag = 0;
-  int parity = 0, stage = 0;
-  for (int64_t r = r0; r < p.rows; r += step) {
-    cp_async_wait<S - 2>();
-    if (gw > 1) group_sync(g, nt); else __syncwarp();
-    issue(r + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);
-    const TX* row = reinterpret_cast<const TX*>(own + stage * row_bytes) + row_shift(static_cast<const TX*>(p.x) + r * p.ldx);
-    if (++stage == S) stage = 0;
-    float s = 0.0f, m2 = 0.0f;
-#pragma unroll 4
-    for (int c = t; c < p.k; c += nt) s += to_f32(row[c]);
-    s = warp_sum(s);
-    float mean = s * inv_own;
-#pragma unroll 4
-    for (int c = t; c < p.k; c += nt) {
-      const float d = to_f32(row[c]) - mean;
-      m2 = fmaf(d, d, m2);
-    }
-    m2 = warp_sum(m2);
-    if (gw > 1) {
-      if (lane == 0) red[parity][warp] = make_float2(s, m2);
-      group_sync(g, nt);
-      const float2 w = lane < gw ? red[parity][w0 + lane] : make_float2(0.0f, 0.0f);
-      parity ^= 1;
-      mean = warp_sum(w.x) * inv_k;
-      const float d = fmaf(w.x, inv_lane, -mean);
-      m2 = warp_sum(n_lane > 0.0f ? fmaf(n_lane * d, d, w.y) : 0.0f);
-    }
-    const float rstd = __frsqrt_rn(fmaf(m2, inv_k, p.eps));
-    float* yf = static_cast<float*>(p.y) + r * p.ldy;
-    __nv_bfloat16* yh = static_cast<__nv_bfloat16*>(p.y) + r * p.ldy;
-#pragma unroll 4
-    for (int c = t; c < p.k; c += nt) {
-      const float gm = params_shared ? gamma[c] : p.gamma ? load_param(p.gamma, p.param_f32, c) : 1.0f;
-      const float bt = params_shared ? beta[c] : p.beta ? load_param(p.beta, p.param_f32, c) : 0.0f;
-      const float v = fmaf((to_f32(row[c]) - mean) * rstd, gm, bt);
-      if (p.y_f32) {
-        yf[c] = v;
-        mag = max(mag, mag_bits(v));
-      } else {
-        const __nv_bfloat16 o = __float2bfloat16_rn(v);
-        yh[c] = o;
-        mag = max(mag, mag_bits(o));
-      }
-    }
-    if (t == 0) {
-      if (p.mean) p.mean[r] = mean;
-      if (p.rstd) p.rstd[r] = rstd;
-    }
-  }
-  cp_async_wait<0>();
-  if (p.amax) {
-    mag = block_max(mag, mags);
-    if (threadIdx.x == 0) atomicMax(reinterpret_cast<unsigned int*>(p.amax), mag);
-  }
-}
-
-// Backward: the column sums of a group live in shared memory, each column
-// touched by one thread only.
-template <typename TX, typename TDY>
-__global__ void __launch_bounds__(LO_THREADS, 1) ln_backward_odd_kernel(const LnBwdParams p, int nt, uint32_t* mag_out) {
-  constexpr int S = LO_STAGES;
-  extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ float2 red[2][LO_THREADS / 32];
-  __shared__ uint32_t mags[LO_THREADS / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int groups = blockDim.x / nt, g = threadIdx.x / nt, t = threadIdx.x - g * nt;
-  const int gw = nt >> 5, w0 = g * gw;
-  const int dy_bytes = odd_row_bytes(p.k, sizeof(TDY)), x_bytes = odd_row_bytes(p.k, sizeof(TX));
-  const int stage_bytes = dy_bytes + x_bytes * (p.res ? 2 : 1);
-  float* acc = reinterpret_cast<float*>(ring);            // [groups][2][k]
-  float* dg = acc + 2 * g * p.k;
-  float* db = dg + p.k;
-  float* gamma = acc + static_cast<size_t>(groups) * 2 * p.k;
-  uint8_t* own = ring + (static_cast<size_t>(groups) * 2 + 1) * p.k * 4 / 16 * 16 + 16 + static_cast<size_t>(g) * S * stage_bytes;
-  const float inv_k = 1.0f / static_cast<float>(p.k);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * groups + g;
-  auto issue = [&](int64_t r, int stage) {
-    if (r < p.rows) {
-      uint8_t* b = own + stage * stage_bytes;
-      odd_in(b, static_cast<const TDY*>(p.dy) + r * p.lddy, t, nt, p.k);
-      odd_in(b + dy_bytes, static_cast<const TX*>(p.x) + r * p.ldx, t, nt, p.k);
-      if (p.res) odd_in(b + dy_bytes + x_bytes, static_cast<const TX*>(p.res) + r * p.ldr, t, nt, p.k);
-    }
-    cp_async_commit();
-  };
-#pragma unroll
-  for (int i = 0; i < S - 1; ++i) issue(r0 + i * step, i);
-  odd_params(gamma, p.gamma, p.param_f32, p.k, 1.0f);
-  for (int c = t; c < p.k; c += nt) dg[c] = db[c] = 0.0f;
-  __syncthreads();
-  uint32_t mag = 0;
-  int parity = 0, stage = 0;
-  float mean_next = r0 < p.rows ? p.mean[r0] : 0.0f, rstd_next = r0 < p.rows ? p.rstd[r0] : 0.0f;
-  for (int64_t r = r0; r < p.rows; r += step) {
-    const float mean = mean_next, rstd = rstd_next;
-    if (r + step < p.rows) {
-      mean_next = p.mean[r + step];
-      rstd_next = p.rstd[r + step];
-    }
-    cp_async_wait<S - 2>();
-    if (gw > 1) group_sync(g, nt); else __syncwarp();
-    issue(r + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);
-    const uint8_t* b = own + stage * stage_bytes;
-    if (++stage == S) stage = 0;
-    const TDY* dy = reinterpret_cast<const TDY*>(b) + row_shift(static_cast<const TDY*>(p.dy) + r * p.lddy);
-    const TX* x = reinterpret_cast<const TX*>(b + dy_bytes) + row_shift(static_cast<const TX*>(p.x) + r * p.ldx);
-    const TX* res = reinterpret_cast<const TX*>(b + dy_bytes + x_bytes) +
-                    (p.res ? row_shift(static_cast<const TX*>(p.res) + r * p.ldr) : 0);
-    float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll 4
-    for (int c = t; c < p.k; c += nt) {
-      const float d = to_f32(dy[c]), xh = (to_f32(x[c]) - mean) * rstd;
-      const float a = d * gamma[c];
-      s1 += a;
-      s2 = fmaf(a, xh, s2);
-      dg[c] = fmaf(d, xh, dg[c]);
-      db[c] += d;
-    }
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
-    if (gw > 1) {
-      if (lane == 0) red[parity][warp] = make_float2(s1, s2);
-      group_sync(g, nt);
-      const float2 w = lane < gw ? red[parity][w0 + lane] : make_float2(0.0f, 0.0f);
-      parity ^= 1;
-      s1 = warp_sum(w.x);
-      s2 = warp_sum(w.y);
-    }
-    const float c1 = s1 * inv_k, c2 = s2 * inv_k;
-    TX* dx = static_cast<TX*>(p.dx) + r * p.lddx;
-#pragma unroll 4
-    for (int c = t; c < p.k; c += nt) {
-      const float d = to_f32(dy[c]), xh = (to_f32(x[c]) - mean) * rstd;
-      const float a = d * gamma[c];
-      float v = rstd * (a - fmaf(xh, c2, c1));
-      if (p.res) v += to_f32(res[c]);
-      const TX o = from_f32<TX>(v);
-      dx[c] = o;
-      mag = max(mag, mag_bits(o));
-    }
-  }
-  cp_async_wait<0>();
-  mag = block_max(mag, mags);
-  if (p.partial) write_partial(p, acc, groups);
-  publish_block(p, mag, mag_out);
+  if constexpr (kCluster) cluster_sync_all();             // no block leaves while a peer may still write to it
 }
 
 // First n0 columns of the blocks' partials [blocks][stride] to out0, the next
@@ -880,11 +962,33 @@ cudaError_t run_forward(const LnParams& p, cudaStream_t s) {
                      : run_forward_rows<TX, bf16, bf16, NV, THREADS>(p, s);
 }
 
-// Threads per row of the kernels for rows that start anywhere: about 16
-// elements each.
-int odd_threads(int k) {
-  const int nt = (k + 511) / 512 * 32;
-  return nt < LO_THREADS ? nt : LO_THREADS;
+template <typename TX, typename TY, int NV>
+cudaError_t run_forward_odd(const LnParams& p, int nt, int64_t group_bytes, int64_t params, cudaStream_t s) {
+  const int64_t per_sm = NV <= 4 ? 2 : 1;                 // blocks per SM
+  int64_t groups = LO_THREADS / nt;
+  int64_t fit = (LO_SMEM / per_sm - params) / group_bytes;
+  const bool shared_sm = fit >= 1;
+  if (!shared_sm) fit = (LO_SMEM - params) / group_bytes;            // one block has the SM
+  if (groups > fit) groups = fit;                         // also with fewer rows: all threads fetch gamma and beta
+  const int64_t need = (p.rows + groups - 1) / groups;
+  const int64_t most = device_sm_count() * (shared_sm ? per_sm : 1);
+  const int smem = static_cast<int>(groups * group_bytes + params);
+  auto kern = ln_forward_odd_kernel<TX, TY, NV>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<static_cast<int>(need < most ? need : most), static_cast<int>(groups) * nt, smem, s>>>(p, nt);
+  return cudaGetLastError();
+}
+
+template <typename TX, typename TY, int NV>
+bool try_forward_odd(const LnParams& p, cudaStream_t s, cudaError_t* e) {
+  const int per_warp = 32 * 8 * NV;
+  const int nt = (p.k + per_warp - 1) / per_warp * 32;
+  const int64_t row = odd_bytes(p.k, sizeof(TX)), out = (p.k + 7) / 8 * 8 * static_cast<int64_t>(sizeof(TY));
+  const int64_t params = (p.k + 7) / 8 * 64;
+  if (nt > LO_THREADS || params + row + out > LO_SMEM) return false;
+  *e = run_forward_odd<TX, TY, NV>(p, nt, row + out, params, s);
+  return true;
 }
 
 template <typename TX>
@@ -892,24 +996,14 @@ cudaError_t dispatch_forward(const LnParams& p, bool vec, cudaStream_t s) {
   if (vec && p.k <= LF_THREADS * 32) return run_forward<TX, 4, LF_THREADS>(p, s);
   if (vec && p.k <= lf_max_k<4>()) return run_forward<TX, 4, 512>(p, s);
   if (vec && p.k <= LF_MAX_K) return run_forward<TX, 8, 512>(p, s);
-  const int64_t ring = static_cast<int64_t>(LO_STAGES) * odd_row_bytes(p.k < LF_MAX_K ? p.k : LF_MAX_K, sizeof(TX));
-  if (!vec && p.k <= LF_MAX_K && ring <= LO_SMEM) {
-    const int nt = odd_threads(p.k);
-    // gamma and beta in shared memory, and two blocks per SM, where they leave room for a row's ring
-    const int64_t half = LO_SMEM / 2;
-    int64_t params = 8 * static_cast<int64_t>(p.k);
-    if (ring + params > LO_SMEM) params = 0;
-    int64_t groups = LO_THREADS / nt;
-    if (groups * ring + params > half) groups = ring + params <= half ? (half - params) / ring : 1;
-    if (groups > p.rows) groups = p.rows;
-    const int64_t need = (p.rows + groups - 1) / groups;
-    const int64_t most = static_cast<int64_t>(device_sm_count()) * (groups * ring + params <= half ? 2 : 1);
-    const int smem = static_cast<int>(groups * ring + params);
-    auto kern = ln_forward_odd_kernel<TX>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    kern<<<static_cast<int>(need < most ? need : most), static_cast<int>(groups) * nt, smem, s>>>(p, nt, params > 0);
-    return cudaGetLastError();
+  cudaError_t e;
+  if (!vec && p.k <= LF_MAX_K) {
+    using bf16 = __nv_bfloat16;
+    if (p.k <= lf_max_k<4>()) {
+      if (p.y_f32 ? try_forward_odd<TX, float, 4>(p, s, &e) : try_forward_odd<TX, bf16, 4>(p, s, &e)) return e;
+    } else if (p.y_f32 ? try_forward_odd<TX, float, 8>(p, s, &e) : try_forward_odd<TX, bf16, 8>(p, s, &e)) {
+      return e;
+    }
   }
   const int grid = static_cast<int>(p.rows < 8 * device_sm_count() ? p.rows : 8 * device_sm_count());
   ln_forward_long_kernel<TX><<<grid, LN_THREADS, 0, s>>>(p);
@@ -918,27 +1012,6 @@ cudaError_t dispatch_forward(const LnParams& p, bool vec, cudaStream_t s) {
 
 // Every row of the operand starts on a 16-byte boundary.
 bool rows_aligned16(const void* p, int64_t ld, bool f32) { return aligned16(p) && (ld * (f32 ? 4 : 2)) % 16 == 0; }
-
-// Blocks of a one-pass backward kernel, each with `groups` groups of nt
-// threads and smem bytes of shared memory, and the sum over them.
-template <typename Kernel>
-cudaError_t run_backward_blocks(Kernel kern, const LnBwdParams& p, int nt, int groups, size_t smem, float* dgamma,
-                                float* dbeta, uint32_t* mags, cudaStream_t s) {
-  const int sms = device_sm_count() < LB_MAX_BLOCKS ? device_sm_count() : LB_MAX_BLOCKS;
-  const int64_t need = (p.rows + groups - 1) / groups;
-  const int blocks = static_cast<int>(need < sms ? need : sms);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  // the sum over blocks also joins their maxima: only without it has *amax to be cleared
-  if (e == cudaSuccess && p.amax && !p.partial) e = cudaMemsetAsync(p.amax, 0, sizeof(float), s);
-  if (e != cudaSuccess) return e;
-  kern<<<blocks, groups * nt, smem, s>>>(p, nt, mags);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || !p.partial) return e;
-  return launch_sum_partials(p.partial, blocks, 2 * static_cast<int64_t>(p.k), p.k, p.k, dgamma, dbeta, mags, blocks, p.amax, s);
-}
-
-template <typename TX, typename TDY>
-constexpr int64_t lb_elem(bool res) { return static_cast<int64_t>(sizeof(TDY) + sizeof(TX) * (res ? 2 : 1)); }
 
 template <typename TX, typename TDY>
 cudaError_t run_backward_long(const LnBwdParams& p, float* dgamma, float* dbeta, cudaStream_t s) {
@@ -960,38 +1033,74 @@ cudaError_t run_backward_long(const LnBwdParams& p, float* dgamma, float* dbeta,
   return cudaGetLastError();
 }
 
-// Shared memory per group of the odd kernel (beside gamma), 0 where a row is too long for it.
-template <typename TX, typename TDY>
-int64_t odd_backward_bytes(int64_t k, bool res) {
-  if (k > LB_MAX_K) return 0;
-  const int64_t stage = odd_row_bytes(static_cast<int>(k), sizeof(TDY)) +
-                        odd_row_bytes(static_cast<int>(k), sizeof(TX)) * (res ? 2 : 1);
-  const int64_t bytes = LO_STAGES * stage + 8 * k;
-  return bytes + 4 * k + 32 <= LO_SMEM ? bytes : 0;
+// A launch of the one-pass backward kernel: rows cut between `cluster` blocks.
+template <typename TX, typename TDY, bool kOdd, int S>
+cudaError_t run_backward_rows(const LnBwdParams& p, int cluster, int kc, float* dgamma, float* dbeta, uint32_t* mags,
+                              cudaStream_t s) {
+  const int per_warp = 32 * 8 * LB_NV;
+  const int nt = (kc + per_warp - 1) / per_warp * 32;
+  const int64_t each = lb_group_bytes<TX, TDY, kOdd, S>(kc, nt, p.res != nullptr);
+  int64_t groups = cluster > 1 ? 1 : LB_THREADS / nt;
+  if (groups > LB_SMEM / each) groups = LB_SMEM / each;
+  if (groups > p.rows) groups = p.rows;
+  int64_t smem = groups * each;
+  if (groups * 2 * kc * 4 > smem) smem = groups * 2 * kc * 4;        // the column sums
+  const int64_t sms = (device_sm_count() < LB_MAX_BLOCKS ? device_sm_count() : LB_MAX_BLOCKS) / cluster;
+  const int64_t need = (p.rows + groups - 1) / groups;
+  const int blocks = static_cast<int>(need < sms ? need : sms) * cluster;
+  auto kern = cluster > 1 ? ln_backward_rows_kernel<TX, TDY, kOdd, true, S> : ln_backward_rows_kernel<TX, TDY, kOdd, false, S>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  // the sum over blocks also joins their maxima: only without it has *amax to be cleared
+  if (e == cudaSuccess && p.amax && !p.partial) e = cudaMemsetAsync(p.amax, 0, sizeof(float), s);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(static_cast<unsigned>(groups * nt));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, kern, p, nt, kc, mags);
+  if (e != cudaSuccess || !p.partial) return e;
+  return launch_sum_partials(p.partial, blocks / cluster, 2 * static_cast<int64_t>(p.k), p.k, p.k, dgamma, dbeta, mags, blocks,
+                             p.amax, s);
+}
+
+// The smallest cluster whose blocks hold their share of a row and a ring of
+// it: four stages, or three or two of long rows.
+template <typename TX, typename TDY, bool kOdd>
+bool try_backward_rows(const LnBwdParams& p, float* dgamma, float* dbeta, uint32_t* mags, cudaStream_t s, cudaError_t* e) {
+  for (int cluster = 1; cluster <= LB_MAX_CLUSTER; cluster *= 2) {
+    const int64_t kc = ((static_cast<int64_t>(p.k) + cluster - 1) / cluster + 7) / 8 * 8;
+    if (kc > LB_MAX_COLS || kc * (cluster - 1) >= p.k) continue;
+    const int cols = static_cast<int>(kc);
+    const int per_warp = 32 * 8 * LB_NV;
+    const int nt = (cols + per_warp - 1) / per_warp * 32;
+    const bool res = p.res != nullptr;
+    if (lb_group_bytes<TX, TDY, kOdd, 4>(cols, nt, res) <= LB_SMEM)
+      *e = run_backward_rows<TX, TDY, kOdd, 4>(p, cluster, cols, dgamma, dbeta, mags, s);
+    else if (lb_group_bytes<TX, TDY, kOdd, 3>(cols, nt, res) <= LB_SMEM)
+      *e = run_backward_rows<TX, TDY, kOdd, 3>(p, cluster, cols, dgamma, dbeta, mags, s);
+    else if (lb_group_bytes<TX, TDY, kOdd, 2>(cols, nt, res) <= LB_SMEM)
+      *e = run_backward_rows<TX, TDY, kOdd, 2>(p, cluster, cols, dgamma, dbeta, mags, s);
+    else
+      continue;
+    return true;
+  }
+  return false;
 }
 
 template <typename TX, typename TDY>
 cudaError_t dispatch_backward(const LnBwdParams& p, bool vec, float* dgamma, float* dbeta, uint32_t* mags, cudaStream_t s) {
-  if (vec && p.k <= LB_MAX_K) {
-    const int per_warp = 32 * 8 * LB_NV;
-    const int nt = (p.k + per_warp - 1) / per_warp * 32;
-    int groups = LB_THREADS / nt;
-    if (groups > p.rows) groups = static_cast<int>(p.rows);
-    size_t smem = static_cast<size_t>(lb_stages<TX, TDY>() * groups * nt * 8 * LB_NV * lb_elem<TX, TDY>(p.res != nullptr));
-    const size_t sums = static_cast<size_t>(groups) * 2 * p.k * sizeof(float);
-    if (sums > smem) smem = sums;
-    return run_backward_blocks(ln_backward_rows_kernel<TX, TDY>, p, nt, groups, smem, dgamma, dbeta, mags, s);
-  }
-  const int64_t each = vec ? 0 : odd_backward_bytes<TX, TDY>(p.k, p.res != nullptr);
-  if (each > 0) {
-    const int nt = odd_threads(p.k);
-    int64_t groups = LO_THREADS / nt;
-    const int64_t gamma = 4 * static_cast<int64_t>(p.k) + 32;
-    if (groups > (LO_SMEM - gamma) / each) groups = (LO_SMEM - gamma) / each;
-    if (groups > p.rows) groups = p.rows;
-    return run_backward_blocks(ln_backward_odd_kernel<TX, TDY>, p, nt, static_cast<int>(groups),
-                               static_cast<size_t>(groups * each + gamma), dgamma, dbeta, mags, s);
-  }
+  cudaError_t e = cudaSuccess;
+  if (vec ? try_backward_rows<TX, TDY, false>(p, dgamma, dbeta, mags, s, &e)
+          : try_backward_rows<TX, TDY, true>(p, dgamma, dbeta, mags, s, &e))
+    return e;
   return run_backward_long<TX, TDY>(p, dgamma, dbeta, s);
 }
 
