@@ -66,7 +66,28 @@ struct LnParams {
   float* amax;
   int64_t rows;
   int k;
+  int joined;            // the grid is one cluster, which joins its blocks' maxima itself
 };
+
+// Few blocks: a single cluster, whose first block writes the maximum; clearing
+// it first would take another launch, a third of a decoding step's call.
+constexpr int LF_MAX_CLUSTER = 8;
+
+__device__ __forceinline__ void publish_amax(const LnParams& p, uint32_t mag, uint32_t* mags) {
+  __shared__ uint32_t blocks[LF_MAX_CLUSTER];
+  if (!p.amax) return;
+  uint32_t m = block_max(mag, mags);
+  if (!p.joined) {
+    if (threadIdx.x == 0) atomicMax(reinterpret_cast<unsigned int*>(p.amax), m);
+    return;
+  }
+  if (threadIdx.x == 0) st_shared_cluster_u32(mapa_shared(smem_u32(&blocks[blockIdx.x]), 0), m);
+  cluster_sync_all();
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    for (int i = 1; i < static_cast<int>(gridDim.x); ++i) m = max(m, blocks[i]);
+    *p.amax = __uint_as_float(m);
+  }
+}
 
 // Rows of any length: one block per row at a time, three passes over the row
 // (L2 holds it after the first).
@@ -491,6 +512,7 @@ __global__ void __launch_bounds__(THREADS, lf_blocks<TX, NV>(THREADS)) ln_forwar
   const float inv_warp = inverse(count(t - lane, 32));
   const float n_lane = lane < gw ? count(32 * lane, 32) : 0.0f;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  if (p.joined) cluster_sync_all();                       // every block has started, before its memory is written to
   Mag<TY> mag;
   int parity = 0;
   for (int64_t r = static_cast<int64_t>(blockIdx.x) * groups + g; r < p.rows; r += step) {
@@ -546,10 +568,7 @@ __global__ void __launch_bounds__(THREADS, lf_blocks<TX, NV>(THREADS)) ln_forwar
       if (p.rstd) p.rstd[r] = rstd;
     }
   }
-  if (p.amax) {
-    const uint32_t m = block_max(mag.bits(), mags);
-    if (threadIdx.x == 0) atomicMax(reinterpret_cast<unsigned int*>(p.amax), m);
-  }
+  publish_amax(p, mag.bits(), mags);
 }
 
 // Forward of rows that start anywhere, of up to LF_MAX_K elements: the chunks
@@ -596,6 +615,7 @@ __global__ void __launch_bounds__(LO_THREADS, NV <= 4 ? 2 : 1) ln_forward_odd_ke
   issue(r0);
   params_in(gamma, beta, p);
   __syncthreads();
+  if (p.joined) cluster_sync_all();                       // every block has started, before its memory is written to
   Mag<TY> mag;
   int parity = 0;
   for (int64_t r = r0; r < p.rows; r += step) {
@@ -659,10 +679,7 @@ __global__ void __launch_bounds__(LO_THREADS, NV <= 4 ? 2 : 1) ln_forward_odd_ke
       if (p.rstd) p.rstd[r] = rstd;
     }
   }
-  if (p.amax) {
-    const uint32_t m = block_max(mag.bits(), mags);
-    if (threadIdx.x == 0) atomicMax(reinterpret_cast<unsigned int*>(p.amax), m);
-  }
+  publish_amax(p, mag.bits(), mags);
 }
 
 // ---------------------------------------------------------------------------
@@ -939,17 +956,41 @@ __global__ void __launch_bounds__(256) sum_partials_kernel(const float* partial,
 constexpr int LN_CHUNKS = 64;
 constexpr int LB_MAX_BLOCKS = 160;     // of the one-pass backward kernel; a workspace is sized for it
 
+// Launches a forward kernel for `need` blocks' worth of rows, `most` of them at
+// a time.  Up to a cluster's blocks go as one cluster.
+template <typename Kernel>
+cudaError_t launch_forward(Kernel kern, LnParams p, int64_t need, int64_t most, int threads, int smem, int nt, cudaStream_t s) {
+  if (need <= LF_MAX_CLUSTER) {
+    most = LF_MAX_CLUSTER;
+    p.joined = 1;
+  }
+  cudaError_t e = cudaSuccess;
+  if (p.amax && !p.joined) e = cudaMemsetAsync(p.amax, 0, sizeof(float), s);
+  if (e == cudaSuccess && smem > 0) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(static_cast<unsigned>(need < most ? need : most));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cfg.gridDim.x;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.joined ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, p, nt);
+}
+
 template <typename TX, typename TY, typename TP, int NV, int THREADS>
 cudaError_t run_forward_rows(const LnParams& p, cudaStream_t s) {
   const int per_warp = 32 * 8 * NV;
   const int nt = (p.k + per_warp - 1) / per_warp * 32;
   int groups = THREADS / nt;
   if (groups > p.rows) groups = static_cast<int>(p.rows);
-  const int64_t need = (p.rows + groups - 1) / groups;
-  const int64_t most = static_cast<int64_t>(device_sm_count()) * lf_blocks<TX, NV>(THREADS);
-  ln_forward_rows_kernel<TX, TY, TP, NV, THREADS>
-      <<<static_cast<int>(need < most ? need : most), groups * nt, 0, s>>>(p, nt);
-  return cudaGetLastError();
+  return launch_forward(ln_forward_rows_kernel<TX, TY, TP, NV, THREADS>, p, (p.rows + groups - 1) / groups,
+                        static_cast<int64_t>(device_sm_count()) * lf_blocks<TX, NV>(THREADS), groups * nt, 0, nt, s);
 }
 
 template <typename TX, int NV, int THREADS>
@@ -970,14 +1011,9 @@ cudaError_t run_forward_odd(const LnParams& p, int nt, int64_t group_bytes, int6
   const bool shared_sm = fit >= 1;
   if (!shared_sm) fit = (LO_SMEM - params) / group_bytes;            // one block has the SM
   if (groups > fit) groups = fit;                         // also with fewer rows: all threads fetch gamma and beta
-  const int64_t need = (p.rows + groups - 1) / groups;
-  const int64_t most = device_sm_count() * (shared_sm ? per_sm : 1);
-  const int smem = static_cast<int>(groups * group_bytes + params);
-  auto kern = ln_forward_odd_kernel<TX, TY, NV>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  kern<<<static_cast<int>(need < most ? need : most), static_cast<int>(groups) * nt, smem, s>>>(p, nt);
-  return cudaGetLastError();
+  return launch_forward(ln_forward_odd_kernel<TX, TY, NV>, p, (p.rows + groups - 1) / groups,
+                        device_sm_count() * (shared_sm ? per_sm : 1), static_cast<int>(groups) * nt,
+                        static_cast<int>(groups * group_bytes + params), nt, s);
 }
 
 template <typename TX, typename TY, int NV>
@@ -1004,6 +1040,10 @@ cudaError_t dispatch_forward(const LnParams& p, bool vec, cudaStream_t s) {
     } else if (p.y_f32 ? try_forward_odd<TX, float, 8>(p, s, &e) : try_forward_odd<TX, bf16, 8>(p, s, &e)) {
       return e;
     }
+  }
+  if (p.amax) {
+    e = cudaMemsetAsync(p.amax, 0, sizeof(float), s);
+    if (e != cudaSuccess) return e;
   }
   const int grid = static_cast<int>(p.rows < 8 * device_sm_count() ? p.rows : 8 * device_sm_count());
   ln_forward_long_kernel<TX><<<grid, LN_THREADS, 0, s>>>(p);
@@ -1127,14 +1167,10 @@ size_t layernorm_backward_workspace_bytes(int64_t rows, int64_t k) {
 }
 
 nvfp4_status launch_layernorm(const LayerNorm& a, cudaStream_t s) {
-  if (a.amax) {
-    const cudaError_t e = cudaMemsetAsync(a.amax, 0, sizeof(float), s);
-    if (e != cudaSuccess) return launch_status(e);
-  }
-  if (a.rows == 0) return NVFP4_OK;
+  if (a.rows == 0) return a.amax ? launch_status(cudaMemsetAsync(a.amax, 0, sizeof(float), s)) : NVFP4_OK;
   const bool xf = a.x_dtype == NVFP4_DTYPE_F32, yf = a.y_dtype == NVFP4_DTYPE_F32;
   const LnParams p{a.x, a.ldx, a.gamma, a.beta, a.param_dtype == NVFP4_DTYPE_F32, a.eps, a.y, a.ldy,
-                   yf, a.mean, a.rstd, a.amax, a.rows, static_cast<int>(a.k)};
+                   yf, a.mean, a.rstd, a.amax, a.rows, static_cast<int>(a.k), 0};
   const bool vec = a.k % 8 == 0 && rows_aligned16(a.x, a.ldx, xf) && rows_aligned16(a.y, a.ldy, yf) && aligned16(a.gamma) && aligned16(a.beta);
   return launch_status(xf ? dispatch_forward<float>(p, vec, s) : dispatch_forward<__nv_bfloat16>(p, vec, s));
 }
