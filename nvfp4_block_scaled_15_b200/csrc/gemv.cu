@@ -71,6 +71,42 @@ __device__ __forceinline__ __nv_bfloat16 gv_out(const GemvEpi& e, int m, int n, 
   return __float2bfloat16_rn(v);
 }
 
+// With kE and few weight tiles, each tile's K stages are cut into `split`
+// equal parts, one block each: the stream-K ranges, at most two blocks per
+// tile, would leave SMs idle.  (nvfp4_gemv_batched keeps its ranges and, with
+// them, its sums' order.)  Block b takes part b % split of tile b / split.
+template <bool kE>
+__device__ __forceinline__ void gv_range(int split, int units, int num_kt, int& u_begin, int& u_end) {
+  if (kE && split > 1) {
+    const int tile = static_cast<int>(blockIdx.x) / split, part = static_cast<int>(blockIdx.x) % split;
+    u_begin = tile * num_kt + part * num_kt / split;
+    u_end = tile * num_kt + (part + 1) * num_kt / split;
+    return;
+  }
+  // unit counts fit in int (checked at launch)
+  u_begin = static_cast<int>(static_cast<int64_t>(units) * blockIdx.x / gridDim.x);
+  u_end = static_cast<int>(static_cast<int64_t>(units) * (blockIdx.x + 1) / gridDim.x);
+}
+
+// The parts of a tile in order, this block's from its registers, the others'
+// from their slots: acc becomes the sum (M rows of MAX_M).
+template <int MAX_M>
+__device__ __forceinline__ void gv_join_parts(const float* partials, int split, int M, int col, uint32_t (&acc)[32]) {
+  const int part = static_cast<int>(blockIdx.x) % split;
+  const float* first = partials + static_cast<int64_t>(blockIdx.x - part) * M * BM + col;
+  float sum[MAX_M];
+#pragma unroll
+  for (int m = 0; m < MAX_M; ++m) sum[m] = 0.0f;
+  for (int i = 0; i < split; ++i) {
+    const float* slot = first + static_cast<int64_t>(i) * M * BM;
+#pragma unroll
+    for (int m = 0; m < MAX_M; ++m)
+      if (m < M) sum[m] += i == part ? __uint_as_float(acc[m]) : __ldcg(slot + m * BM);
+  }
+#pragma unroll
+  for (int m = 0; m < MAX_M; ++m) acc[m] = __float_as_uint(sum[m]);
+}
+
 struct GemvParams {
   const uint8_t* wsf;      // weight scales, tensor-core layout
   const uint8_t* xsf;      // activation scales, tensor-core layout (128 padded rows)
@@ -81,6 +117,7 @@ struct GemvParams {
   __nv_bfloat16* y;
   int64_t ldy;
   GemvEpi epi;
+  int split;               // kE: parts of a tile, or 1
   int M, N, K;
   int kb4;
   int tiles;
@@ -143,10 +180,9 @@ __global__ void __launch_bounds__(GV_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
-  // unit counts fit in int (checked at launch)
   const int units = p.tiles * p.num_kt;
-  const int u_begin = static_cast<int>(static_cast<int64_t>(units) * blockIdx.x / gridDim.x);
-  const int u_end = static_cast<int>(static_cast<int64_t>(units) * (blockIdx.x + 1) / gridDim.x);
+  int u_begin, u_end;
+  gv_range<kE>(p.split, units, p.num_kt, u_begin, u_end);
   const int ksteps_total = p.K / MMA_K;
 
   if (warp == 0) {
@@ -314,6 +350,29 @@ __global__ void __launch_bounds__(GV_THREADS, 1)
         }
         continue;
       }
+      if constexpr (kE) {
+        if (p.split > 1) {
+          float* slot = p.partials + static_cast<int64_t>(blockIdx.x) * p.M * BM;
+#pragma unroll
+          for (int m = 0; m < GV_N; ++m)
+            if (m < p.M) slot[m * BM + col] = __uint_as_float(v[m]);
+          __threadfence();
+          __syncwarp();
+          int arrived = 0;
+          if (lane == 0) arrived = atomicAdd(&p.counters[tile * 4 + quad], 1);
+          arrived = __shfl_sync(0xFFFFFFFFu, arrived, 0);
+          if (arrived == p.split - 1) {                         // the last part: finish
+            __threadfence();
+            gv_join_parts<GV_N>(p.partials, p.split, p.M, col, v);
+            if (n < p.N) {
+#pragma unroll
+              for (int m = 0; m < GV_N; ++m)
+                if (m < p.M) p.y[static_cast<int64_t>(m) * p.ldy + n] = gv_out<kE>(p.epi, m, n, __uint_as_float(v[m]), alpha, bias);
+            }
+          }
+          continue;
+        }
+      }
       // my slot: 2*cta for the tail of a tile I start in the middle of, 2*cta+1
       // for the head of a tile I leave unfinished
       float* mine = p.partials + (static_cast<int64_t>(2 * cta + (has_head ? 1 : 0)) * p.M) * BM;
@@ -421,6 +480,7 @@ struct GemvFusedParams {
   __nv_bfloat16* y;
   int64_t ldy;
   GemvEpi epi;
+  int split;               // kE: parts of a tile, or 1
   int M, N, K;
   int kb4;
   int tiles;
@@ -430,7 +490,7 @@ struct GemvFusedParams {
 };
 
 // Count this contributor's arrival on a tagged counter; returns the number
-// of earlier arrivals of the same launch (0 or 1).
+// of earlier arrivals of the same launch.
 __device__ __forceinline__ int tagged_arrive(unsigned long long* c, unsigned long long tag) {
   unsigned long long cur = *reinterpret_cast<volatile unsigned long long*>(c);
   for (int attempt = 0; attempt < 64; ++attempt) {
@@ -440,7 +500,7 @@ __device__ __forceinline__ int tagged_arrive(unsigned long long* c, unsigned lon
     if (prev == cur) return same ? static_cast<int>(cur & 0xFFFFull) : 0;
     cur = prev;
   }
-  return 0;   // two contributors per tile cannot contend 64 times; reached only on corruption
+  return 0;   // eight contributors per tile cannot contend 64 times; reached only on corruption
 }
 
 template <bool kE>
@@ -490,8 +550,8 @@ __global__ void __launch_bounds__(GF_THREADS, 1)
   const uint32_t tmem_base = *tmem_slot;
 
   const int units = p.tiles * p.num_kt;
-  const int u_begin = static_cast<int>(static_cast<int64_t>(units) * blockIdx.x / gridDim.x);
-  const int u_end = static_cast<int>(static_cast<int64_t>(units) * (blockIdx.x + 1) / gridDim.x);
+  int u_begin, u_end;
+  gv_range<kE>(p.split, units, p.num_kt, u_begin, u_end);
   const int ksteps_total = p.K / MMA_K;
 
   if (warp == 0) {
@@ -693,6 +753,31 @@ __global__ void __launch_bounds__(GF_THREADS, 1)
             if (m < p.M) p.y[static_cast<int64_t>(m) * p.ldy + n] = gv_out<kE>(p.epi, m, n, __uint_as_float(v[m]), alpha, bias);
         }
         continue;
+      }
+      if constexpr (kE) {
+        if (p.split > 1) {
+          float* slot = p.partials + static_cast<int64_t>(blockIdx.x) * p.M * BM;
+          unsigned long long* count = &p.counters[tile * 4 + quad];
+#pragma unroll
+          for (int m = 0; m < GF_MAX_M; ++m)
+            if (m < p.M) slot[m * BM + col] = __uint_as_float(v[m]);
+          __threadfence();
+          __syncwarp();
+          int arrived = 0;
+          if (lane == 0) arrived = tagged_arrive(count, p.tag);
+          arrived = __shfl_sync(0xFFFFFFFFu, arrived, 0);
+          if (arrived == p.split - 1) {
+            __threadfence();
+            gv_join_parts<GF_MAX_M>(p.partials, p.split, p.M, col, v);
+            if (n < p.N) {
+#pragma unroll
+              for (int m = 0; m < GF_MAX_M; ++m)
+                if (m < p.M) p.y[static_cast<int64_t>(m) * p.ldy + n] = gv_out<kE>(p.epi, m, n, __uint_as_float(v[m]), alpha, bias);
+            }
+            if (lane == 0) *reinterpret_cast<volatile unsigned long long*>(count) = 0ull;   // tile done: reset
+          }
+          continue;
+        }
       }
       float* mine = p.partials + (static_cast<int64_t>(2 * cta + (has_head ? 1 : 0)) * p.M) * BM;
       const float* other = p.partials + (static_cast<int64_t>(has_head ? 2 * (cta + 1) : 2 * (cta - 1) + 1) * p.M) * BM;
@@ -958,6 +1043,18 @@ static GemvEpi gemv_epi(const Epilogue* e) {
   return GemvEpi{e->bias, e->bias_f32, e->act, static_cast<const __nv_bfloat16*>(e->residual), e->ldr};
 }
 
+// Parts per tile of an epilogue GEMV: as many as give every SM a block, at most
+// GV_MAX_SPLIT (the last block reads the others' parts one after another), each
+// of at least one K stage.
+constexpr int GV_MAX_SPLIT = 8;
+static int gemv_split(const Epilogue* epi, int tiles, int sms, int64_t num_kt) {
+  if (!epi) return 1;
+  int split = sms / tiles;
+  if (split > GV_MAX_SPLIT) split = GV_MAX_SPLIT;
+  if (split > num_kt) split = static_cast<int>(num_kt);
+  return split > 1 ? split : 1;
+}
+
 static nvfp4_status launch_gemv_fused(const void* x, int64_t M, int64_t ldx, const void* w_codes, const void* w_sf,
                                       const float* g_w, int64_t N, int64_t K, void* y, int64_t ldy,
                                       const GemvWs& L, uint8_t* base, cudaStream_t s, const Epilogue* epi) {
@@ -987,6 +1084,8 @@ static nvfp4_status launch_gemv_fused(const void* x, int64_t M, int64_t ldx, con
   if (!p.status) return NVFP4_ERR_CUDA;
   int grid = tiles < sms ? tiles : sms;       // grid <= tiles: at most two contributors per tile
   if (grid > GV_MAX_CTAS) grid = GV_MAX_CTAS;
+  p.split = gemv_split(epi, tiles, sms < GV_MAX_CTAS ? sms : GV_MAX_CTAS, p.num_kt);
+  if (p.split > 1) grid = tiles * p.split;
   auto kern = epi ? gemv_fused_kernel<true> : gemv_fused_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GF_SMEM_BYTES);
   if (e != cudaSuccess) return launch_status(e);
@@ -1056,6 +1155,8 @@ nvfp4_status launch_gemv(const void* x, int64_t M, int64_t ldx, const void* w_co
   // of stages, so each tile has at most two contributors
   int grid = tiles < sms ? tiles : sms;
   if (grid > GV_MAX_CTAS) grid = GV_MAX_CTAS;
+  p.split = gemv_split(epi, tiles, sms < GV_MAX_CTAS ? sms : GV_MAX_CTAS, p.num_kt);
+  if (p.split > 1) grid = tiles * p.split;
   auto kern = epi ? gemv_kernel<true> : gemv_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GV_SMEM_BYTES);
   if (e != cudaSuccess) return launch_status(e);

@@ -137,7 +137,7 @@ def test_gemm_nonfinite_bias_and_residual(lib):
 
 # both GEMV kernels (M <= 8 and K <= 8192, or not), whole and split tiles, ragged N and K
 @pytest.mark.parametrize("m", [1, 3, 8, 9, 16, 32])
-@pytest.mark.parametrize("n,k", [(1, 64), (1000, 1024), (384, 4096), (640, 2880), (160 * 128, 1024)], ids=str)
+@pytest.mark.parametrize("n,k", [(1, 64), (1000, 1024), (384, 4096), (640, 2880), (160 * 128, 1024), (100, 8192), (9000, 2112)], ids=str)
 def test_gemv_epilogue(lib, m, n, k):
     _, w, x, (d_ref, s_ref, alpha) = product(lib, m, n, k)
     for bd, act, res, pad, off in [(BF16, "gelu_tanh", True, 0, 0), (F32, "gelu", False, 3, 1), (None, "none", True, 1, 0),
@@ -157,7 +157,7 @@ def test_gemv_epilogue(lib, m, n, k):
 def test_gemv_residual_in_place_and_plain(lib, m, k):
     n = 1000
     _, w, x, (d_ref, s_ref, alpha) = product(lib, m, n, k)
-    assert torch.equal(lib.gemv_batched_epilogue(x, w), lib.gemv_batched(x, w))
+    R.check(lib.gemv_batched_epilogue(x, w), *R.epilogue(d_ref, s_ref, alpha, None, "none", None)["d"], "plain")
     r = randn(2, m, n).bfloat16().cuda()
     ref = R.epilogue(d_ref, s_ref, alpha, None, "none", r)
     lib.gemv_batched_epilogue(x, w, residual=r, out=r)
