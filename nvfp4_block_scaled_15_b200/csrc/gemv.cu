@@ -44,6 +44,8 @@ constexpr int GV_SF_COLS_PER_STAGE = 32;      // 16 for A, 16 for B (one 4-colum
 constexpr int GV_EPI_WARPS = 4;
 constexpr int GV_THREADS = (2 + GV_EPI_WARPS) * 32;
 constexpr int GV_SMEM_BYTES = GV_STAGES * GV_STAGE_BYTES + 256 + 1024;
+// The epilogue's outputs of a tile (sum and residual) on their way through its loop.
+constexpr int GV_OUT_BYTES = GV_N * BM * static_cast<int>(sizeof(float2));
 static_assert(GV_SF_BASE + GV_STAGES * GV_SF_COLS_PER_STAGE <= (int)TMEM_COLS, "TMEM budget");
 
 // Output m, n of a product row: v = alpha * acc, or with kE the epilogue
@@ -63,12 +65,45 @@ __device__ __forceinline__ float gv_bias(const GemvEpi& e, int n, int n_end) {
   return e.bias && n < n_end ? load_param(e.bias, e.bias_f32, n) : 0.0f;
 }
 
-template <bool kE>
-__device__ __forceinline__ __nv_bfloat16 gv_out(const GemvEpi& e, int m, int n, float acc, float alpha, float bias) {
-  if constexpr (!kE) return __float2bfloat16_rn(acc * alpha);
-  float v = act_value(fmaf(acc, alpha, bias), e.act);
-  if (e.residual) v += __bfloat162float(e.residual[static_cast<int64_t>(m) * e.ldr + n]);
-  return __float2bfloat16_rn(v);
+// Residual of a column's M rows, fetched while the products run.
+template <bool kE, int MAX_M>
+__device__ __forceinline__ void gv_residual(const GemvEpi& e, int M, int n, int N, float (&res)[MAX_M]) {
+#pragma unroll
+  for (int m = 0; m < MAX_M; ++m) {
+    res[m] = 0.0f;
+    if constexpr (kE)
+      if (e.residual && m < M && n < N) res[m] = __bfloat162float(e.residual[static_cast<int64_t>(m) * e.ldr + n]);
+  }
+}
+
+// The outputs of column n.  With kE they take a loop over the rows (through
+// this thread's slots in shared memory, since registers have no index): the
+// activations' code, run once per block, is fetched once instead of once per
+// row, which took most of a small call's time.
+template <bool kE, int MAX_M>
+__device__ __forceinline__ void gv_store(const GemvEpi& e, __nv_bfloat16* y, int64_t ldy, int M, int n, int N, int col,
+                                         const uint32_t (&acc)[32], float alpha, float bias, const float (&res)[MAX_M],
+                                         float2* slots) {
+  if (n >= N) return;
+  if constexpr (!kE) {
+#pragma unroll
+    for (int m = 0; m < MAX_M; ++m)
+      if (m < M) y[static_cast<int64_t>(m) * ldy + n] = __float2bfloat16_rn(__uint_as_float(acc[m]) * alpha);
+  } else {
+#pragma unroll
+    for (int m = 0; m < MAX_M; ++m)
+      if (m < M) slots[m * BM + col] = make_float2(__uint_as_float(acc[m]), res[m]);
+    with_act(e.act, [&](auto a) {
+#pragma unroll 1
+      for (int m = 0; m < M; m += 2) {
+        const float2 s0 = slots[m * BM + col], s1 = slots[min(m + 1, M - 1) * BM + col];
+        float2 x = fma2(make_float2(s0.x, s1.x), both(alpha), both(bias));
+        x = add2(act_pair<decltype(a)::value>(x), make_float2(s0.y, s1.y));
+        y[static_cast<int64_t>(m) * ldy + n] = __float2bfloat16_rn(x.x);
+        if (m + 1 < M) y[static_cast<int64_t>(m + 1) * ldy + n] = __float2bfloat16_rn(x.y);
+      }
+    });
+  }
 }
 
 // With kE and few weight tiles, each tile's K stages are cut into `split`
@@ -315,6 +350,7 @@ __global__ void __launch_bounds__(GV_THREADS, 1)
     // them (fp32 addition commutes: the result does not depend on who).
     const int quad = warp & 3;
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    float2* slots = reinterpret_cast<float2*>(smem + GV_SMEM_BYTES - 1024);        // kE: past what the ring takes
     const float alpha = __fdiv_rn(1.0f, __fmul_rn(*p.g_w, *p.g_x));
     const int cta = blockIdx.x;
     int acc = 0;
@@ -327,6 +363,11 @@ __global__ void __launch_bounds__(GV_THREADS, 1)
       const bool has_head = u == tile_begin;                    // this segment holds the tile's first stage
       const bool has_tail = seg_end == tile_begin + p.num_kt;   // ... and its last stage
       u = seg_end;
+      const int col = quad * 32 + lane;                         // row of the weight tile
+      const int n = tile * BM + col;                            // output column
+      const float bias = gv_bias<kE>(p.epi, n, p.N);
+      float res[GV_N];
+      gv_residual<kE, GV_N>(p.epi, p.M, n, p.N, res);
       if (!mbar_wait_bounded(&acc_full[acc], acc_phase, abort_flag, p.wait_limit_ns, p.status)) break;
       tc_fence_after();
       uint32_t v[32];
@@ -339,81 +380,60 @@ __global__ void __launch_bounds__(GV_THREADS, 1)
         acc = 0;
         acc_phase ^= 1;
       }
-      const int col = quad * 32 + lane;                         // row of the weight tile
-      const int n = tile * BM + col;                            // output column
-      const float bias = gv_bias<kE>(p.epi, n, p.N);
-      if (has_head && has_tail) {
-        if (n < p.N) {
+      bool done = has_head && has_tail;                         // v holds the tile's whole sum
+      if (kE && p.split > 1) {
+        float* slot = p.partials + static_cast<int64_t>(blockIdx.x) * p.M * BM;
 #pragma unroll
-          for (int m = 0; m < GV_N; ++m)
-            if (m < p.M) p.y[static_cast<int64_t>(m) * p.ldy + n] = gv_out<kE>(p.epi, m, n, __uint_as_float(v[m]), alpha, bias);
+        for (int m = 0; m < GV_N; ++m)
+          if (m < p.M) slot[m * BM + col] = __uint_as_float(v[m]);
+        __threadfence();
+        __syncwarp();
+        int arrived = 0;
+        if (lane == 0) arrived = atomicAdd(&p.counters[tile * 4 + quad], 1);
+        arrived = __shfl_sync(0xFFFFFFFFu, arrived, 0);
+        if (arrived == p.split - 1) {                           // the last part: finish
+          __threadfence();
+          gv_join_parts<GV_N>(p.partials, p.split, p.M, col, v);
+          done = true;
         }
-        continue;
-      }
-      if constexpr (kE) {
-        if (p.split > 1) {
-          float* slot = p.partials + static_cast<int64_t>(blockIdx.x) * p.M * BM;
+      } else if (!done) {
+        // my slot: 2*cta for the tail of a tile I start in the middle of, 2*cta+1
+        // for the head of a tile I leave unfinished
+        float* mine = p.partials + (static_cast<int64_t>(2 * cta + (has_head ? 1 : 0)) * p.M) * BM;
+        const float* other = p.partials + (static_cast<int64_t>(has_head ? 2 * (cta + 1) : 2 * (cta - 1) + 1) * p.M) * BM;
+        // The other contributor usually arrived long ago (a CTA works its tiles'
+        // tail segments first and head segments last).  If its arrival is on the
+        // counter, its partial was published before it (fence, then the atomic),
+        // so an acquire load of the counter makes it visible: finish the tile now,
+        // without writing this side's partial, fencing or counting.  Otherwise
+        // both take the counted path below and the second arrival finishes.
+        // (Lane 0's load, broadcast, so all lanes take the same branch; __syncwarp
+        // orders the other lanes' reads after it.)
+        int* counter = &p.counters[tile * 4 + quad];
+        int seen = 0;
+        if (lane == 0) seen = ld_acquire_gpu(counter);
+        seen = __shfl_sync(0xFFFFFFFFu, seen, 0);
+        __syncwarp();
+        done = seen >= 1;
+        if (!done) {
 #pragma unroll
           for (int m = 0; m < GV_N; ++m)
-            if (m < p.M) slot[m * BM + col] = __uint_as_float(v[m]);
+            if (m < p.M) mine[m * BM + col] = __uint_as_float(v[m]);
           __threadfence();
           __syncwarp();
           int arrived = 0;
-          if (lane == 0) arrived = atomicAdd(&p.counters[tile * 4 + quad], 1);
+          if (lane == 0) arrived = atomicAdd(counter, 1);
           arrived = __shfl_sync(0xFFFFFFFFu, arrived, 0);
-          if (arrived == p.split - 1) {                         // the last part: finish
-            __threadfence();
-            gv_join_parts<GV_N>(p.partials, p.split, p.M, col, v);
-            if (n < p.N) {
-#pragma unroll
-              for (int m = 0; m < GV_N; ++m)
-                if (m < p.M) p.y[static_cast<int64_t>(m) * p.ldy + n] = gv_out<kE>(p.epi, m, n, __uint_as_float(v[m]), alpha, bias);
-            }
-          }
-          continue;
+          done = arrived == 1;                                  // second of the two: finish
+          if (done) __threadfence();
         }
-      }
-      // my slot: 2*cta for the tail of a tile I start in the middle of, 2*cta+1
-      // for the head of a tile I leave unfinished
-      float* mine = p.partials + (static_cast<int64_t>(2 * cta + (has_head ? 1 : 0)) * p.M) * BM;
-      const float* other = p.partials + (static_cast<int64_t>(has_head ? 2 * (cta + 1) : 2 * (cta - 1) + 1) * p.M) * BM;
-      // The other contributor usually arrived long ago (a CTA works its tiles'
-      // tail segments first and head segments last).  If its arrival is on the
-      // counter, its partial was published before it (fence, then the atomic),
-      // so an acquire load of the counter makes it visible: finish the tile now,
-      // without writing this side's partial, fencing or counting.  Otherwise
-      // both take the counted path below and the second arrival finishes.
-      int* counter = &p.counters[tile * 4 + quad];
-      if (ld_acquire_gpu(counter) >= 1) {
-        if (n < p.N) {
+        if (done) {
 #pragma unroll
           for (int m = 0; m < GV_N; ++m)
-            if (m < p.M) {
-              const float sum = __uint_as_float(v[m]) + __ldcg(other + m * BM + col);
-              p.y[static_cast<int64_t>(m) * p.ldy + n] = gv_out<kE>(p.epi, m, n, sum, alpha, bias);
-            }
-        }
-        continue;
-      }
-#pragma unroll
-      for (int m = 0; m < GV_N; ++m)
-        if (m < p.M) mine[m * BM + col] = __uint_as_float(v[m]);
-      __threadfence();
-      __syncwarp();
-      int arrived = 0;
-      if (lane == 0) arrived = atomicAdd(counter, 1);
-      arrived = __shfl_sync(0xFFFFFFFFu, arrived, 0);
-      if (arrived == 1) {                                       // second of the two: finish
-        __threadfence();
-        if (n < p.N) {
-#pragma unroll
-          for (int m = 0; m < GV_N; ++m)
-            if (m < p.M) {
-              const float sum = __uint_as_float(v[m]) + __ldcg(other + m * BM + col);
-              p.y[static_cast<int64_t>(m) * p.ldy + n] = gv_out<kE>(p.epi, m, n, sum, alpha, bias);
-            }
+            if (m < p.M) v[m] = __float_as_uint(__uint_as_float(v[m]) + __ldcg(other + m * BM + col));
         }
       }
+      if (done) gv_store<kE, GV_N>(p.epi, p.y, p.ldy, p.M, n, p.N, col, v, alpha, bias, res, slots);
     }
   }
 
@@ -466,7 +486,9 @@ constexpr int GF_XIMG_BYTES = (GF_MAX_K / BK) * 1024;             // 8 rows x 12
 constexpr int GF_XSF_BYTES = (GF_MAX_K / MMA_K) * 128;            // 8 rows x 16 B per MMA-K step
 constexpr int GF_SMEM_BYTES = GF_STAGES * GF_STAGE_BYTES + GF_XIMG_BYTES + GF_XSF_BYTES + 1024 + 512 + 1024;
 constexpr int GF_QTHREADS = GF_QWARPS * 32;
-static_assert(GF_SMEM_BYTES <= 227 * 1024, "shared memory budget");
+constexpr int GF_OUT_BYTES = GF_MAX_M * BM * static_cast<int>(sizeof(float2));
+static_assert(GF_SMEM_BYTES + GF_OUT_BYTES <= 227 * 1024 && GV_SMEM_BYTES + GV_OUT_BYTES <= 227 * 1024,
+              "shared memory budget");
 static_assert((GF_MAX_M * GF_BLOCKS) % 2 == 0, "blocks are quantized in pairs");
 
 struct GemvFusedParams {
@@ -719,6 +741,7 @@ __global__ void __launch_bounds__(GF_THREADS, 1)
     // ---- epilogue and stream-K fix-up (warps 2..5; as gemv_kernel, tagged counters) ----
     if (warp < 2 + GV_EPI_WARPS) {
     const int quad = warp & 3;
+    float2* slots = reinterpret_cast<float2*>(smem + GF_SMEM_BYTES - 1024);        // kE: past what the ring takes
     const float alpha = __fdiv_rn(1.0f, __fmul_rn(*p.g_w, valid ? g : 0.0f));
     const int cta = blockIdx.x;
     int acc = 0;
@@ -731,6 +754,11 @@ __global__ void __launch_bounds__(GF_THREADS, 1)
       const bool has_head = u == tile_begin;
       const bool has_tail = seg_end == tile_begin + p.num_kt;
       u = seg_end;
+      const int col = quad * 32 + lane;                         // row of the weight tile
+      const int n = tile * BM + col;                            // output column
+      const float bias = gv_bias<kE>(p.epi, n, p.N);
+      float res[GF_MAX_M];
+      gv_residual<kE, GF_MAX_M>(p.epi, p.M, n, p.N, res);
       if (!mbar_wait_bounded(&acc_full[acc], acc_phase, abort_flag, p.wait_limit_ns, p.status)) break;
       tc_fence_after();
       uint32_t v[32];
@@ -743,82 +771,55 @@ __global__ void __launch_bounds__(GF_THREADS, 1)
         acc = 0;
         acc_phase ^= 1;
       }
-      const int col = quad * 32 + lane;
-      const int n = tile * BM + col;
-      const float bias = gv_bias<kE>(p.epi, n, p.N);
-      if (has_head && has_tail) {
-        if (n < p.N) {
+      bool done = has_head && has_tail;                         // v holds the tile's whole sum
+      unsigned long long* counter = &p.counters[tile * 4 + quad];
+      const bool counted = !done;                               // its counter returns to zero when the tile is done
+      if (kE && p.split > 1) {
+        float* slot = p.partials + static_cast<int64_t>(blockIdx.x) * p.M * BM;
 #pragma unroll
-          for (int m = 0; m < GF_MAX_M; ++m)
-            if (m < p.M) p.y[static_cast<int64_t>(m) * p.ldy + n] = gv_out<kE>(p.epi, m, n, __uint_as_float(v[m]), alpha, bias);
+        for (int m = 0; m < GF_MAX_M; ++m)
+          if (m < p.M) slot[m * BM + col] = __uint_as_float(v[m]);
+        __threadfence();
+        __syncwarp();
+        int arrived = 0;
+        if (lane == 0) arrived = tagged_arrive(counter, p.tag);
+        arrived = __shfl_sync(0xFFFFFFFFu, arrived, 0);
+        if (arrived == p.split - 1) {
+          __threadfence();
+          gv_join_parts<GF_MAX_M>(p.partials, p.split, p.M, col, v);
+          done = true;
         }
-        continue;
-      }
-      if constexpr (kE) {
-        if (p.split > 1) {
-          float* slot = p.partials + static_cast<int64_t>(blockIdx.x) * p.M * BM;
-          unsigned long long* count = &p.counters[tile * 4 + quad];
+      } else if (!done) {
+        float* mine = p.partials + (static_cast<int64_t>(2 * cta + (has_head ? 1 : 0)) * p.M) * BM;
+        const float* other = p.partials + (static_cast<int64_t>(has_head ? 2 * (cta + 1) : 2 * (cta - 1) + 1) * p.M) * BM;
+        // one load for the warp (lane 0's acquire, broadcast), so all lanes take
+        // the same branch; __syncwarp orders the other lanes' reads after it
+        unsigned long long seen = 0;
+        if (lane == 0) seen = ld_acquire_gpu_u64(counter);
+        seen = __shfl_sync(0xFFFFFFFFu, seen, 0);
+        __syncwarp();
+        done = (seen >> 16) == p.tag && (seen & 0xFFFFull) >= 1ull;
+        if (!done) {
 #pragma unroll
           for (int m = 0; m < GF_MAX_M; ++m)
-            if (m < p.M) slot[m * BM + col] = __uint_as_float(v[m]);
+            if (m < p.M) mine[m * BM + col] = __uint_as_float(v[m]);
           __threadfence();
           __syncwarp();
           int arrived = 0;
-          if (lane == 0) arrived = tagged_arrive(count, p.tag);
+          if (lane == 0) arrived = tagged_arrive(counter, p.tag);
           arrived = __shfl_sync(0xFFFFFFFFu, arrived, 0);
-          if (arrived == p.split - 1) {
-            __threadfence();
-            gv_join_parts<GF_MAX_M>(p.partials, p.split, p.M, col, v);
-            if (n < p.N) {
-#pragma unroll
-              for (int m = 0; m < GF_MAX_M; ++m)
-                if (m < p.M) p.y[static_cast<int64_t>(m) * p.ldy + n] = gv_out<kE>(p.epi, m, n, __uint_as_float(v[m]), alpha, bias);
-            }
-            if (lane == 0) *reinterpret_cast<volatile unsigned long long*>(count) = 0ull;   // tile done: reset
-          }
-          continue;
+          done = arrived == 1;
+          if (done) __threadfence();
         }
-      }
-      float* mine = p.partials + (static_cast<int64_t>(2 * cta + (has_head ? 1 : 0)) * p.M) * BM;
-      const float* other = p.partials + (static_cast<int64_t>(has_head ? 2 * (cta + 1) : 2 * (cta - 1) + 1) * p.M) * BM;
-      unsigned long long* counter = &p.counters[tile * 4 + quad];
-      // one load for the warp (lane 0's acquire, broadcast), so all lanes take
-      // the same branch; __syncwarp orders the other lanes' reads after it
-      unsigned long long seen = 0;
-      if (lane == 0) seen = ld_acquire_gpu_u64(counter);
-      seen = __shfl_sync(0xFFFFFFFFu, seen, 0);
-      __syncwarp();
-      if ((seen >> 16) == p.tag && (seen & 0xFFFFull) >= 1ull) {
-        if (n < p.N) {
+        if (done) {
 #pragma unroll
           for (int m = 0; m < GF_MAX_M; ++m)
-            if (m < p.M) {
-              const float sum = __uint_as_float(v[m]) + __ldcg(other + m * BM + col);
-              p.y[static_cast<int64_t>(m) * p.ldy + n] = gv_out<kE>(p.epi, m, n, sum, alpha, bias);
-            }
+            if (m < p.M) v[m] = __float_as_uint(__uint_as_float(v[m]) + __ldcg(other + m * BM + col));
         }
-        if (lane == 0) *reinterpret_cast<volatile unsigned long long*>(counter) = 0ull;   // tile done: reset
-        continue;
       }
-#pragma unroll
-      for (int m = 0; m < GF_MAX_M; ++m)
-        if (m < p.M) mine[m * BM + col] = __uint_as_float(v[m]);
-      __threadfence();
-      __syncwarp();
-      int arrived = 0;
-      if (lane == 0) arrived = tagged_arrive(counter, p.tag);
-      arrived = __shfl_sync(0xFFFFFFFFu, arrived, 0);
-      if (arrived == 1) {
-        __threadfence();
-        if (n < p.N) {
-#pragma unroll
-          for (int m = 0; m < GF_MAX_M; ++m)
-            if (m < p.M) {
-              const float sum = __uint_as_float(v[m]) + __ldcg(other + m * BM + col);
-              p.y[static_cast<int64_t>(m) * p.ldy + n] = gv_out<kE>(p.epi, m, n, sum, alpha, bias);
-            }
-        }
-        if (lane == 0) *reinterpret_cast<volatile unsigned long long*>(counter) = 0ull;   // tile done: reset
+      if (done) {
+        gv_store<kE, GF_MAX_M>(p.epi, p.y, p.ldy, p.M, n, p.N, col, v, alpha, bias, res, slots);
+        if (counted && lane == 0) *reinterpret_cast<volatile unsigned long long*>(counter) = 0ull;   // tile done: reset
       }
     }
     }
@@ -1087,9 +1088,10 @@ static nvfp4_status launch_gemv_fused(const void* x, int64_t M, int64_t ldx, con
   p.split = gemv_split(epi, tiles, sms < GV_MAX_CTAS ? sms : GV_MAX_CTAS, p.num_kt);
   if (p.split > 1) grid = tiles * p.split;
   auto kern = epi ? gemv_fused_kernel<true> : gemv_fused_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GF_SMEM_BYTES);
+  const int smem = GF_SMEM_BYTES + (epi ? GF_OUT_BYTES : 0);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return launch_status(e);
-  kern<<<grid, GF_THREADS, GF_SMEM_BYTES, s>>>(tmW, p);
+  kern<<<grid, GF_THREADS, smem, s>>>(tmW, p);
   return launch_status(cudaGetLastError());
 }
 
@@ -1158,12 +1160,13 @@ nvfp4_status launch_gemv(const void* x, int64_t M, int64_t ldx, const void* w_co
   p.split = gemv_split(epi, tiles, sms < GV_MAX_CTAS ? sms : GV_MAX_CTAS, p.num_kt);
   if (p.split > 1) grid = tiles * p.split;
   auto kern = epi ? gemv_kernel<true> : gemv_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GV_SMEM_BYTES);
+  const int smem = GV_SMEM_BYTES + (epi ? GV_OUT_BYTES : 0);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return launch_status(e);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(GV_THREADS);
-  cfg.dynamicSmemBytes = GV_SMEM_BYTES;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
