@@ -20,7 +20,9 @@ constexpr int EB_THREADS = 256;
 constexpr int EB_WARPS = EB_THREADS / 32;
 constexpr int EB_BLOCKS_PER_SM = 3;
 constexpr int EB_MAX_CHUNKS = 64;
-constexpr int EB_MAX_BLOCKS = 640;     // of a grid whose columns alone need fewer; a workspace is sized for it
+constexpr int EB_MAX_BLOCKS = 4096;    // of a grid whose columns alone need fewer; a workspace is sized for it
+constexpr int EO_COLS = 4;             // columns of a thread whose rows start anywhere, 32 apart
+constexpr int EO_BLOCKS_PER_SM = 3;
 
 struct EpiBwdParams {
   const void* dd;
@@ -147,56 +149,66 @@ __global__ void __launch_bounds__(EB_THREADS, EB_BLOCKS_PER_SM) epilogue_backwar
   publish_block_mag(p, mag.bits(), warp_mags);
 }
 
-// Rows that start anywhere: a thread takes one column, a warp's accesses are
-// 32 neighbouring elements; U rows' loads in flight.
+// Rows that start anywhere: a thread takes EO_COLS columns 32 apart, a warp's
+// accesses are 32 neighbouring elements; EO_COLS x U elements' loads in flight.
 template <typename T, int kAct>
-__global__ void __launch_bounds__(EB_THREADS) epilogue_backward_odd_kernel(const EpiBwdParams p) {
-  constexpr int U = 8;
-  __shared__ float sums[EB_WARPS][32];
+__global__ void __launch_bounds__(EB_THREADS, EO_BLOCKS_PER_SM) epilogue_backward_odd_kernel(const EpiBwdParams p) {
+  constexpr int U = 4;
+  __shared__ float sums[EB_WARPS][EO_COLS][32];
   __shared__ uint32_t warp_mags[EB_WARPS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
+  const int c0 = blockIdx.x * (32 * EO_COLS) + lane;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * p.rows_per_chunk;
   const int64_t r1 = min(p.M, r0 + p.rows_per_chunk);
-  const T* dd = static_cast<const T*>(p.dd) + c;
-  const T* pre = static_cast<const T*>(p.pre) + c;
-  T* dpre = static_cast<T*>(p.dpre) + c;
-  float s = 0.0f;
+  const T* dd = static_cast<const T*>(p.dd) + c0;
+  const T* pre = static_cast<const T*>(p.pre) + c0;
+  T* dpre = static_cast<T*>(p.dpre) + c0;
+  float s[EO_COLS];
+  bool in[EO_COLS];
+#pragma unroll
+  for (int j = 0; j < EO_COLS; ++j) s[j] = 0.0f, in[j] = c0 + 32 * j < p.N;
   uint32_t mag = 0;
-  if (c < p.N) {
-    for (int64_t r = r0 + warp; r < r1; r += U * EB_WARPS) {
-      float a[U], b[U];
+  for (int64_t r = r0 + warp; r < r1; r += U * EB_WARPS) {
+    T a[U][EO_COLS], b[U][EO_COLS];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t q = r + u * EB_WARPS;
-        a[u] = q < r1 ? to_f32(dd[q * p.ldd]) : 0.0f;
-        b[u] = kAct != NVFP4_ACT_NONE && q < r1 ? to_f32(pre[q * p.ldp]) : 0.0f;
+    for (int u = 0; u < U; ++u) {
+      const int64_t q = r + u * EB_WARPS;
+#pragma unroll
+      for (int j = 0; j < EO_COLS; ++j) {
+        const bool on = in[j] && q < r1;
+        a[u][j] = on ? dd[q * p.ldd + 32 * j] : from_f32<T>(0.0f);
+        b[u][j] = kAct != NVFP4_ACT_NONE && on ? pre[q * p.ldp + 32 * j] : from_f32<T>(0.0f);
       }
+    }
 #pragma unroll
-      for (int u = 0; u < U; u += 2) {
-        float2 d = make_float2(a[u], a[u + 1]);
-        if constexpr (kAct != NVFP4_ACT_NONE) d = mul2(d, slope_pair<kAct>(make_float2(b[u], b[u + 1])));
+    for (int u = 0; u < U; ++u) {
+      const int64_t q = r + u * EB_WARPS;
+      if (q >= r1) break;
+#pragma unroll
+      for (int j = 0; j < EO_COLS; j += 2) {
+        float2 d = make_float2(to_f32(a[u][j]), to_f32(a[u][j + 1]));
+        if constexpr (kAct != NVFP4_ACT_NONE) d = mul2(d, slope_pair<kAct>(make_float2(to_f32(b[u][j]), to_f32(b[u][j + 1]))));
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int64_t q = r + (u + h) * EB_WARPS;
+          if (!in[j + h]) continue;
           const float v = h ? d.y : d.x;
-          if (q < r1) {
-            s += v;
-            const T o = from_f32<T>(v);
-            if (p.dpre) dpre[q * p.lddp] = o;
-            mag = max(mag, mag_bits(o));
-          }
+          s[j + h] += v;
+          const T o = from_f32<T>(v);
+          if (p.dpre) dpre[q * p.lddp + 32 * (j + h)] = o;
+          mag = max(mag, mag_bits(o));
         }
       }
     }
   }
   if (p.partial) {
-    sums[warp][lane] = s;
-    __syncthreads();
-    if (warp == 0 && c < p.N) {
 #pragma unroll
-      for (int w = 1; w < EB_WARPS; ++w) s += sums[w][lane];
-      p.partial[static_cast<int64_t>(blockIdx.y) * p.N + c] = s;
+    for (int j = 0; j < EO_COLS; ++j) sums[warp][j][lane] = s[j];
+    __syncthreads();
+    if (warp < EO_COLS && c0 + 32 * warp < p.N) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < EB_WARPS; ++w) sum += sums[w][warp][lane];
+      p.partial[static_cast<int64_t>(blockIdx.y) * p.N + c0 + 32 * warp] = sum;
     }
   }
   publish_block_mag(p, mag, warp_mags);
@@ -221,9 +233,28 @@ void launch_act(const EpiBwdParams& p, bool vec, dim3 grid, cudaStream_t s) {
   }
 }
 
+// Chunks of rows: the fewest whose blocks fill the last wave of SMs to within a
+// few percent (4096 x 28672, 112 strips: one wave of three chunks leaves a
+// quarter of the SMs idle), each of at least two rows per warp.
+int64_t chunk_count(int64_t strips, int64_t M, bool vec) {
+  const int64_t slots = static_cast<int64_t>(device_sm_count()) * (vec ? EB_BLOCKS_PER_SM : EO_BLOCKS_PER_SM);
+  int64_t most = EB_MAX_BLOCKS / strips;
+  const int64_t by_rows = (M + 2 * EB_WARPS - 1) / (2 * EB_WARPS);
+  if (most > by_rows) most = by_rows;
+  if (most > EB_MAX_CHUNKS) most = EB_MAX_CHUNKS;
+  int64_t best = 1;
+  double best_fill = 0.0;
+  for (int64_t c = 1; c <= most; ++c) {
+    const int64_t blocks = strips * c, waves = (blocks + slots - 1) / slots;
+    const double fill = static_cast<double>(blocks) / static_cast<double>(waves * slots);
+    if (fill > best_fill + 0.02) best = c, best_fill = fill;
+  }
+  return best;
+}
+
 // Most blocks that a grid for N columns has.
 int64_t most_blocks(int64_t N) {
-  const int64_t strips = (N + 31) / 32;                    // the narrower strips
+  const int64_t strips = (N + 32 * EO_COLS - 1) / (32 * EO_COLS);     // the narrower strips
   return strips > EB_MAX_BLOCKS ? strips : EB_MAX_BLOCKS;
 }
 
@@ -248,14 +279,9 @@ nvfp4_status launch_epilogue_backward(const EpilogueBackward& a, cudaStream_t s)
   const auto aligned = [&](const void* q, int64_t ld) { return aligned16(q) && (ld * (f32 ? 4 : 2)) % 16 == 0; };
   const bool vec = a.N % 8 == 0 && aligned(a.dd, a.ldd) && (a.act == NVFP4_ACT_NONE || aligned(a.pre, a.ldp)) &&
                    (!a.dpre || aligned(a.dpre, a.lddp));
-  // one wave of blocks; chunks of at least one row per warp
-  const int width = vec ? 256 : 32;
+  const int width = vec ? 256 : 32 * EO_COLS;
   const int64_t strips = (a.N + width - 1) / width;
-  const int64_t slots = static_cast<int64_t>(device_sm_count()) * (vec ? EB_BLOCKS_PER_SM : 4);
-  int64_t chunks = (slots < EB_MAX_BLOCKS ? slots : EB_MAX_BLOCKS) / strips;
-  if (chunks > EB_MAX_CHUNKS) chunks = EB_MAX_CHUNKS;
-  if (chunks > (a.M + EB_WARPS - 1) / EB_WARPS) chunks = (a.M + EB_WARPS - 1) / EB_WARPS;
-  if (chunks < 1) chunks = 1;
+  int64_t chunks = chunk_count(strips, a.M, vec);
   const int64_t per = (a.M + chunks - 1) / chunks;
   chunks = (a.M + per - 1) / per;
   EpiBwdParams p{a.dd, a.ldd, a.pre, a.ldp, a.act, a.dpre, a.lddp,

@@ -123,20 +123,26 @@ __device__ __forceinline__ void gv_range(int split, int units, int num_kt, int& 
   u_end = static_cast<int>(static_cast<int64_t>(units) * (blockIdx.x + 1) / gridDim.x);
 }
 
-// The parts of a tile in order, this block's from its registers, the others'
-// from their slots: acc becomes the sum (M rows of MAX_M).
+// The parts of a tile, added in order from their slots: acc becomes the sum (M
+// rows of MAX_M).  Two parts' loads are in flight at a time.
 template <int MAX_M>
 __device__ __forceinline__ void gv_join_parts(const float* partials, int split, int M, int col, uint32_t (&acc)[32]) {
-  const int part = static_cast<int>(blockIdx.x) % split;
-  const float* first = partials + static_cast<int64_t>(blockIdx.x - part) * M * BM + col;
+  const float* slot = partials + static_cast<int64_t>(blockIdx.x - blockIdx.x % split) * M * BM + col;
   float sum[MAX_M];
 #pragma unroll
   for (int m = 0; m < MAX_M; ++m) sum[m] = 0.0f;
-  for (int i = 0; i < split; ++i) {
-    const float* slot = first + static_cast<int64_t>(i) * M * BM;
+#pragma unroll 1
+  for (int i = 0; i < split; i += 2) {
+    float x[MAX_M], y[MAX_M];
+    const float* next = slot + static_cast<int64_t>(M) * BM;
 #pragma unroll
-    for (int m = 0; m < MAX_M; ++m)
-      if (m < M) sum[m] += i == part ? __uint_as_float(acc[m]) : __ldcg(slot + m * BM);
+    for (int m = 0; m < MAX_M; ++m) {
+      x[m] = m < M ? __ldcg(slot + m * BM) : 0.0f;
+      y[m] = m < M && i + 1 < split ? __ldcg(next + m * BM) : 0.0f;
+    }
+#pragma unroll
+    for (int m = 0; m < MAX_M; ++m) sum[m] = (sum[m] + x[m]) + y[m];
+    slot = next + static_cast<int64_t>(M) * BM;
   }
 #pragma unroll
   for (int m = 0; m < MAX_M; ++m) acc[m] = __float_as_uint(sum[m]);
@@ -1044,16 +1050,17 @@ static GemvEpi gemv_epi(const Epilogue* e) {
   return GemvEpi{e->bias, e->bias_f32, e->act, static_cast<const __nv_bfloat16*>(e->residual), e->ldr};
 }
 
-// Parts per tile of an epilogue GEMV: as many as give every SM a block, at most
-// GV_MAX_SPLIT (the last block reads the others' parts one after another), each
-// of at least one K stage.
-constexpr int GV_MAX_SPLIT = 8;
+// Parts per tile of an epilogue GEMV: as many as give every SM a block, each of
+// at least GV_PART_STAGES K stages (8192 x 8192, M = 16: 15.4 us against 18.2 with
+// one block per tile; 4096 x 8192, M = 1: 11.5 against 16.5; parts of 4 stages
+// cost the join half a microsecond more than they save, parts of 16 leave SMs idle:
+// 1024 x 8192, M = 1: 12.0, 11.5 and 13.1 us with 4, 8 and 16).
+constexpr int GV_PART_STAGES = 8;
 static int gemv_split(const Epilogue* epi, int tiles, int sms, int64_t num_kt) {
   if (!epi) return 1;
-  int split = sms / tiles;
-  if (split > GV_MAX_SPLIT) split = GV_MAX_SPLIT;
-  if (split > num_kt) split = static_cast<int>(num_kt);
-  return split > 1 ? split : 1;
+  int64_t split = sms / tiles;
+  if (split > num_kt / GV_PART_STAGES) split = num_kt / GV_PART_STAGES;
+  return split > 1 ? static_cast<int>(split) : 1;
 }
 
 static nvfp4_status launch_gemv_fused(const void* x, int64_t M, int64_t ldx, const void* w_codes, const void* w_sf,
