@@ -67,7 +67,7 @@ template <int BN_, bool kMx, bool kE = false>
 struct GemmCfg {
   using F = ScaleFmt<kMx>;
   static constexpr int BN = BN_;
-  // kE: one stage makes room for the epilogue's boxes (4 KB per epilogue warp)
+  // kE: one stage makes room for the epilogue's boxes (4 KB and the bias per epilogue warp)
   static constexpr int STAGES = ((BN == 256) ? 4 : 6) - (kE ? 1 : 0);
   static constexpr int A_BYTES = BM * BK_BYTES;
   static constexpr int B_BYTES = BN * BK_BYTES;
@@ -81,7 +81,7 @@ struct GemmCfg {
   static constexpr int EPI_WARPS = 8;
   static constexpr int THREADS = (2 + EPI_WARPS) * 32;
   static constexpr int BAR_BYTES = 256;
-  static constexpr int BOX_BYTES = kE ? EPI_WARPS * 32 * 32 * 4 : 0;
+  static constexpr int BOX_BYTES = kE ? EPI_WARPS * (32 * 32 * 4 + BN / 2 * 4) : 0;      // a box and the bias per warp
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + BOX_BYTES + BAR_BYTES + 1024;
   static_assert(TMEM_SF_BASE + STAGES * SF_COLS_PER_STAGE <= (int)TMEM_COLS, "TMEM budget");
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
@@ -381,21 +381,38 @@ __device__ __forceinline__ void box_rows_in(uint8_t* box, const void* base, int6
   }
 }
 
-// x = alpha acc + bias of a box; lane l holds the bias of column col + l.
-__device__ __forceinline__ void box_values(const uint32_t* v, float alpha, bool has_bias, float bias, BoxRow& x) {
+// x = alpha acc + bias of a box; bias: its 32 values in shared memory (16-byte
+// reads that every lane shares; lane-to-lane shuffles instead took 10 us of a
+// 4096 x 8192 x 1024 call's 47), or null.
+__device__ __forceinline__ void box_values(const uint32_t* v, float alpha, const float* bias, BoxRow& x) {
 #pragma unroll
-  for (int i = 0; i < EPI_BOX / 2; ++i) {
-    x[i] = make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-    if (has_bias)
-      x[i] = fma2(x[i], both(alpha),
-                  make_float2(__shfl_sync(0xFFFFFFFFu, bias, 2 * i), __shfl_sync(0xFFFFFFFFu, bias, 2 * i + 1)));
-    else
-      x[i] = mul2(x[i], both(alpha));
+  for (int i = 0; i < EPI_BOX / 4; ++i) {
+    const float2 lo = make_float2(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]));
+    const float2 hi = make_float2(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+    if (bias) {
+      const float4 b = *reinterpret_cast<const float4*>(bias + 4 * i);
+      x[2 * i] = fma2(lo, both(alpha), make_float2(b.x, b.y));
+      x[2 * i + 1] = fma2(hi, both(alpha), make_float2(b.z, b.w));
+    } else {
+      x[2 * i] = mul2(lo, both(alpha));
+      x[2 * i + 1] = mul2(hi, both(alpha));
+    }
   }
 }
-__device__ __forceinline__ float box_bias(const GemmParams& p, int col) {
-  const int c = col + static_cast<int>(threadIdx.x & 31);
-  return p.bias && c < p.N ? load_param(p.bias, p.bias_f32, c) : 0.0f;
+// The bias of a warp's NV columns from col0, into its place in shared memory
+// (before the accumulator is waited for; a __syncwarp lies between here and
+// box_values).
+template <int NV>
+__device__ __forceinline__ void bias_in(const GemmParams& p, int col0, float* bias) {
+  if (!p.bias) return;
+  float b[NV / 32];
+#pragma unroll
+  for (int i = 0; i < NV / 32; ++i) {
+    const int c = col0 + 32 * i + static_cast<int>(threadIdx.x & 31);
+    b[i] = c < p.N ? load_param(p.bias, p.bias_f32, c) : 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < NV / 32; ++i) bias[32 * i + (threadIdx.x & 31)] = b[i];
 }
 
 // Largest stored magnitude of this thread's row, columns below n_valid.
@@ -409,12 +426,12 @@ __device__ __forceinline__ void box_mag(const BoxRow& x, int n_valid, uint32_t& 
 // One box of any type and alignment; `box`: EPI_ROWS_BYTES of this warp.
 template <typename T>
 __device__ __forceinline__ void store_box_rows(const GemmParams& p, uint8_t* box, int row0, int col, const uint32_t* v,
-                                               float alpha, float bias, uint32_t& mag) {
+                                               float alpha, const float* bias, uint32_t& mag) {
   const int lane = threadIdx.x & 31;
   const int rows = min(EPI_BOX, p.M - row0);
   const bool in = col + lane < p.N;
   BoxRow x;
-  box_values(v, alpha, p.bias != nullptr, bias, x);
+  box_values(v, alpha, p.bias ? bias : nullptr, x);
   if (p.pre) {
     box_put<T>(box, lane, x);
     __syncwarp();
@@ -435,21 +452,14 @@ __device__ __forceinline__ void store_box_rows(const GemmParams& p, uint8_t* box
   if (lane < rows) box_mag<T>(x, p.N - col, mag);
 }
 
-// NV columns (held in v, a row per thread) from column col0, box by box.
-template <int NV>
-__device__ __forceinline__ void store_rows_epi(const GemmParams& p, uint8_t* box, int row0, int col0,
-                                               const uint32_t (&v)[NV], float alpha, uint32_t& mag) {
-  if (row0 >= p.M) return;
-#pragma unroll
-  for (int c = 0; c < NV / EPI_BOX; ++c) {
-    const int col = col0 + c * EPI_BOX;
-    if (col >= p.N) break;
-    const float bias = box_bias(p, col);
-    if (p.out_f32)
-      store_box_rows<float>(p, box, row0, col, v + c * EPI_BOX, alpha, bias, mag);
-    else
-      store_box_rows<__nv_bfloat16>(p, box, row0, col, v + c * EPI_BOX, alpha, bias, mag);
-  }
+// A box at column col (a row per thread in v) by rows; bias: its 32 values.
+__device__ __forceinline__ void store_box_epi(const GemmParams& p, uint8_t* box, int row0, int col,
+                                              const uint32_t (&v)[EPI_BOX], float alpha, const float* bias, uint32_t& mag) {
+  if (row0 >= p.M || col >= p.N) return;
+  if (p.out_f32)
+    store_box_rows<float>(p, box, row0, col, v, alpha, bias, mag);
+  else
+    store_box_rows<__nv_bfloat16>(p, box, row0, col, v, alpha, bias, mag);
 }
 
 __device__ __forceinline__ void publish_mag(const GemmParams& p, uint32_t mag) {
@@ -632,10 +642,32 @@ __global__ void __launch_bounds__(GemmCfg<BN, kMx>::THREADS, 1)
     for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
       const int tm = t % p.tiles_m;
       const int tn = t / p.tiles_m;
+      [[maybe_unused]] float* bias = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE_BYTES + 8 * EPI_ROWS_BYTES) + ew * HALF;
+      if constexpr (kE) bias_in<HALF>(p, tn * BN + half * HALF, bias);
       if (!mbar_wait_bounded(&acc_full[acc], acc_phase, abort_flag, p.wait_limit_ns, p.status)) break;
       tc_fence_after();
-      uint32_t v[HALF];
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * BN + half * HALF;
+      if constexpr (kE) {
+        // box by box in a loop: the epilogue's code is long, and straight-line
+        // copies of it per box spent more on fetching instructions than on them
+#pragma unroll 1
+        for (int c = 0; c < HALF; c += EPI_BOX) {
+          uint32_t w[EPI_BOX];
+          tmem_ld_32x32b_x32(taddr + c, w);
+          tmem_ld_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (c + EPI_BOX == HALF && lane == 0) mbar_arrive(&acc_empty[acc]);
+          store_box_epi(p, smem + C::STAGES * C::STAGE_BYTES + ew * EPI_ROWS_BYTES, tm * BM + quad * 32,
+                        tn * BN + half * HALF + c, w, alpha, bias + c, mag);
+        }
+        if (++acc == C::ACC_BUFS) {
+          acc = 0;
+          acc_phase ^= 1;
+        }
+        continue;
+      }
+      uint32_t v[HALF];
 #pragma unroll
       for (int c = 0; c < HALF / 32; ++c) tmem_ld_32x32b_x32(taddr + c * 32, v + c * 32);
       tmem_ld_wait();
@@ -649,9 +681,7 @@ __global__ void __launch_bounds__(GemmCfg<BN, kMx>::THREADS, 1)
       const int row = tm * BM + quad * 32 + lane;
       const int col0 = tn * BN + half * HALF;
       if (col0 < p.N) {
-        if constexpr (kE)
-          store_rows_epi<HALF>(p, smem + C::STAGES * C::STAGE_BYTES + ew * EPI_ROWS_BYTES, row - lane, col0, v, alpha, mag);
-        else if (p.out_q)
+        if (p.out_q)
           store_row_q<HALF>(p, row, col0, v, alpha, gd, amax_run);
         else
           store_row<HALF>(p, row, col0, v, alpha);
@@ -715,7 +745,8 @@ struct PairCfg {
   static constexpr int EPI_BOX_BYTES = 32 * EPI_BOX_COLS * 2;
   static constexpr int EPI_BOXES = kE ? 4 : 2;         // per warp (kE: residual in and D out, pre; or two fp32 boxes)
   static constexpr int EPI_BYTES = EPI_WARPS * EPI_BOXES * EPI_BOX_BYTES;
-  static constexpr int RES_BAR_BYTES = kE ? EPI_WARPS * EPI_BOXES * 8 : 0;   // one mbarrier per residual box
+  // one mbarrier per residual box, and the bias of each warp's 128 columns
+  static constexpr int RES_BAR_BYTES = kE ? EPI_WARPS * (EPI_BOXES * 8 + 128 * 4) : 0;
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_BYTES + 256 + RES_BAR_BYTES + 1024;
   // Quantize-and-GEMM kernel: QA_WARPS more warps quantize A's rows; the
   // E4M3 scale table takes 1 KB more.
@@ -854,9 +885,10 @@ struct NoMaps {};
 //   steps' fetched when the store that reads the box is done.  pre: boxes 2, 3.
 struct EpiWriter {
   uint8_t* boxes;
+  float* bias;               // of the warp's 128 columns
   uint64_t* bars;            // arrivals of residual boxes
   Mag<__nv_bfloat16> mag;    // |D| of box()
-  uint32_t mag_rows = 0;     // |D| of store_rows_epi()
+  uint32_t mag_rows = 0;     // |D| of store_box_epi()
   uint32_t parity = 0;       // of bars[0..3]
   uint32_t pending = 0;      // residual boxes fetched and not waited for
   int row0 = 0, col0 = 0, first = 0;
@@ -874,11 +906,9 @@ struct EpiWriter {
     }
   }
 
-  __device__ __forceinline__ void start(const GemmParams& p, const EpiMaps& m, int row, int column, int shared_first,
-                                        float (&bias)[4]) {
+  __device__ __forceinline__ void start(const GemmParams& p, const EpiMaps& m, int row, int column, int shared_first) {
     row0 = row, col0 = column, first = shared_first;
-#pragma unroll
-    for (int s = 0; s < 4; ++s) bias[s] = box_bias(p, col(s));
+    bias_in<4 * EPI_BOX>(p, col0, bias);
     if (p.tma_store && p.res && row0 < p.M) {
       if ((threadIdx.x & 31) == 0) bulk_wait_group_read<0>();     // the last tile's boxes have left
       fetch(p, m, 0, 0);
@@ -891,13 +921,13 @@ struct EpiWriter {
   }
 
   __device__ __forceinline__ void box(const GemmParams& p, const CUtensorMap& d, const EpiMaps& m, int s, const uint32_t* v,
-                                      float alpha, float bias, volatile int* abort_flag) {
+                                      float alpha, volatile int* abort_flag) {
     const int lane = threadIdx.x & 31;
     const int c = col(s);
     if (row0 >= p.M || c >= p.N) return;
     const int buf = p.res && !p.pre ? s : s & 1, pre_buf = 2 + (s & 1);
     BoxRow x;
-    box_values(v, alpha, p.bias != nullptr, bias, x);
+    box_values(v, alpha, p.bias ? bias + (c - col0) : nullptr, x);
     if (!p.res) {
       if (lane == 0) bulk_wait_group_read<1>();                   // the step before last has left its boxes
       __syncwarp();
@@ -1216,7 +1246,9 @@ __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>:
     }
     const float gd = kQ ? *p.g_d : 0.0f;
     float amax_run = 0.0f;
-    [[maybe_unused]] EpiWriter ep{epi_smem + ew * C::EPI_BOXES * C::EPI_BOX_BYTES, res_bar + ew * C::EPI_BOXES};
+    [[maybe_unused]] EpiWriter ep{epi_smem + ew * C::EPI_BOXES * C::EPI_BOX_BYTES,
+                                  reinterpret_cast<float*>(res_bar + C::EPI_WARPS * C::EPI_BOXES) + ew * HALF,
+                                  res_bar + ew * C::EPI_BOXES};
     const uint32_t acc_empty_leader = mapa_shared(smem_u32(acc_empty), 0);
     const uint32_t ovl_free_leader = mapa_shared(smem_u32(ovl_free), 0);
     int j = 0;
@@ -1229,9 +1261,8 @@ __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>:
         tm = t % tiles_m;
         tn = t / tiles_m;
       }
-      [[maybe_unused]] float bias[4];
       if constexpr (kE) ep.start(p, tmE, tm * 256 + static_cast<int>(rank) * 128 + quad * 32, tn * C::BN + half * HALF,
-                                 b == 0 && half == 1 ? 64 : 0, bias);
+                                 b == 0 && half == 1 ? 64 : 0);
       if (!mbar_wait_bounded(&acc_full[b], static_cast<uint32_t>(j >> 1) & 1u, abort_flag, p.wait_limit_ns, p.status)) break;
       tc_fence_after();
       uint32_t v[HALF];
@@ -1255,10 +1286,18 @@ __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>:
             if (part == 1) mbar_arrive_cluster_relaxed(acc_empty_leader + 8u * b);
           }
           if (p.tma_store) {
-            ep.box(p, tmD, tmE, 2 * part, w, alpha, part ? bias[2] : bias[0], abort_flag);
-            ep.box(p, tmD, tmE, 2 * part + 1, w + 32, alpha, part ? bias[3] : bias[1], abort_flag);
-          } else {
-            store_rows_epi<64>(p, ep.boxes, ep.row0, tn * C::BN + half * HALF + c_off, w, alpha, ep.mag_rows);
+            ep.box(p, tmD, tmE, 2 * part, w, alpha, abort_flag);
+            ep.box(p, tmD, tmE, 2 * part + 1, w + EPI_BOX, alpha, abort_flag);
+            continue;
+          }
+          // one copy of the longer code by rows for both boxes (see gemm_kernel)
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            uint32_t x[EPI_BOX];
+#pragma unroll
+            for (int i = 0; i < EPI_BOX; ++i) x[i] = h ? w[EPI_BOX + i] : w[i];
+            const int c = c_off + h * EPI_BOX;
+            store_box_epi(p, ep.boxes, ep.row0, tn * C::BN + half * HALF + c, x, alpha, ep.bias + c, ep.mag_rows);
           }
         }
         continue;
