@@ -317,9 +317,10 @@ NVFP4_API nvfp4_status nvfp4_gemm_requant(const void* a_codes, const void* a_sf_
  *   amax_dev : out, max |y| over the stored y, may be null (zeroed by the call
  *           first): the amax that nvfp4_quantize takes with amax_given = 1, so
  *           a bf16 y is quantized in one pass.  Non-finite y propagate to it.
- * rows >= 0 (0: only *amax_dev is written), k >= 1, eps >= 0 and finite.
- * Pointers and pitches need only element alignment (16-byte aligned rows of
- * x, y, gamma and beta are the fast case).  y must not overlap x.
+ * rows >= 0 (0: only *amax_dev is written), 1 <= k <= 2^28, eps >= 0 and finite.
+ * Pointers and pitches need only element alignment (k a multiple of 8 and
+ * 16-byte aligned rows of x, y, gamma and beta are the fast case).  y must not
+ * overlap x.
  */
 NVFP4_API nvfp4_status nvfp4_layernorm(const void* x, nvfp4_dtype x_dtype, int64_t rows, int64_t k, int64_t ldx,
                              const void* gamma, const void* beta, nvfp4_dtype param_dtype, float eps, void* y,
@@ -342,8 +343,8 @@ NVFP4_API nvfp4_status nvfp4_layernorm(const void* x, nvfp4_dtype x_dtype, int64
  *           bytes, 16-byte aligned; may be null if dgamma and dbeta are.  It
  *           needs no clearing; calls sharing one must not overlap.
  * The column sums are taken in a fixed order: equal inputs give equal bits.
- * rows >= 0 (0: dgamma, dbeta and *amax_dx are 0), k >= 1; alignment as in
- * nvfp4_layernorm.
+ * rows >= 0 (0: dgamma, dbeta and *amax_dx are 0), 1 <= k <= 2^28; alignment
+ * as in nvfp4_layernorm.
  */
 NVFP4_API nvfp4_status nvfp4_layernorm_backward(const void* dy, nvfp4_dtype dy_dtype, int64_t lddy, const void* x,
                                       nvfp4_dtype x_dtype, int64_t ldx, const float* mean, const float* rstd,
@@ -387,7 +388,8 @@ NVFP4_API nvfp4_status nvfp4_gemm_epilogue(const void* a_codes, const void* a_sf
  *           bytes, 16-byte aligned; may be null if dbias is.  It needs no
  *           clearing; calls sharing one must not overlap.
  * dbias is summed in a fixed order: equal inputs give equal bits.  M >= 0 (0:
- * dbias and *amax_dpre are 0), N >= 1; element alignment.  Relu's slope at 0 is 0.
+ * dbias and *amax_dpre are 0), 1 <= N <= 2^28; element alignment (16-byte aligned
+ * rows of a multiple of 8 columns are the fast case).  Relu's slope at 0 is 0.
  */
 NVFP4_API nvfp4_status nvfp4_epilogue_backward(const void* dd, int64_t ldd, const void* pre, int64_t ldp,
                                      nvfp4_dtype dtype, nvfp4_act act, int64_t M, int64_t N, void* dpre,

@@ -115,6 +115,10 @@ nvfp4_status check_bf16_input(const void* x, int64_t rows, int64_t k, int64_t ld
   return NVFP4_OK;
 }
 
+// Longest row of the layer norm and the epilogue's gradient: their kernels count
+// columns, twice a row's and a grid's rounding, in 32 bits.
+constexpr int64_t kMaxColumns = int64_t{1} << 28;
+
 // Scalar tail of the quantize-and-multiply workspace: g_a, the amax and one
 // 32-bit counter per 256-row block of A from byte 64.
 // g_a at 0, amax_a at 16, the unit ticket at 64, the (row block, K chunk)
@@ -347,7 +351,7 @@ nvfp4_status nvfp4_gemm_requant(const void* a_codes, const void* a_sf_tc, const 
 
 size_t nvfp4_workspace_bytes(nvfp4_op op, int64_t M, int64_t N, int64_t K) {
   if (op == NVFP4_OP_LAYERNORM_BACKWARD || op == NVFP4_OP_EPILOGUE_BACKWARD) {
-    if (M < 0 || N < 1 || M > 0x7FFFFFFF || N > 0x7FFFFFFF) return 0;
+    if (M < 0 || N < 1 || M > 0x7FFFFFFF || N > kMaxColumns) return 0;
     return op == NVFP4_OP_LAYERNORM_BACKWARD ? layernorm_backward_workspace_bytes(M, N)
                                              : epilogue_backward_workspace_bytes(M, N);
   }
@@ -506,7 +510,7 @@ nvfp4_status nvfp4_layernorm(const void* x, nvfp4_dtype x_dtype, int64_t rows, i
   if (rows < 0 || k < 1 || bad_dtype(x_dtype) || bad_dtype(y_dtype) || bad_dtype(param_dtype)) return NVFP4_ERR_INVALID_ARG;
   if (!(eps >= 0.0f) || eps > 3.402823466e38f) return NVFP4_ERR_INVALID_ARG;
   if (rows > 0 && (!x || !y)) return NVFP4_ERR_INVALID_ARG;
-  if (rows > 0x7FFFFFFF || k > 0x7FFFFFFF) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (rows > 0x7FFFFFFF || k > kMaxColumns) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   nvfp4_status st;
   if ((st = check_rows(x, x_dtype, k, ldx)) != NVFP4_OK || (st = check_rows(y, y_dtype, k, ldy)) != NVFP4_OK ||
       (st = check_rows(gamma, param_dtype, 0, 0)) != NVFP4_OK || (st = check_rows(beta, param_dtype, 0, 0)) != NVFP4_OK)
@@ -526,7 +530,7 @@ nvfp4_status nvfp4_layernorm_backward(const void* dy, nvfp4_dtype dy_dtype, int6
   if (rows < 0 || k < 1 || bad_dtype(x_dtype) || bad_dtype(dy_dtype) || bad_dtype(param_dtype)) return NVFP4_ERR_INVALID_ARG;
   if (rows > 0 && (!dy || !x || !mean || !rstd || !dx)) return NVFP4_ERR_INVALID_ARG;
   if (dx && dx == d_residual && lddx != ldr) return NVFP4_ERR_INVALID_ARG;
-  if (rows > 0x7FFFFFFF || k > 0x7FFFFFFF) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (rows > 0x7FFFFFFF || k > kMaxColumns) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   nvfp4_status st;
   if ((st = check_rows(dy, dy_dtype, k, lddy)) != NVFP4_OK || (st = check_rows(x, x_dtype, k, ldx)) != NVFP4_OK ||
       (st = check_rows(gamma, param_dtype, 0, 0)) != NVFP4_OK || (st = check_rows(dx, x_dtype, k, lddx)) != NVFP4_OK ||
@@ -590,7 +594,7 @@ nvfp4_status nvfp4_epilogue_backward(const void* dd, int64_t ldd, const void* pr
   if (M < 0 || N < 1 || bad_dtype(dtype) || bad_act(act)) return NVFP4_ERR_INVALID_ARG;
   if (M > 0 && (!dd || (!pre && act != NVFP4_ACT_NONE))) return NVFP4_ERR_INVALID_ARG;
   if (dpre && ((dpre == dd && lddp != ldd) || dpre == pre)) return NVFP4_ERR_INVALID_ARG;
-  if (M > 0x7FFFFFFF || N > 0x7FFFFFFF) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (M > 0x7FFFFFFF || N > kMaxColumns) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   nvfp4_status st;
   if ((st = check_rows(dd, dtype, N, ldd)) != NVFP4_OK || (pre && (st = check_rows(pre, dtype, N, ldp)) != NVFP4_OK) ||
       (dpre && (st = check_rows(dpre, dtype, N, lddp)) != NVFP4_OK))

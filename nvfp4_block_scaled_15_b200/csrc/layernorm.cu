@@ -571,6 +571,81 @@ __global__ void __launch_bounds__(THREADS, lf_blocks<TX, NV>(THREADS)) ln_forwar
   publish_amax(p, mag.bits(), mags);
 }
 
+// Forward of short rows (k <= 32 E) of any alignment: a warp takes RP rows at a
+// time, lane l their elements l, l + 32, ..., straight from and to memory, with
+// gamma and beta in registers.  The rows' sums are formed two at the price of
+// one, and RP rows hide each other's latency.
+constexpr int LS_MAX_K = 256;
+template <typename TX, typename TY, int E>
+__global__ void __launch_bounds__(256) ln_forward_short_kernel(const LnParams p, int) {
+  constexpr int RP = E <= 2 ? 8 : 4;
+  __shared__ uint32_t mags[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float inv_k = 1.0f / static_cast<float>(p.k);
+  float gm[E], bt[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int c = lane + 32 * e;
+    gm[e] = p.gamma && c < p.k ? load_param(p.gamma, p.param_f32, c) : 1.0f;
+    bt[e] = p.beta && c < p.k ? load_param(p.beta, p.param_f32, c) : 0.0f;
+  }
+  if (p.joined) cluster_sync_all();                       // every block has started, before its memory is written to
+  uint32_t mag = 0;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 8 * RP;
+  for (int64_t r = (static_cast<int64_t>(blockIdx.x) * 8 + warp) * RP; r < p.rows; r += step) {
+    float x[RP][E];
+    float s[RP], mean[RP], rstd[RP];
+#pragma unroll
+    for (int q = 0; q < RP; ++q) {
+      const TX* row = static_cast<const TX*>(p.x) + (r + q) * p.ldx;
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[q][e] = r + q < p.rows && lane + 32 * e < p.k ? to_f32(row[lane + 32 * e]) : 0.0f;
+    }
+#pragma unroll
+    for (int q = 0; q < RP; ++q) {
+      s[q] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) s[q] += x[q][e];
+    }
+#pragma unroll
+    for (int q = 0; q < RP; q += 2) {
+      const float2 t = warp_sum2(s[q], s[q + 1]);
+      mean[q] = t.x * inv_k, mean[q + 1] = t.y * inv_k;
+    }
+#pragma unroll
+    for (int q = 0; q < RP; ++q) {
+      s[q] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float d = lane + 32 * e < p.k ? x[q][e] - mean[q] : 0.0f;
+        s[q] = fmaf(d, d, s[q]);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < RP; q += 2) {
+      const float2 t = warp_sum2(s[q], s[q + 1]);
+      rstd[q] = __frsqrt_rn(fmaf(t.x, inv_k, p.eps)), rstd[q + 1] = __frsqrt_rn(fmaf(t.y, inv_k, p.eps));
+    }
+#pragma unroll
+    for (int q = 0; q < RP; ++q) {
+      if (r + q >= p.rows) break;
+      TY* row = static_cast<TY*>(p.y) + (r + q) * p.ldy;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        if (lane + 32 * e >= p.k) continue;
+        const TY o = from_f32<TY>(fmaf((x[q][e] - mean[q]) * rstd[q], gm[e], bt[e]));
+        row[lane + 32 * e] = o;
+        mag = max(mag, mag_bits(o));
+      }
+      if (lane == 0) {
+        if (p.mean) p.mean[r + q] = mean[q];
+        if (p.rstd) p.rstd[r + q] = rstd[q];
+      }
+    }
+  }
+  publish_amax(p, mag, mags);
+}
+
 // Forward of rows that start anywhere, of up to LF_MAX_K elements: the chunks
 // of the kernel above out of the row's image in shared memory, where gamma and
 // beta lie too.  A thread holds its chunks in registers, so the next row's image
@@ -783,15 +858,15 @@ __global__ void __launch_bounds__(LB_THREADS, 1) ln_backward_rows_kernel(const L
     const int c = chunk_col(t, nt, j);
 #pragma unroll
     for (int i = 0; i < 4; ++i) dg[j].v[i] = db[j].v[i] = both(0.0f);
-    if constexpr (!kOdd) {
+    if constexpr (kOdd) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const auto one = [&](int e) { return p.gamma && c + e < k ? load_param(p.gamma, p.param_f32, c0 + c + e) : 1.0f; };
+        gam[j].v[i] = make_float2(one(2 * i), one(2 * i + 1));
+      }
+    } else {
       const int in = c0 + min(c, k - 8);
       gam[j] = p.param_f32 ? load_param_chunk<float>(p.gamma, in, 1.0f) : load_param_chunk<__nv_bfloat16>(p.gamma, in, 1.0f);
-      continue;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      gam[j].v[i].x = p.gamma && c + 2 * i < k ? load_param(p.gamma, p.param_f32, c0 + c + 2 * i) : 1.0f;
-      gam[j].v[i].y = p.gamma && c + 2 * i + 1 < k ? load_param(p.gamma, p.param_f32, c0 + c + 2 * i + 1) : 1.0f;
     }
   }
   Mag<TX> mag;
@@ -918,6 +993,91 @@ __global__ void __launch_bounds__(LB_THREADS, 1) ln_backward_rows_kernel(const L
   if constexpr (kCluster) cluster_sync_all();             // no block leaves while a peer may still write to it
 }
 
+// Backward of short rows of any alignment, as the forward kernel above: a warp
+// takes RP rows at a time and keeps its columns' sums in registers.  (For rows of
+// up to 256 it measured three times as slow as the kernel for whole chunks.)
+constexpr int LB_SHORT_K = 64;
+constexpr int LB_SHORT_RP = 4;
+constexpr int LB_SHORT_ROWS = LB_THREADS / 32 * LB_SHORT_RP;           // of a block at a time
+template <typename TX, typename TDY>
+__global__ void __launch_bounds__(LB_THREADS) ln_backward_short_kernel(const LnBwdParams p, uint32_t* mag_out) {
+  constexpr int E = LB_SHORT_K / 32, RP = LB_SHORT_RP;
+  constexpr int WARPS = LB_THREADS / 32;
+  __shared__ float acc[WARPS][2][32 * E];
+  __shared__ uint32_t mags[WARPS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float inv_k = 1.0f / static_cast<float>(p.k);
+  float gm[E], dg[E], db[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    gm[e] = p.gamma && lane + 32 * e < p.k ? load_param(p.gamma, p.param_f32, lane + 32 * e) : 1.0f;
+    dg[e] = db[e] = 0.0f;
+  }
+  uint32_t mag = 0;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * WARPS * RP;
+  for (int64_t r = (static_cast<int64_t>(blockIdx.x) * WARPS + warp) * RP; r < p.rows; r += step) {
+    float dy[RP][E], xh[RP][E], res[RP][E], mean[RP], rstd[RP];
+    float2 sum[RP];
+#pragma unroll
+    for (int q = 0; q < RP; ++q) {
+      const bool on = r + q < p.rows;
+      const TDY* d = static_cast<const TDY*>(p.dy) + (r + q) * p.lddy;
+      const TX* x = static_cast<const TX*>(p.x) + (r + q) * p.ldx;
+      const TX* z = static_cast<const TX*>(p.res) + (r + q) * p.ldr;
+      mean[q] = on ? p.mean[r + q] : 0.0f, rstd[q] = on ? p.rstd[r + q] : 0.0f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int c = lane + 32 * e;
+        const bool in = on && c < p.k;
+        dy[q][e] = in ? to_f32(d[c]) : 0.0f;
+        xh[q][e] = in ? to_f32(x[c]) : mean[q];
+        res[q][e] = p.res && in ? to_f32(z[c]) : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < RP; ++q) {
+      float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        if (lane + 32 * e >= p.k) continue;
+        xh[q][e] = (xh[q][e] - mean[q]) * rstd[q];
+        const float a = dy[q][e] * gm[e];
+        s1 += a;
+        s2 = fmaf(a, xh[q][e], s2);
+        dg[e] = fmaf(dy[q][e], xh[q][e], dg[e]);
+        db[e] += dy[q][e];
+      }
+      sum[q] = warp_sum2(s1, s2);
+    }
+#pragma unroll
+    for (int q = 0; q < RP; ++q) {
+      if (r + q >= p.rows) break;
+      const float c1 = -rstd[q] * (sum[q].x * inv_k), c2 = -rstd[q] * (sum[q].y * inv_k);
+      TX* out = static_cast<TX*>(p.dx) + (r + q) * p.lddx;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        if (lane + 32 * e >= p.k) continue;
+        const TX o = from_f32<TX>(fmaf(dy[q][e] * gm[e], rstd[q], fmaf(xh[q][e], c2, c1)) + res[q][e]);
+        out[lane + 32 * e] = o;
+        mag = max(mag, mag_bits(o));
+      }
+    }
+  }
+  const uint32_t m = block_max(mag, mags);
+  if (p.partial) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[warp][0][lane + 32 * e] = dg[e], acc[warp][1][lane + 32 * e] = db[e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * p.k; i += LB_THREADS) {
+      const int which = i >= p.k, c = which ? i - p.k : i;
+      float s = 0.0f;
+      for (int w = 0; w < WARPS; ++w) s += acc[w][which][c];
+      p.partial[static_cast<int64_t>(blockIdx.x) * 2 * p.k + i] = s;
+    }
+  }
+  publish_block(p, m, mag_out);
+}
+
 // First n0 columns of the blocks' partials [blocks][stride] to out0, the next
 // n1 to out1 (either may be null), and the largest of their magnitudes to
 // amax.  A block of 8 warps takes 32 columns; warp w sums the partials w, w +
@@ -1027,8 +1187,19 @@ bool try_forward_odd(const LnParams& p, cudaStream_t s, cudaError_t* e) {
   return true;
 }
 
+template <typename TX, typename TY>
+cudaError_t run_forward_short(const LnParams& p, cudaStream_t s) {
+  const int rp = p.k <= 64 ? 8 : 4;
+  const int64_t need = (p.rows + 8 * rp - 1) / (8 * rp), most = static_cast<int64_t>(device_sm_count()) * 4;
+  return p.k <= 64 ? launch_forward(ln_forward_short_kernel<TX, TY, 2>, p, need, most, 256, 0, 32, s)
+                   : launch_forward(ln_forward_short_kernel<TX, TY, 8>, p, need, most, 256, 0, 32, s);
+}
+
 template <typename TX>
 cudaError_t dispatch_forward(const LnParams& p, bool vec, cudaStream_t s) {
+  // 32768 rows of 64: 14 us against 18 of the kernel for whole chunks, of 99: 23 against 28 of the one for odd rows;
+  // of 200 in whole chunks: 33 against 19
+  if (p.k <= 64 || (!vec && p.k <= LS_MAX_K)) return p.y_f32 ? run_forward_short<TX, float>(p, s) : run_forward_short<TX, __nv_bfloat16>(p, s);
   if (vec && p.k <= LF_THREADS * 32) return run_forward<TX, 4, LF_THREADS>(p, s);
   if (vec && p.k <= lf_max_k<4>()) return run_forward<TX, 4, 512>(p, s);
   if (vec && p.k <= LF_MAX_K) return run_forward<TX, 8, 512>(p, s);
@@ -1136,7 +1307,22 @@ bool try_backward_rows(const LnBwdParams& p, float* dgamma, float* dbeta, uint32
 }
 
 template <typename TX, typename TDY>
+cudaError_t run_backward_short(const LnBwdParams& p, float* dgamma, float* dbeta, uint32_t* mags, cudaStream_t s) {
+  const int64_t need = (p.rows + LB_SHORT_ROWS - 1) / LB_SHORT_ROWS;
+  const int64_t most = device_sm_count() < LB_MAX_BLOCKS ? device_sm_count() : LB_MAX_BLOCKS;
+  const int blocks = static_cast<int>(need < most ? need : most);
+  cudaError_t e = cudaSuccess;
+  if (p.amax && !p.partial) e = cudaMemsetAsync(p.amax, 0, sizeof(float), s);
+  if (e != cudaSuccess) return e;
+  ln_backward_short_kernel<TX, TDY><<<blocks, LB_THREADS, 0, s>>>(p, mags);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !p.partial) return e;
+  return launch_sum_partials(p.partial, blocks, 2 * static_cast<int64_t>(p.k), p.k, p.k, dgamma, dbeta, mags, blocks, p.amax, s);
+}
+
+template <typename TX, typename TDY>
 cudaError_t dispatch_backward(const LnBwdParams& p, bool vec, float* dgamma, float* dbeta, uint32_t* mags, cudaStream_t s) {
+  if (p.k <= LB_SHORT_K) return run_backward_short<TX, TDY>(p, dgamma, dbeta, mags, s);
   cudaError_t e = cudaSuccess;
   if (vec ? try_backward_rows<TX, TDY, false>(p, dgamma, dbeta, mags, s, &e)
           : try_backward_rows<TX, TDY, true>(p, dgamma, dbeta, mags, s, &e))

@@ -64,7 +64,7 @@ def check_forward(lib, x, g, b, y, stats, eps=EPS):
 # (rows, k): one element, one warp's and one block's limits on both sides, a whole vector less or more, lengths past
 # what registers hold, more rows than a grid
 SHAPES = [(1, 1), (1, 8192), (8, 8192), (3, 7), (5, 33), (130, 1000), (64, 1155), (33, 1024), (33, 1032), (9, 2048),
-          (300, 2056), (5, 4096), (3, 8200), (2, 16384), (3, 28672), (2, 32768), (2, 32776), (2, 40001), (2, 70001), (2500, 64), (400, 8191), (170, 20001)]
+          (300, 2056), (5, 4096), (3, 8200), (2, 16384), (3, 28672), (2, 32768), (2, 32776), (2, 40001), (2, 70001), (2500, 64), (400, 8191), (170, 20001), (700, 63), (90, 65), (1300, 256), (50, 257)]
 
 
 @pytest.mark.parametrize("rows,k", SHAPES, ids=str)

@@ -43,6 +43,7 @@ EB = dict(dd=FAKE, ldd=10, pre=FAKE, ldp=10, dtype=0, act=2, m=8, n=10, dpre=FAK
     (dict(x_dtype=2), "INVALID_ARG"), (dict(y_dtype=-1), "INVALID_ARG"), (dict(p_dtype=7), "INVALID_ARG"),
     (dict(eps=-1e-5), "INVALID_ARG"), (dict(eps=float("nan")), "INVALID_ARG"), (dict(eps=float("inf")), "INVALID_ARG"),
     (dict(rows=1 << 31), "UNSUPPORTED_SHAPE"), (dict(k=1 << 31, ldx=1 << 31, ldy=1 << 31), "UNSUPPORTED_SHAPE"),
+    (dict(k=(1 << 28) + 1, ldx=1 << 30, ldy=1 << 30), "UNSUPPORTED_SHAPE"),
     (dict(x=FAKE + 1), "MISALIGNED"), (dict(x=FAKE + 2, x_dtype=1), "MISALIGNED"), (dict(y=FAKE + 1), "MISALIGNED"),
     (dict(gamma=FAKE + 2), "MISALIGNED"), (dict(beta=FAKE + 1, p_dtype=0), "MISALIGNED"), (dict(mean=FAKE + 2), "MISALIGNED"),
     (dict(amax=FAKE + 1), "MISALIGNED")], ids=str)
@@ -56,7 +57,8 @@ def test_layernorm_refuses(nv, change, status):
     (dict(lddy=32), "INVALID_ARG"), (dict(lddx=32), "INVALID_ARG"), (dict(res=FAKE + 64, ldr=32), "INVALID_ARG"),
     (dict(res=FAKE, ldr=40), "INVALID_ARG"), (dict(dy_dtype=3), "INVALID_ARG"), (dict(ws=None), "INVALID_ARG"),
     (dict(ws_bytes=64), "WORKSPACE"), (dict(ws=FAKE + 8), "MISALIGNED"), (dict(dgamma=FAKE + 2), "MISALIGNED"),
-    (dict(res=FAKE + 1, ldr=33), "MISALIGNED"), (dict(rows=1 << 31), "UNSUPPORTED_SHAPE")], ids=str)
+    (dict(res=FAKE + 1, ldr=33), "MISALIGNED"), (dict(rows=1 << 31), "UNSUPPORTED_SHAPE"),
+    (dict(k=(1 << 28) + 1, ldx=1 << 30, lddy=1 << 30, lddx=1 << 30), "UNSUPPORTED_SHAPE")], ids=str)
 def test_layernorm_backward_refuses(nv, change, status):
     assert call(nv, "nvfp4_layernorm_backward", LNB, **change) == getattr(nv, "ERR_" + status)
 
@@ -87,7 +89,8 @@ def test_gemv_epilogue_refuses(nv, change, status):
     (dict(act=6), "INVALID_ARG"), (dict(dtype=2), "INVALID_ARG"), (dict(ldd=9), "INVALID_ARG"), (dict(lddp=9), "INVALID_ARG"),
     (dict(dpre=FAKE, lddp=12), "INVALID_ARG"), (dict(pre=FAKE + (1 << 16)), "INVALID_ARG"), (dict(ws=None), "INVALID_ARG"),
     (dict(ws_bytes=16), "WORKSPACE"), (dict(ws=FAKE + 4), "MISALIGNED"), (dict(dd=FAKE + 1), "MISALIGNED"),
-    (dict(dbias=FAKE + 1), "MISALIGNED")], ids=str)
+    (dict(dbias=FAKE + 1), "MISALIGNED"), (dict(m=1 << 31), "UNSUPPORTED_SHAPE"),
+    (dict(n=(1 << 28) + 1, ldd=1 << 30, ldp=1 << 30, lddp=1 << 30), "UNSUPPORTED_SHAPE")], ids=str)
 def test_epilogue_backward_refuses(nv, change, status):
     assert call(nv, "nvfp4_epilogue_backward", EB, **change) == getattr(nv, "ERR_" + status)
 
@@ -113,3 +116,4 @@ def test_workspace_sizes(nv):
         assert nv.nvfp4_workspace_bytes(op, -1, 33, 0) == 0
         assert nv.nvfp4_workspace_bytes(op, 4, 0, 0) == 0
         assert nv.nvfp4_workspace_bytes(op, 1 << 31, 33, 0) == 0
+        assert nv.nvfp4_workspace_bytes(op, 4, (1 << 28) + 1, 0) == 0
