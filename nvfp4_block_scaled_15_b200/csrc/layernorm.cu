@@ -577,8 +577,8 @@ __global__ void __launch_bounds__(THREADS, lf_blocks<TX, NV>(THREADS)) ln_forwar
 // one, and RP rows hide each other's latency.
 constexpr int LS_MAX_K = 256;
 template <typename TX, typename TY, int E>
-__global__ void __launch_bounds__(256) ln_forward_short_kernel(const LnParams p, int) {
-  constexpr int RP = E <= 2 ? 8 : 4;
+__global__ void __launch_bounds__(256, 4) ln_forward_short_kernel(const LnParams p, int) {
+  constexpr int RP = E <= 2 ? 4 : 2;
   __shared__ uint32_t mags[8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float inv_k = 1.0f / static_cast<float>(p.k);
@@ -1189,7 +1189,7 @@ bool try_forward_odd(const LnParams& p, cudaStream_t s, cudaError_t* e) {
 
 template <typename TX, typename TY>
 cudaError_t run_forward_short(const LnParams& p, cudaStream_t s) {
-  const int rp = p.k <= 64 ? 8 : 4;
+  const int rp = p.k <= 64 ? 4 : 2;
   const int64_t need = (p.rows + 8 * rp - 1) / (8 * rp), most = static_cast<int64_t>(device_sm_count()) * 4;
   return p.k <= 64 ? launch_forward(ln_forward_short_kernel<TX, TY, 2>, p, need, most, 256, 0, 32, s)
                    : launch_forward(ln_forward_short_kernel<TX, TY, 8>, p, need, most, 256, 0, 32, s);
@@ -1197,7 +1197,7 @@ cudaError_t run_forward_short(const LnParams& p, cudaStream_t s) {
 
 template <typename TX>
 cudaError_t dispatch_forward(const LnParams& p, bool vec, cudaStream_t s) {
-  // 32768 rows of 64: 14 us against 18 of the kernel for whole chunks, of 99: 23 against 28 of the one for odd rows;
+  // 32768 rows of 64: 12 us against 18 of the kernel for whole chunks, of 99: 19 against 28 of the one for odd rows;
   // of 200 in whole chunks: 33 against 19
   if (p.k <= 64 || (!vec && p.k <= LS_MAX_K)) return p.y_f32 ? run_forward_short<TX, float>(p, s) : run_forward_short<TX, __nv_bfloat16>(p, s);
   if (vec && p.k <= LF_THREADS * 32) return run_forward<TX, 4, LF_THREADS>(p, s);
