@@ -880,7 +880,7 @@ struct NoMaps {};
 // with the other accumulator first).  The residual's boxes are fetched before
 // the accumulator is waited for, added in place, and leave from where they
 // arrived; pre leaves from boxes of its own:
-//   no residual: D in boxes 0, 1 in turn;  residual without pre: all four
+//   no residual: D in boxes 0, 1 in turn, pre in 2, 3;  residual without pre: all four
 //   steps' boxes fetched at once;  residual and pre: boxes 0, 1, the later two
 //   steps' fetched when the store that reads the box is done.  pre: boxes 2, 3.
 struct EpiWriter {
@@ -891,6 +891,7 @@ struct EpiWriter {
   uint32_t mag_rows = 0;     // |D| of store_box_epi()
   uint32_t parity = 0;       // of bars[0..3]
   uint32_t pending = 0;      // residual boxes fetched and not waited for
+  int turn = 0;              // boxes stored: without a residual they alternate by it, also where a tile ends early
   int row0 = 0, col0 = 0, first = 0;
 
   static constexpr uint32_t BYTES = EPI_BOX * EPI_BOX * 2;
@@ -924,8 +925,24 @@ struct EpiWriter {
                                       float alpha, volatile int* abort_flag) {
     const int lane = threadIdx.x & 31;
     const int c = col(s);
-    if (row0 >= p.M || c >= p.N) return;
-    const int buf = p.res && !p.pre ? s : s & 1, pre_buf = 2 + (s & 1);
+    if (row0 >= p.M) return;
+    const int buf = !p.res ? turn & 1 : p.pre ? s & 1 : s;
+    const int pre_buf = 2 + (p.res ? s & 1 : turn & 1);
+    // a box past D's columns has nothing to store, but the box two steps on, which
+    // may lie before them, still has to be fetched
+    if (c < p.N) {
+      store(p, d, m, c, buf, pre_buf, v, alpha, abort_flag);
+      ++turn;
+    }
+    if (p.res && p.pre && s < 2) {
+      if (lane == 0) bulk_wait_group_read<0>();
+      fetch(p, m, s + 2, buf);
+    }
+  }
+
+  __device__ __forceinline__ void store(const GemmParams& p, const CUtensorMap& d, const EpiMaps& m, int c, int buf,
+                                        int pre_buf, const uint32_t* v, float alpha, volatile int* abort_flag) {
+    const int lane = threadIdx.x & 31;
     BoxRow x;
     box_values(v, alpha, p.bias ? bias + (c - col0) : nullptr, x);
     if (!p.res) {
@@ -956,10 +973,6 @@ struct EpiWriter {
       if (p.pre) tma_store_2d(&m.pre, boxes + pre_buf * BYTES, c, row0);
       tma_store_2d(&d, boxes + buf * BYTES, c, row0);
       bulk_commit_group();
-    }
-    if (p.res && p.pre && s < 2) {
-      if (lane == 0) bulk_wait_group_read<0>();
-      fetch(p, m, s + 2, buf);
     }
   }
 

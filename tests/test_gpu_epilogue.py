@@ -120,6 +120,30 @@ def test_gemm_epilogue_slower_than_the_product(lib, n, k, res, pre):
         R.check(p, *ref["pre"], "pre")
 
 
+@pytest.mark.parametrize("n", [264, 296, 328, 376, 392, 424, 456, 488, 504, 904])
+@pytest.mark.parametrize("res,pre", [(True, True), (True, False), (False, True)], ids=["res_pre", "res", "pre"])
+def test_gemm_ends_inside_a_tile(lib, n, res, pre):
+    """N ends in each of a tile's eight boxes of 32 columns (the boxes shared between the accumulators are taken first, so
+    the first ones may lie past N and the later ones before it), with enough rows for tiles in both accumulators."""
+    m, k = 18944 + 300, 64
+    _, w, x, ref = product(lib, 300, n, k)
+    bias = randn(1, n).bfloat16().cuda()
+    # the rows of one small product over and over: enough tiles that every CTA pair takes several
+    rows = torch.arange(m, device="cuda") % 300
+    big = lib.quantize(x[rows])
+    d_ref, s_ref, alpha = ref
+    r = randn(2, m, n).bfloat16().cuda() if res else None
+    p = torch.empty(m, n, dtype=BF16, device="cuda") if pre else None
+    for _ in range(2):
+        d = lib.gemm_epilogue(big, w, bias, "relu", r, pre=p if pre else False)
+    assert lib.nvfp4_check_device_status() == lib.OK
+    idx = rows.cpu().numpy()
+    ref = R.epilogue(d_ref[idx], s_ref[idx], alpha, bias, "relu", r)
+    R.check(d, *ref["d"], "d")
+    if pre:
+        R.check(p, *ref["pre"], "pre")
+
+
 def test_gemm_nonfinite_bias_and_residual(lib):
     a, w, _, _ = product(lib, 300, 520, 1088)
     bias = torch.zeros(520, device="cuda")
