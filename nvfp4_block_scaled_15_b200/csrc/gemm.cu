@@ -1259,6 +1259,7 @@ __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>:
     }
     const float gd = kQ ? *p.g_d : 0.0f;
     float amax_run = 0.0f;
+    [[maybe_unused]] int turn = 0;                     // boxes stored by this warp
     [[maybe_unused]] EpiWriter ep{epi_smem + ew * C::EPI_BOXES * C::EPI_BOX_BYTES,
                                   reinterpret_cast<float*>(res_bar + C::EPI_WARPS * C::EPI_BOXES) + ew * HALF,
                                   res_bar + ew * C::EPI_BOXES};
@@ -1341,8 +1342,8 @@ __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>:
 #pragma unroll
               for (int cc = 0; cc < 2; ++cc) {
                 if (col0 + cc * C::EPI_BOX_COLS >= p.N) break;
-                const int box_id = c_off / C::EPI_BOX_COLS + cc;     // staging buffers alternate by box
-                uint8_t* box = epi_smem + (ew * 2 + (box_id & 1)) * C::EPI_BOX_BYTES;
+                // staging buffers alternate by boxes stored, also across a tile that ends early
+                uint8_t* box = epi_smem + (ew * 2 + (turn++ & 1)) * C::EPI_BOX_BYTES;
                 if (lane == 0) bulk_wait_group_read<1>();
                 __syncwarp();
 #pragma unroll
@@ -1409,7 +1410,7 @@ __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>:
 #pragma unroll
           for (int c = 0; c < HALF / C::EPI_BOX_COLS; ++c) {
             if (col0 + c * C::EPI_BOX_COLS >= p.N) break;
-            uint8_t* box = epi_smem + (ew * 2 + (c & 1)) * C::EPI_BOX_BYTES;
+            uint8_t* box = epi_smem + (ew * 2 + (turn++ & 1)) * C::EPI_BOX_BYTES;
             if (lane == 0) bulk_wait_group_read<1>();   // the store that last read this buffer is done
             __syncwarp();
 #pragma unroll
