@@ -345,39 +345,49 @@ __device__ __forceinline__ void box_add(const uint8_t* box, int row, BoxRow& x) 
 
 // A box between shared memory and the rows row0 .. of a matrix, lane l at
 // column col + l: one coalesced access per row, any alignment.
+// (Elements on the way are held as bits in a register each.)
 template <typename T>
-__device__ __forceinline__ T* box_elem(uint8_t* box, int row, int lane) {
+using ElemBits = std::conditional_t<sizeof(T) == 2, unsigned short, uint32_t>;
+template <typename T>
+__device__ __forceinline__ ElemBits<T>* box_elem(uint8_t* box, int row, int lane) {
   constexpr int PER = 16 / sizeof(T);
-  return reinterpret_cast<T*>(box + box_chunk<T>(row, lane / PER)) + lane % PER;
+  return reinterpret_cast<ElemBits<T>*>(box + box_chunk<T>(row, lane / PER)) + lane % PER;
 }
-// (Eight rows' accesses are issued before the first is used.)
+// (Eight rows at a time: a loop over all 32 unrolled keeps 32 addresses, and
+// these kernels' shared memory leaves so little L1 that a spilled register
+// costs an L2 access.)
 template <typename T>
 __device__ __forceinline__ void box_rows_out(uint8_t* box, void* base, int64_t ld, int row0, int rows, int col, bool in) {
   const int lane = threadIdx.x & 31;
-  T* out = static_cast<T*>(base) + static_cast<int64_t>(row0) * ld + col + lane;
+  ElemBits<T>* out = static_cast<ElemBits<T>*>(base) + static_cast<int64_t>(row0) * ld + col + lane;
   if (!in) return;
-#pragma unroll
-  for (int r = 0; r < EPI_BOX; r += 8) {
-    T x[8];
+#pragma unroll 1
+  for (int r = 0; r < rows; r += 8) {
+    uint32_t x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = *box_elem<T>(box, r + i, lane);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (r + i < rows) out[(r + i) * ld] = x[i];
+    for (int i = 0; i < 8; ++i) {
+      if (r + i < rows) *out = static_cast<ElemBits<T>>(x[i]);
+      out += ld;
+    }
   }
 }
 template <typename T>
 __device__ __forceinline__ void box_rows_in(uint8_t* box, const void* base, int64_t ld, int row0, int rows, int col, bool in) {
   const int lane = threadIdx.x & 31;
-  const T* src = static_cast<const T*>(base) + static_cast<int64_t>(row0) * ld + col + lane;
+  const ElemBits<T>* src = static_cast<const ElemBits<T>*>(base) + static_cast<int64_t>(row0) * ld + col + lane;
   if (!in) return;
+#pragma unroll 1
+  for (int r = 0; r < rows; r += 16) {
+    uint32_t x[16];
 #pragma unroll
-  for (int r = 0; r < EPI_BOX; r += 16) {
-    T x[16];
+    for (int i = 0; i < 16; ++i) {
+      x[i] = r + i < rows ? *src : 0u;
+      src += ld;
+    }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = r + i < rows ? src[(r + i) * ld] : from_f32<T>(0.0f);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) *box_elem<T>(box, r + i, lane) = x[i];
+    for (int i = 0; i < 16; ++i) *box_elem<T>(box, r + i, lane) = static_cast<ElemBits<T>>(x[i]);
   }
 }
 
@@ -423,10 +433,21 @@ __device__ __forceinline__ void box_mag(const BoxRow& x, int n_valid, uint32_t& 
     if (i < n_valid) mag = max(mag, mag_bits(from_f32<T>(i & 1 ? x[i / 2].y : x[i / 2].x)));
 }
 
-// One box of any type and alignment; `box`: EPI_ROWS_BYTES of this warp.
+// Which epilogue a kernel is built with: none, the one whose boxes go by TMA
+// (CTA-pair kernel, bf16), or the one that writes rows of bf16 or fp32 at any
+// alignment.  One kernel for all spent registers and instruction fetches on
+// code that a call never reaches.
+constexpr int EPI_NONE = 0, EPI_TMA = 1, EPI_ROWS_BF16 = 2, EPI_ROWS_F32 = 3;
+
+// One box of any type and alignment, column col of a row per thread in v; `box`:
+// EPI_ROWS_BYTES of this warp; bias: its 32 values.
+template <int kE>
+using EpiRow = std::conditional_t<kE == EPI_ROWS_F32, float, __nv_bfloat16>;
+
 template <typename T>
 __device__ __forceinline__ void store_box_rows(const GemmParams& p, uint8_t* box, int row0, int col, const uint32_t* v,
                                                float alpha, const float* bias, uint32_t& mag) {
+  if (row0 >= p.M || col >= p.N) return;
   const int lane = threadIdx.x & 31;
   const int rows = min(EPI_BOX, p.M - row0);
   const bool in = col + lane < p.N;
@@ -449,17 +470,7 @@ __device__ __forceinline__ void store_box_rows(const GemmParams& p, uint8_t* box
   __syncwarp();
   box_rows_out<T>(box, p.d, p.ldd, row0, rows, col, in);
   __syncwarp();
-  if (lane < rows) box_mag<T>(x, p.N - col, mag);
-}
-
-// A box at column col (a row per thread in v) by rows; bias: its 32 values.
-__device__ __forceinline__ void store_box_epi(const GemmParams& p, uint8_t* box, int row0, int col,
-                                              const uint32_t (&v)[EPI_BOX], float alpha, const float* bias, uint32_t& mag) {
-  if (row0 >= p.M || col >= p.N) return;
-  if (p.out_f32)
-    store_box_rows<float>(p, box, row0, col, v, alpha, bias, mag);
-  else
-    store_box_rows<__nv_bfloat16>(p, box, row0, col, v, alpha, bias, mag);
+  if (p.amax_d && lane < rows) box_mag<T>(x, p.N - col, mag);
 }
 
 __device__ __forceinline__ void publish_mag(const GemmParams& p, uint32_t mag) {
@@ -468,12 +479,12 @@ __device__ __forceinline__ void publish_mag(const GemmParams& p, uint32_t mag) {
   if ((threadIdx.x & 31) == 0) atomicMax(reinterpret_cast<unsigned int*>(p.amax_d), mag);
 }
 
-// kE: the epilogue applies bias, activation and residual (store_row_epi).
-template <int BN, bool kMx, bool kE>
+// kE: the epilogue (EPI_NONE, EPI_ROWS_BF16 or EPI_ROWS_F32).
+template <int BN, bool kMx, int kE>
 __global__ void __launch_bounds__(GemmCfg<BN, kMx>::THREADS, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const GemmParams p) {
-  using C = GemmCfg<BN, kMx, kE>;
+  using C = GemmCfg<BN, kMx, kE != EPI_NONE>;
   using F = typename C::F;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
@@ -634,7 +645,7 @@ __global__ void __launch_bounds__(GemmCfg<BN, kMx>::THREADS, 1)
     const int half = ew >> 2;                  // which half of the tile's columns
     constexpr int HALF = BN / 2;
     const float alpha = kMx ? 1.0f : __fdiv_rn(1.0f, __fmul_rn(*p.g_a, *p.g_b));
-    const float gd = !kE && p.out_q ? *p.g_d : 0.0f;
+    const float gd = kE == EPI_NONE && p.out_q ? *p.g_d : 0.0f;
     float amax_run = 0.0f;
     uint32_t mag = 0;
     int acc = 0;
@@ -643,11 +654,11 @@ __global__ void __launch_bounds__(GemmCfg<BN, kMx>::THREADS, 1)
       const int tm = t % p.tiles_m;
       const int tn = t / p.tiles_m;
       [[maybe_unused]] float* bias = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE_BYTES + 8 * EPI_ROWS_BYTES) + ew * HALF;
-      if constexpr (kE) bias_in<HALF>(p, tn * BN + half * HALF, bias);
+      if constexpr (kE != EPI_NONE) bias_in<HALF>(p, tn * BN + half * HALF, bias);
       if (!mbar_wait_bounded(&acc_full[acc], acc_phase, abort_flag, p.wait_limit_ns, p.status)) break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * BN + half * HALF;
-      if constexpr (kE) {
+      if constexpr (kE != EPI_NONE) {
         // box by box in a loop: the epilogue's code is long, and straight-line
         // copies of it per box spent more on fetching instructions than on them
 #pragma unroll 1
@@ -658,8 +669,8 @@ __global__ void __launch_bounds__(GemmCfg<BN, kMx>::THREADS, 1)
           tc_fence_before();
           __syncwarp();
           if (c + EPI_BOX == HALF && lane == 0) mbar_arrive(&acc_empty[acc]);
-          store_box_epi(p, smem + C::STAGES * C::STAGE_BYTES + ew * EPI_ROWS_BYTES, tm * BM + quad * 32,
-                        tn * BN + half * HALF + c, w, alpha, bias + c, mag);
+          store_box_rows<EpiRow<kE>>(p, smem + C::STAGES * C::STAGE_BYTES + ew * EPI_ROWS_BYTES, tm * BM + quad * 32,
+                                     tn * BN + half * HALF + c, w, alpha, bias + c, mag);
         }
         if (++acc == C::ACC_BUFS) {
           acc = 0;
@@ -687,7 +698,7 @@ __global__ void __launch_bounds__(GemmCfg<BN, kMx>::THREADS, 1)
           store_row<HALF>(p, row, col0, v, alpha);
       }
     }
-    if constexpr (kE)
+    if constexpr (kE != EPI_NONE)
       publish_mag(p, mag);
     else
       publish_amax(p, amax_run);
@@ -887,8 +898,7 @@ struct EpiWriter {
   uint8_t* boxes;
   float* bias;               // of the warp's 128 columns
   uint64_t* bars;            // arrivals of residual boxes
-  Mag<__nv_bfloat16> mag;    // |D| of box()
-  uint32_t mag_rows = 0;     // |D| of store_box_epi()
+  Mag<__nv_bfloat16> mag;    // |D|
   uint32_t parity = 0;       // of bars[0..3]
   uint32_t pending = 0;      // residual boxes fetched and not waited for
   int turn = 0;              // boxes stored: without a residual they alternate by it, also where a tile ends early
@@ -910,7 +920,7 @@ struct EpiWriter {
   __device__ __forceinline__ void start(const GemmParams& p, const EpiMaps& m, int row, int column, int shared_first) {
     row0 = row, col0 = column, first = shared_first;
     bias_in<4 * EPI_BOX>(p, col0, bias);
-    if (p.tma_store && p.res && row0 < p.M) {
+    if (p.res && row0 < p.M) {
       if ((threadIdx.x & 31) == 0) bulk_wait_group_read<0>();     // the last tile's boxes have left
       fetch(p, m, 0, 0);
       fetch(p, m, 1, 1);
@@ -983,7 +993,7 @@ struct EpiWriter {
         volatile int no_abort = 0;
         (void)mbar_wait_bounded(&bars[b], (parity >> b) & 1u, &no_abort, p.wait_limit_ns, p.status);
       }
-    if (p.tma_store && (threadIdx.x & 31) == 0) bulk_wait_group<0>();
+    if ((threadIdx.x & 31) == 0) bulk_wait_group<0>();
   }
 };
 
@@ -992,14 +1002,14 @@ struct EpiWriter {
 // path's registers out of it.
 // kQA: the quantize-and-GEMM kernel (bf16 A quantized by extra warps, tiles
 // taken in row-major order so the first tiles need only the first rows).
-// kE: the epilogue applies bias, activation and residual (store_row_epi).
-template <bool kMx, bool kQ, bool kQA = false, bool kE = false>
+// kE: the epilogue (EPI_TMA, EPI_ROWS_BF16 or EPI_ROWS_F32) in place of the plain output.
+template <bool kMx, bool kQ, bool kQA = false, int kE = EPI_NONE>
 __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>::THREADS, 1)
     gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmSFA, const __grid_constant__ CUtensorMap tmSFB,
                      const __grid_constant__ CUtensorMap tmD,
-                     const __grid_constant__ std::conditional_t<kE, EpiMaps, NoMaps> tmE, const GemmParams p) {
-  using C = PairCfg<kMx, kE>;
+                     const __grid_constant__ std::conditional_t<kE == EPI_TMA, EpiMaps, NoMaps> tmE, const GemmParams p) {
+  using C = PairCfg<kMx, kE != EPI_NONE>;
   using F = typename C::F;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
@@ -1039,7 +1049,7 @@ __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>:
     mbar_init(&acc_empty[1], 2 * C::EPI_WARPS);
     mbar_init(ovl_free, 2 * 4);                // the 4 warps per CTA that hold the shared columns
     mbar_init(mma_done, 1);
-    if constexpr (kE)
+    if constexpr (kE == EPI_TMA)
       for (int b = 0; b < C::EPI_WARPS * C::EPI_BOXES; ++b) mbar_init(&res_bar[b], 1);
     *abort_flag = 0;
     // One ticket batch for the CTA's first units (one per quantizer and
@@ -1260,6 +1270,7 @@ __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>:
     const float gd = kQ ? *p.g_d : 0.0f;
     float amax_run = 0.0f;
     [[maybe_unused]] int turn = 0;                     // boxes stored by this warp
+    [[maybe_unused]] uint32_t mag = 0;
     [[maybe_unused]] EpiWriter ep{epi_smem + ew * C::EPI_BOXES * C::EPI_BOX_BYTES,
                                   reinterpret_cast<float*>(res_bar + C::EPI_WARPS * C::EPI_BOXES) + ew * HALF,
                                   res_bar + ew * C::EPI_BOXES};
@@ -1275,14 +1286,40 @@ __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>:
         tm = t % tiles_m;
         tn = t / tiles_m;
       }
-      if constexpr (kE) ep.start(p, tmE, tm * 256 + static_cast<int>(rank) * 128 + quad * 32, tn * C::BN + half * HALF,
-                                 b == 0 && half == 1 ? 64 : 0);
+      if constexpr (kE == EPI_TMA)
+        ep.start(p, tmE, tm * 256 + static_cast<int>(rank) * 128 + quad * 32, tn * C::BN + half * HALF,
+                 b == 0 && half == 1 ? 64 : 0);
+      [[maybe_unused]] const int shared_first = b == 0 && half == 1 ? 64 : 0;
+      [[maybe_unused]] const int epi_row = tm * 256 + static_cast<int>(rank) * 128 + quad * 32;
+      if constexpr (kE == EPI_ROWS_BF16 || kE == EPI_ROWS_F32) bias_in<HALF>(p, tn * C::BN + half * HALF, ep.bias);
       if (!mbar_wait_bounded(&acc_full[b], static_cast<uint32_t>(j >> 1) & 1u, abort_flag, p.wait_limit_ns, p.status)) break;
       tc_fence_after();
       uint32_t v[HALF];
       const uint32_t taddr =
           tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + (b ? C::ACC1_COL : 0) + half * HALF;
-      if constexpr (kE) {
+      if constexpr (kE == EPI_ROWS_BF16 || kE == EPI_ROWS_F32) {
+        // one copy of the longer code by rows for a tile's four boxes (see
+        // gemm_kernel), the columns shared with the other accumulator first
+        const bool shared_cols = (b == 0 && half == 1) || (b == 1 && half == 0);
+        const auto col_of = [&](int i) { return (i < 2 ? shared_first : 64 - shared_first) + (i & 1) * EPI_BOX; };
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w[EPI_BOX];
+          tmem_ld_32x32b_x32(taddr + col_of(i), w);
+          tmem_ld_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (i == 1 && shared_cols) mbar_arrive_cluster_relaxed(ovl_free_leader);
+            if (i == 3) mbar_arrive_cluster_relaxed(acc_empty_leader + 8u * b);
+          }
+          const int col0 = tn * C::BN + half * HALF;
+          store_box_rows<EpiRow<kE>>(p, ep.boxes, epi_row, col0 + col_of(i), w, alpha, ep.bias + col_of(i),
+                                     mag);
+        }
+        continue;
+      }
+      if constexpr (kE == EPI_TMA) {
         // 64 columns at a time, the columns shared with the other accumulator first
         const bool shared_cols = (b == 0 && half == 1) || (b == 1 && half == 0);
         const int first = (b == 0 && half == 1) ? 64 : 0;
@@ -1299,20 +1336,8 @@ __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>:
             if (part == 0 && shared_cols) mbar_arrive_cluster_relaxed(ovl_free_leader);
             if (part == 1) mbar_arrive_cluster_relaxed(acc_empty_leader + 8u * b);
           }
-          if (p.tma_store) {
-            ep.box(p, tmD, tmE, 2 * part, w, alpha, abort_flag);
-            ep.box(p, tmD, tmE, 2 * part + 1, w + EPI_BOX, alpha, abort_flag);
-            continue;
-          }
-          // one copy of the longer code by rows for both boxes (see gemm_kernel)
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            uint32_t x[EPI_BOX];
-#pragma unroll
-            for (int i = 0; i < EPI_BOX; ++i) x[i] = h ? w[EPI_BOX + i] : w[i];
-            const int c = c_off + h * EPI_BOX;
-            store_box_epi(p, ep.boxes, ep.row0, tn * C::BN + half * HALF + c, x, alpha, ep.bias + c, ep.mag_rows);
-          }
+          ep.box(p, tmD, tmE, 2 * part, w, alpha, abort_flag);
+          ep.box(p, tmD, tmE, 2 * part + 1, w + EPI_BOX, alpha, abort_flag);
         }
         continue;
       }
@@ -1436,12 +1461,13 @@ __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>:
         store_row<HALF>(p, row0 + lane, col0, v, alpha);
       }
     }
-    if (!kQ && !kE && p.tma_store && lane == 0) bulk_wait_group<0>();
+    if (!kQ && kE == EPI_NONE && p.tma_store && lane == 0) bulk_wait_group<0>();
     if constexpr (kQ) publish_amax(p, amax_run);
-    if constexpr (kE) {
+    if constexpr (kE == EPI_TMA) {
       ep.finish(p);
-      publish_mag(p, max(ep.mag_rows, ep.mag.bits()));
+      mag = ep.mag.bits();
     }
+    if constexpr (kE != EPI_NONE) publish_mag(p, mag);
   } else if constexpr (kQA) {
     // ------------------- A quantizers (quantize-and-GEMM) -------------------
     // Units taken in ticket order (qa_unit maps a ticket to a row and a K
@@ -1655,8 +1681,13 @@ nvfp4_status run_gemm_pair(const void* a_codes, const void* a_sf, const float* g
       p.qa_group = qa->group;
     }
   }
-  auto kern_epi = gemm_pair_kernel<false, false, false, true>;
-  const void* func = epi ? reinterpret_cast<const void*>(kern_epi) : reinterpret_cast<const void*>(kern);
+  auto kern_epi = gemm_pair_kernel<false, false, false, EPI_TMA>;
+  const bool epi_tma = epi && tma_store;
+  if constexpr (!kMx) {
+    if (epi && !tma_store)
+      kern = p.out_f32 ? gemm_pair_kernel<false, false, false, EPI_ROWS_F32> : gemm_pair_kernel<false, false, false, EPI_ROWS_BF16>;
+  }
+  const void* func = epi_tma ? reinterpret_cast<const void*>(kern_epi) : reinterpret_cast<const void*>(kern);
   cudaError_t e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return launch_status(e);
   cudaLaunchConfig_t cfg = {};
@@ -1674,7 +1705,7 @@ nvfp4_status run_gemm_pair(const void* a_codes, const void* a_sf, const float* g
   cfg.attrs = attr;
   cfg.numAttrs = qa ? 2 : 1;
   // as many resident pairs as the device holds at once, never more than tiles
-  static int max_pairs[3][64] = {{0}};
+  static int max_pairs[3][64] = {{0}};         // the epilogue kernels all have the same threads and memory
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return launch_status(cudaGetLastError());
   int* mp = &max_pairs[epi ? 2 : qa ? 1 : 0][dev < 64 ? dev : 0];
@@ -1688,7 +1719,7 @@ nvfp4_status run_gemm_pair(const void* a_codes, const void* a_sf, const float* g
   const int tiles = p.tiles_m * p.tiles_n;
   const int pairs = tiles < *mp ? tiles : *mp;
   cfg.gridDim = dim3(2 * pairs);
-  e = epi ? cudaLaunchKernelEx(&cfg, kern_epi, tmA, tmB, tmSFA, tmSFB, tmD, tmE, p)
+  e = epi_tma ? cudaLaunchKernelEx(&cfg, kern_epi, tmA, tmB, tmSFA, tmSFB, tmD, tmE, p)
           : cudaLaunchKernelEx(&cfg, kern, tmA, tmB, tmSFA, tmSFB, tmD, NoMaps{}, p);
   return launch_status(e);
 }
@@ -1720,11 +1751,11 @@ nvfp4_status run_gemm(const void* a_codes, const void* a_sf, const float* g_a, c
   p.wait_limit_ns = wait_limit_ns();
   p.status = device_status_ptr();
   if (!p.status) return NVFP4_ERR_CUDA;
-  auto kern = gemm_kernel<BN, kMx, false>;
+  auto kern = gemm_kernel<BN, kMx, EPI_NONE>;
   int smem = GemmCfg<BN, kMx>::SMEM_BYTES;
   if constexpr (!kMx) {
     if (epi) {
-      kern = gemm_kernel<BN, false, true>;
+      kern = p.out_f32 ? gemm_kernel<BN, false, EPI_ROWS_F32> : gemm_kernel<BN, false, EPI_ROWS_BF16>;
       smem = GemmCfg<BN, false, true>::SMEM_BYTES;
     }
   }
