@@ -956,8 +956,8 @@ __global__ void __launch_bounds__(LB_THREADS, 1) ln_backward_rows_kernel(const L
     if constexpr (kOdd) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const auto one = [&](int e) { return p.gamma && c + e < k ? load_param(p.gamma, p.param_f32, c0 + c + e) : 1.0f; };
-        gam[j].v[i] = make_float2(one(2 * i), one(2 * i + 1));
+        gam[j].v[i].x = p.gamma && c + 2 * i < k ? load_param(p.gamma, p.param_f32, c0 + c + 2 * i) : 1.0f;
+        gam[j].v[i].y = p.gamma && c + 2 * i + 1 < k ? load_param(p.gamma, p.param_f32, c0 + c + 2 * i + 1) : 1.0f;
       }
     } else {
       const int in = c0 + min(c, k - 8);
