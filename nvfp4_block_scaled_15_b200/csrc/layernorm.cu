@@ -1092,7 +1092,7 @@ __global__ void __launch_bounds__(LB_THREADS, 1) ln_backward_rows_kernel(const L
 // threads of a group hold elements t, t + NT, ... as in the forward kernel, and
 // their column sums.  A row's loads, sums and stores alternate; the block's other
 // groups and the number of elements in flight (three operands) keep the memory
-// busy.  Longer and more rows go through the ring kernel above.
+// busy.  dispatch_backward says which rows the ring kernel above takes instead.
 constexpr int LB_ODD_ELEMS = 16;
 constexpr int LB_ODD_K = LB_THREADS * LB_ODD_ELEMS;
 template <typename TX, typename TDY, typename TP, int NT>
@@ -1463,6 +1463,12 @@ cudaError_t run_backward_long(const LnBwdParams& p, float* dgamma, float* dbeta,
   return cudaGetLastError();
 }
 
+// Rows that start anywhere, fp32 dy and x: up to LB_ODD_K elements the kernel
+// without a ring takes them at every size (dispatch_backward), so only rows cut
+// between blocks are left for the ring.
+template <typename TX, typename TDY, bool kOdd>
+constexpr bool kRingAlone = !(kOdd && sizeof(TX) + sizeof(TDY) == 8);
+
 // A launch of the one-pass backward kernel: rows cut between `cluster` blocks.
 template <typename TX, typename TDY, bool kOdd, int S>
 cudaError_t run_backward_rows(const LnBwdParams& p, int cluster, int kc, float* dgamma, float* dbeta, uint32_t* mags,
@@ -1478,7 +1484,9 @@ cudaError_t run_backward_rows(const LnBwdParams& p, int cluster, int kc, float* 
   const int64_t sms = (device_sm_count() < LB_MAX_BLOCKS ? device_sm_count() : LB_MAX_BLOCKS) / cluster;
   const int64_t need = (p.rows + groups - 1) / groups;
   const int blocks = static_cast<int>(need < sms ? need : sms) * cluster;
-  auto kern = cluster > 1 ? ln_backward_rows_kernel<TX, TDY, kOdd, true, S> : ln_backward_rows_kernel<TX, TDY, kOdd, false, S>;
+  auto kern = ln_backward_rows_kernel<TX, TDY, kOdd, true, S>;
+  if constexpr (kRingAlone<TX, TDY, kOdd>)
+    if (cluster == 1) kern = ln_backward_rows_kernel<TX, TDY, kOdd, false, S>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   // the sum over blocks also joins their maxima: only without it has *amax to be cleared
   if (e == cudaSuccess && p.amax && !p.partial) e = cudaMemsetAsync(p.amax, 0, sizeof(float), s);
@@ -1505,7 +1513,7 @@ cudaError_t run_backward_rows(const LnBwdParams& p, int cluster, int kc, float* 
 // it: four stages, or three or two of long rows.
 template <typename TX, typename TDY, bool kOdd>
 bool try_backward_rows(const LnBwdParams& p, float* dgamma, float* dbeta, uint32_t* mags, cudaStream_t s, cudaError_t* e) {
-  for (int cluster = 1; cluster <= LB_MAX_CLUSTER; cluster *= 2) {
+  for (int cluster = kRingAlone<TX, TDY, kOdd> ? 1 : 2; cluster <= LB_MAX_CLUSTER; cluster *= 2) {
     const int64_t kc = ((static_cast<int64_t>(p.k) + cluster - 1) / cluster + 7) / 8 * 8;
     if (kc > LB_MAX_COLS || kc * (cluster - 1) >= p.k) continue;
     const int cols = static_cast<int>(kc);
@@ -1568,10 +1576,13 @@ cudaError_t dispatch_backward_odd(const LnBwdParams& p, float* dgamma, float* db
 template <typename TX, typename TDY>
 cudaError_t dispatch_backward(const LnBwdParams& p, bool vec, float* dgamma, float* dbeta, uint32_t* mags, cudaStream_t s) {
   if (p.k <= LB_SHORT_K) return run_backward_short<TX, TDY>(p, dgamma, dbeta, mags, s);
-  // up to a few million elements (by their bytes) the kernel without a ring, whose blocks start sooner: 100 x 1155 bf16
-  // 9.2 against 12.4 us, 1500 x 1155 17.8 against 20.7; 500 x 4095 22 against 20.5, 1500 x 4095 98 against 44
+  // The kernel without a ring: fp32 rows at every size, whose accesses fill whole sectors (1500 x 1155 13.9 us against
+  // 23.9 of the ring, 20000 x 1155 88 against 176, 3000 x 8001 105 against 196).  With a 16-bit type up to a few million
+  // elements (by their bytes), where it wins by its blocks' earlier start: bf16 100 x 1155 9.2 against 12.4 us, 8000 x 301
+  // 20 against 22; 700 x 4095 39 against 24, 20000 x 1155 266 against 111; fp32 x with bf16 dy 3000 x 1155 47 against 36
   if (!vec && p.k <= LB_ODD_K &&
-      p.rows * p.k * static_cast<int64_t>(sizeof(TX) + sizeof(TDY)) <= (int64_t{1} << 23))
+      (!kRingAlone<TX, TDY, true> ||
+       p.rows * p.k * static_cast<int64_t>(sizeof(TX) + sizeof(TDY)) <= (int64_t{1} << 23)))
     return p.param_f32 ? dispatch_backward_odd<TX, TDY, float>(p, dgamma, dbeta, mags, s)
                        : dispatch_backward_odd<TX, TDY, __nv_bfloat16>(p, dgamma, dbeta, mags, s);
   cudaError_t e = cudaSuccess;

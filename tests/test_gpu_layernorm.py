@@ -189,6 +189,16 @@ def test_backward(lib, rows, k, xd, dyd, pd, res, pad, off):
     untouched(flat, dx)
 
 
+@pytest.mark.parametrize("rows,k", [(20000, 66), (9001, 301), (4003, 1155), (1200, 4095), (700, 8191)], ids=str)
+@pytest.mark.parametrize("xd,dyd", [(F32, F32), (F32, BF16), (BF16, F32), (BF16, BF16)], ids=["f32", "f32_bf16", "bf16_f32", "bf16"])
+def test_backward_many_rows_that_start_anywhere(lib, rows, k, xd, dyd):
+    """Several rounds of rows per group, on both sides of the choice between the ring and rows straight from memory."""
+    inputs = backward_inputs(rows, k, xd, dyd, BF16, True, 1, 1)
+    dx, flat = placed(torch.full((rows, k), 7.0), xd, 1, 1)
+    check_backward(inputs, dx, run_backward(lib, *inputs, dx))
+    untouched(flat, dx)
+
+
 @pytest.mark.parametrize("k", [72, 1155, 8192, 33000])
 def test_backward_in_place_on_the_residual_gradient(lib, k):
     inputs = backward_inputs(20, k, BF16, BF16, F32, True)
