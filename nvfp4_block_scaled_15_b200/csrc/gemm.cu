@@ -1771,9 +1771,10 @@ nvfp4_status run_gemm(const void* a_codes, const void* a_sf, const float* g_a, c
 
 // Most 128 x 128 tiles of an epilogue GEMM that takes one of them per SM instead
 // of a 256 x 256 tile per CTA pair (or a 128 x 256 tile per SM for M <= 128):
-// 64 x 8192 x 8192 24.6 against 38.4 us, 301 x 1001 x 2112 fp32 15.6 against 22.6,
-// 1024 x 2048 x 2048 14.4 against 15.9; with more tiles than SMs the larger ones
-// win: 2048 x 2048 x 8192 26.7 against 37.8 us.
+// 64 x 8192 x 8192 24.6 against 38.4 us, 301 x 1001 x 2112 fp32 16.4 against 22.7,
+// 1024 x 2048 x 2048 15.5 against 16.4; with more tiles than SMs the larger ones
+// win: 2048 x 2048 x 8192 26.7 against 37.8 us.  (At the lower clocks behind a
+// GEMM that met the power cap: 301 x 1001 x 2112 20.5 against 29.4.)
 constexpr int64_t EPI_SMALL_TILES = 148;
 
 template <bool kMx>
