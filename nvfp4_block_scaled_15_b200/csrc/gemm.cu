@@ -392,8 +392,8 @@ __device__ __forceinline__ void box_rows_in(uint8_t* box, const void* base, int6
 }
 
 // x = alpha acc + bias of a box; bias: its 32 values in shared memory (16-byte
-// reads that every lane shares; lane-to-lane shuffles instead took 10 us of a
-// 4096 x 8192 x 1024 call's 47), or null.
+// reads that every lane shares; with lane-to-lane shuffles instead 4096 x 8192 x
+// 1024 took 47 us, 43 so), or null.
 __device__ __forceinline__ void box_values(const uint32_t* v, float alpha, const float* bias, BoxRow& x) {
 #pragma unroll
   for (int i = 0; i < EPI_BOX / 4; ++i) {

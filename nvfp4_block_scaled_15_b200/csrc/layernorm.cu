@@ -70,7 +70,7 @@ struct LnParams {
 };
 
 // Few blocks: a single cluster, whose first block writes the maximum; clearing
-// it first would take another launch, a third of a decoding step's call.
+// it first would take another launch, 8 x 8192 6.2 us against 4.4.
 constexpr int LF_MAX_CLUSTER = 8;
 
 __device__ __forceinline__ void publish_amax(const LnParams& p, uint32_t mag, uint32_t* mags) {
