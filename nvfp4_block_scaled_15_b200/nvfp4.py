@@ -488,9 +488,14 @@ def _dtype_of(t) -> int:
 
 
 def _rows_of(t, shape=None):
+    """Row pitch of a row-major matrix.  Rows may not overlap (a broadcast's pitch is 0): the library takes rows times
+    pitch elements of memory.  The stride of a single row says nothing."""
     assert t.dim() == 2 and (t.shape[1] <= 1 or t.stride(1) == 1), "a row-major matrix"
     assert shape is None or tuple(t.shape) == tuple(shape), (tuple(t.shape), tuple(shape))
-    return max(t.stride(0), t.shape[1])
+    if t.shape[0] <= 1:
+        return t.shape[1]
+    assert t.stride(0) >= t.shape[1], f"rows that overlap: a pitch of {t.stride(0)} for {t.shape[1]} columns"
+    return t.stride(0)
 
 
 class Normalized:

@@ -117,3 +117,67 @@ def test_workspace_sizes(nv):
         assert nv.nvfp4_workspace_bytes(op, 4, 0, 0) == 0
         assert nv.nvfp4_workspace_bytes(op, 1 << 31, 33, 0) == 0
         assert nv.nvfp4_workspace_bytes(op, 4, (1 << 28) + 1, 0) == 0
+
+
+# ---------------------------------------------------------------------------
+# the torch helpers
+# ---------------------------------------------------------------------------
+def quantized(nv, rows, k):
+    return nv.empty_quantized(rows, k, device="cpu")
+
+
+def overlapping(rows, k, dtype):
+    """A broadcast vector (pitch 0) and windows that overlap (pitch 10): rows that share memory."""
+    return [torch.zeros(k, dtype=dtype).expand(rows, k), torch.zeros(10 * rows + k, dtype=dtype).as_strided((rows, k), (10, 1))]
+
+
+def helper_calls(nv, rows=300, k=64, n=128):
+    """{operand: call of its helper with that operand replaced}; no call gets as far as the device."""
+    t = torch.zeros(rows, k, dtype=torch.bfloat16)
+    few, wide = torch.zeros(9, k, dtype=torch.bfloat16), torch.zeros(rows, n, dtype=torch.bfloat16)
+    stat = torch.zeros(rows)
+    a, w = quantized(nv, rows, k), quantized(nv, n, k)
+    back = lambda **c: nv.layernorm_backward(c.get("dy", t), c.get("x", t), stat, stat, d_residual=c.get("res"), out=c.get("out"), stream=0)
+    return {
+        "layernorm x": (rows, k, lambda v: nv.layernorm(v, stream=0)),
+        "layernorm out": (rows, k, lambda v: nv.layernorm(t, out=v, stream=0)),
+        "layernorm_backward dy": (rows, k, lambda v: back(dy=v)),
+        "layernorm_backward x": (rows, k, lambda v: back(x=v)),
+        "layernorm_backward d_residual": (rows, k, lambda v: back(res=v)),
+        "layernorm_backward out": (rows, k, lambda v: back(out=v)),
+        "gemm_epilogue residual": (rows, n, lambda v: nv.gemm_epilogue(a, w, residual=v, stream=0)),
+        "gemm_epilogue out": (rows, n, lambda v: nv.gemm_epilogue(a, w, out=v, stream=0)),
+        "gemm_epilogue pre": (rows, n, lambda v: nv.gemm_epilogue(a, w, pre=v, stream=0)),
+        "gemv_batched_epilogue x": (9, k, lambda v: nv.gemv_batched_epilogue(v, w, stream=0)),
+        "gemv_batched_epilogue residual": (9, n, lambda v: nv.gemv_batched_epilogue(few, w, residual=v, stream=0)),
+        "gemv_batched_epilogue out": (9, n, lambda v: nv.gemv_batched_epilogue(few, w, out=v, stream=0)),
+        "epilogue_backward dd": (rows, n, lambda v: nv.epilogue_backward(v, None, stream=0)),
+        "epilogue_backward pre": (rows, n, lambda v: nv.epilogue_backward(wide, v, "relu", stream=0)),
+        "epilogue_backward out": (rows, n, lambda v: nv.epilogue_backward(wide, None, out=v, stream=0)),
+    }
+
+
+@pytest.mark.parametrize("operand", [
+    "layernorm x", "layernorm out", "layernorm_backward dy", "layernorm_backward x", "layernorm_backward d_residual",
+    "layernorm_backward out", "gemm_epilogue residual", "gemm_epilogue out", "gemm_epilogue pre", "gemv_batched_epilogue x",
+    "gemv_batched_epilogue residual", "gemv_batched_epilogue out", "epilogue_backward dd", "epilogue_backward pre",
+    "epilogue_backward out"])
+def test_helpers_refuse_rows_that_overlap(nv, operand):
+    """Their buffer holds fewer elements than rows times columns: taken as dense rows they would be read, or written,
+    past its end."""
+    rows, cols, call = helper_calls(nv)[operand]
+    for v in overlapping(rows, cols, torch.bfloat16):
+        with pytest.raises(AssertionError, match="overlap"):
+            call(v)
+
+
+def test_pitch_of_a_single_row(nv):
+    """The stride of a matrix of one row (or none) says nothing; of more rows it is the pitch."""
+    flat = torch.zeros(1000)
+    assert nv._rows_of(flat.as_strided((1, 64), (0, 1))) == 64
+    assert nv._rows_of(flat.as_strided((1, 64), (999, 1))) == 64
+    assert nv._rows_of(flat.as_strided((0, 64), (0, 1))) == 64
+    assert nv._rows_of(flat.as_strided((2, 64), (70, 1))) == 70
+    assert nv._rows_of(flat.as_strided((5, 1), (3, 9))) == 3
+    with pytest.raises(AssertionError, match="overlap"):
+        nv._rows_of(flat.as_strided((5, 1), (0, 1)))
