@@ -9,6 +9,8 @@ importing this module fails loudly otherwise.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 
 import torch
@@ -300,6 +302,30 @@ def raw_status(name: str, *args) -> int:
 # ---------------------------------------------------------------------------
 # allocation helpers (torch owns the memory; the work runs in the library)
 # ---------------------------------------------------------------------------
+def _on_its_stream(helper):
+    """A helper called with ``stream=`` runs with that stream current, so that what it allocates (outputs, workspace) and
+    copies belongs to that stream: torch's allocator hands memory out, and again once it is dropped, in the order of
+    the stream that it was allocated on.  Outputs are the given stream's then; the inputs have to be ready on it."""
+    at = list(inspect.signature(helper).parameters).index("stream")
+
+    @functools.wraps(helper)
+    def call(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return helper(*args, **kw)
+        with torch.cuda.stream(_stream_of(stream)):
+            return helper(*args, **kw)
+
+    return call
+
+
+def _stream_of(stream):
+    """torch's stream of a stream or a cudaStream_t handle (0 and 1 name the default stream)."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(stream)) if int(stream) > 1 else torch.cuda.default_stream()
+
+
 class Quantized:
     """NVFP4 tensor: codes [rows, k/2] uint8, sf (layout bytes), g and amax (one fp32 each, on device)."""
 
@@ -315,6 +341,7 @@ def empty_quantized(rows: int, k: int, layout: int = SF_TCGEN05, device="cuda") 
     return Quantized(codes, sf, scal[0:1], scal[4:5], rows, k, layout)
 
 
+@_on_its_stream
 def quantize(x: torch.Tensor, layout: int = SF_TCGEN05, out: Quantized | None = None, amax=None,
              stream=None) -> Quantized:
     """bf16 [rows, k] (row pitch x.stride(0)) -> NVFP4.  ``amax`` (device fp32) skips the amax pass."""
@@ -328,6 +355,7 @@ def quantize(x: torch.Tensor, layout: int = SF_TCGEN05, out: Quantized | None = 
     return q
 
 
+@_on_its_stream
 def quantize_stochastic(x: torch.Tensor, seed: int, offset: int, layout: int = SF_TCGEN05,
                         out: Quantized | None = None, amax=None, stream=None) -> Quantized:
     """bf16 [rows, k] -> NVFP4 with stochastically rounded codes (Philox4x32-10 bits from seed, offset)."""
@@ -341,6 +369,7 @@ def quantize_stochastic(x: torch.Tensor, seed: int, offset: int, layout: int = S
     return q
 
 
+@_on_its_stream
 def quantize_hadamard(x: torch.Tensor, order: int, layout: int = SF_TCGEN05, out: Quantized | None = None,
                       amax=None, stream=None) -> Quantized:
     """bf16 [rows, k] -> NVFP4 of y = x H (block-diagonal Walsh-Hadamard of the given order over
@@ -355,6 +384,7 @@ def quantize_hadamard(x: torch.Tensor, order: int, layout: int = SF_TCGEN05, out
     return q
 
 
+@_on_its_stream
 def quantize_hadamard_stochastic(x: torch.Tensor, order: int, seed: int, offset: int, layout: int = SF_TCGEN05,
                                  out: Quantized | None = None, amax=None, stream=None) -> Quantized:
     """bf16 [rows, k] -> NVFP4 of y = x H with stochastically rounded codes."""
@@ -368,6 +398,7 @@ def quantize_hadamard_stochastic(x: torch.Tensor, order: int, seed: int, offset:
     return q
 
 
+@_on_its_stream
 def gemm(a: Quantized, b: Quantized, out_dtype=torch.bfloat16, out: torch.Tensor | None = None,
          stream=None) -> torch.Tensor:
     """D [M, N] = alpha (s_a A)(s_b B)^T for two TCGEN05-layout NVFP4 operands."""
@@ -378,6 +409,7 @@ def gemm(a: Quantized, b: Quantized, out_dtype=torch.bfloat16, out: torch.Tensor
     return d
 
 
+@_on_its_stream
 def gemm_requant(a: Quantized, b: Quantized, g_d: torch.Tensor, layout: int = SF_TCGEN05,
                  out: Quantized | None = None, stream=None) -> Quantized:
     """D = alpha (s_a A)(s_b B)^T quantized to NVFP4 under the given encode
@@ -390,6 +422,7 @@ def gemm_requant(a: Quantized, b: Quantized, g_d: torch.Tensor, layout: int = SF
     return q
 
 
+@_on_its_stream
 def gemm_fp8_out(a: Quantized, b: Quantized, g_d: torch.Tensor, out: torch.Tensor | None = None,
                  amax_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """FP8 (float8_e4m3fn) e4m3(v * g_d) for v = alpha (s_a A)(s_b B)^T; amax_out receives max |v|."""
@@ -400,6 +433,7 @@ def gemm_fp8_out(a: Quantized, b: Quantized, g_d: torch.Tensor, out: torch.Tenso
     return d
 
 
+@_on_its_stream
 def gemv_batched(x: torch.Tensor, w: Quantized, out: torch.Tensor | None = None, workspace=None,
                  stream=None) -> torch.Tensor:
     """y [M, N] for bf16 activations x [M, K] (M <= 32) and NVFP4 weights w [N, K]."""
@@ -412,6 +446,7 @@ def gemv_batched(x: torch.Tensor, w: Quantized, out: torch.Tensor | None = None,
     return y
 
 
+@_on_its_stream
 def gemm_quant_a(a: torch.Tensor, b: Quantized, out_dtype=torch.bfloat16, out=None, workspace=None,
                  stream=None, amax: torch.Tensor | None = None) -> torch.Tensor:
     """D = A_q @ B_q^T with a bf16 A quantized inside the call; amax: A's tensor
@@ -449,6 +484,7 @@ class MXQuantized:
         self.rows, self.k, self.layout = rows, k, layout
 
 
+@_on_its_stream
 def mxfp4_quantize(x: torch.Tensor, layout: int = SF_TCGEN05, out: MXQuantized | None = None,
                    stream=None) -> MXQuantized:
     """bf16 [rows, k] (row pitch x.stride(0)) -> MXFP4 (one pass)."""
@@ -462,6 +498,7 @@ def mxfp4_quantize(x: torch.Tensor, layout: int = SF_TCGEN05, out: MXQuantized |
     return out
 
 
+@_on_its_stream
 def mxfp4_gemm(a: MXQuantized, b: MXQuantized, out_dtype=torch.bfloat16, out: torch.Tensor | None = None,
                stream=None) -> torch.Tensor:
     """D [M, N] = (s_a A)(s_b B)^T for two TCGEN05-layout MXFP4 operands."""
@@ -505,6 +542,7 @@ class Normalized:
         self.y, self.mean, self.rstd, self.amax = y, mean, rstd, amax
 
 
+@_on_its_stream
 def layernorm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
               eps: float = 1e-5, out_dtype=torch.bfloat16, out: torch.Tensor | None = None,
               stream=None) -> Normalized:
@@ -523,6 +561,7 @@ def layernorm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.T
     return Normalized(y, mean, rstd, amax)
 
 
+@_on_its_stream
 def layernorm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
                        weight: torch.Tensor | None = None, d_residual: torch.Tensor | None = None,
                        out: torch.Tensor | None = None, workspace=None, stream=None):
@@ -550,6 +589,7 @@ def _check_epilogue(m, n, bias, residual, dtype) -> int:
     return 0 if residual is None else _rows_of(residual, (m, n))
 
 
+@_on_its_stream
 def gemm_epilogue(a: Quantized, b: Quantized, bias: torch.Tensor | None = None, act: str | None = None,
                   residual: torch.Tensor | None = None, out_dtype=torch.bfloat16, out: torch.Tensor | None = None,
                   pre: torch.Tensor | bool = False, amax: torch.Tensor | None = None, stream=None):
@@ -567,6 +607,7 @@ def gemm_epilogue(a: Quantized, b: Quantized, bias: torch.Tensor | None = None, 
     return (d, p) if pre is True else d
 
 
+@_on_its_stream
 def gemv_batched_epilogue(x: torch.Tensor, w: Quantized, bias: torch.Tensor | None = None, act: str | None = None,
                           residual: torch.Tensor | None = None, out: torch.Tensor | None = None, workspace=None,
                           stream=None) -> torch.Tensor:
@@ -584,6 +625,7 @@ def gemv_batched_epilogue(x: torch.Tensor, w: Quantized, bias: torch.Tensor | No
     return y
 
 
+@_on_its_stream
 def epilogue_backward(dd: torch.Tensor, pre: torch.Tensor | None, act: str | None = None,
                       out: torch.Tensor | None = None, workspace=None, stream=None):
     """(dpre, dbias, amax of dpre) of D = act(pre) [+ residual], pre = product + bias; dbias fp32."""

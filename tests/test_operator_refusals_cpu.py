@@ -137,23 +137,23 @@ def helper_calls(nv, rows=300, k=64, n=128):
     few, wide = torch.zeros(9, k, dtype=torch.bfloat16), torch.zeros(rows, n, dtype=torch.bfloat16)
     stat = torch.zeros(rows)
     a, w = quantized(nv, rows, k), quantized(nv, n, k)
-    back = lambda **c: nv.layernorm_backward(c.get("dy", t), c.get("x", t), stat, stat, d_residual=c.get("res"), out=c.get("out"), stream=0)
+    back = lambda **c: nv.layernorm_backward(c.get("dy", t), c.get("x", t), stat, stat, d_residual=c.get("res"), out=c.get("out"))
     return {
-        "layernorm x": (rows, k, lambda v: nv.layernorm(v, stream=0)),
-        "layernorm out": (rows, k, lambda v: nv.layernorm(t, out=v, stream=0)),
+        "layernorm x": (rows, k, lambda v: nv.layernorm(v)),
+        "layernorm out": (rows, k, lambda v: nv.layernorm(t, out=v)),
         "layernorm_backward dy": (rows, k, lambda v: back(dy=v)),
         "layernorm_backward x": (rows, k, lambda v: back(x=v)),
         "layernorm_backward d_residual": (rows, k, lambda v: back(res=v)),
         "layernorm_backward out": (rows, k, lambda v: back(out=v)),
-        "gemm_epilogue residual": (rows, n, lambda v: nv.gemm_epilogue(a, w, residual=v, stream=0)),
-        "gemm_epilogue out": (rows, n, lambda v: nv.gemm_epilogue(a, w, out=v, stream=0)),
-        "gemm_epilogue pre": (rows, n, lambda v: nv.gemm_epilogue(a, w, pre=v, stream=0)),
-        "gemv_batched_epilogue x": (9, k, lambda v: nv.gemv_batched_epilogue(v, w, stream=0)),
-        "gemv_batched_epilogue residual": (9, n, lambda v: nv.gemv_batched_epilogue(few, w, residual=v, stream=0)),
-        "gemv_batched_epilogue out": (9, n, lambda v: nv.gemv_batched_epilogue(few, w, out=v, stream=0)),
-        "epilogue_backward dd": (rows, n, lambda v: nv.epilogue_backward(v, None, stream=0)),
-        "epilogue_backward pre": (rows, n, lambda v: nv.epilogue_backward(wide, v, "relu", stream=0)),
-        "epilogue_backward out": (rows, n, lambda v: nv.epilogue_backward(wide, None, out=v, stream=0)),
+        "gemm_epilogue residual": (rows, n, lambda v: nv.gemm_epilogue(a, w, residual=v)),
+        "gemm_epilogue out": (rows, n, lambda v: nv.gemm_epilogue(a, w, out=v)),
+        "gemm_epilogue pre": (rows, n, lambda v: nv.gemm_epilogue(a, w, pre=v)),
+        "gemv_batched_epilogue x": (9, k, lambda v: nv.gemv_batched_epilogue(v, w)),
+        "gemv_batched_epilogue residual": (9, n, lambda v: nv.gemv_batched_epilogue(few, w, residual=v)),
+        "gemv_batched_epilogue out": (9, n, lambda v: nv.gemv_batched_epilogue(few, w, out=v)),
+        "epilogue_backward dd": (rows, n, lambda v: nv.epilogue_backward(v, None)),
+        "epilogue_backward pre": (rows, n, lambda v: nv.epilogue_backward(wide, v, "relu")),
+        "epilogue_backward out": (rows, n, lambda v: nv.epilogue_backward(wide, None, out=v)),
     }
 
 
