@@ -1312,6 +1312,14 @@ __global__ void __launch_bounds__(256) sum_partials_kernel(const float* partial,
 constexpr int LN_CHUNKS = 64;
 constexpr int LB_MAX_BLOCKS = 160;     // of the one-pass backward kernel; a workspace is sized for it
 
+// A kernel's limit of dynamic shared memory is one for the function, whoever
+// calls it: set to the most that any call of it asks for, never to a call's own
+// size, which another thread's launch between the two steps would find too small.
+template <typename Kernel>
+cudaError_t allow_shared(Kernel kern, int most) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+}
+
 // Launches a forward kernel for `need` blocks' worth of rows, `most` of them at
 // a time.  Up to a cluster's blocks go as one cluster.
 template <typename Kernel>
@@ -1322,7 +1330,7 @@ cudaError_t launch_forward(Kernel kern, LnParams p, int64_t need, int64_t most, 
   }
   cudaError_t e = cudaSuccess;
   if (p.amax && !p.joined) e = cudaMemsetAsync(p.amax, 0, sizeof(float), s);
-  if (e == cudaSuccess && smem > 0) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && smem > 0) e = allow_shared(kern, LI_SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -1487,7 +1495,8 @@ cudaError_t run_backward_rows(const LnBwdParams& p, int cluster, int kc, float* 
   auto kern = ln_backward_rows_kernel<TX, TDY, kOdd, true, S>;
   if constexpr (kRingAlone<TX, TDY, kOdd>)
     if (cluster == 1) kern = ln_backward_rows_kernel<TX, TDY, kOdd, false, S>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  static_assert(LB_THREADS * 8 * LB_NV * 2 * 4 <= LB_SMEM, "the column sums of all groups fit where the rings do");
+  cudaError_t e = allow_shared(kern, LB_SMEM);
   // the sum over blocks also joins their maxima: only without it has *amax to be cleared
   if (e == cudaSuccess && p.amax && !p.partial) e = cudaMemsetAsync(p.amax, 0, sizeof(float), s);
   if (e != cudaSuccess) return e;
@@ -1555,7 +1564,7 @@ cudaError_t run_backward_odd(const LnBwdParams& p, float* dgamma, float* dbeta, 
   const int blocks = static_cast<int>(need < most ? need : most);
   const int smem = p.partial ? GROUPS * 2 * p.k * static_cast<int>(sizeof(float)) : 0;
   auto kern = ln_backward_odd_kernel<TX, TDY, TP, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_shared(kern, LB_THREADS * LB_ODD_ELEMS * 2 * static_cast<int>(sizeof(float)));   // GROUPS * k at most
   if (e == cudaSuccess && p.amax && !p.partial) e = cudaMemsetAsync(p.amax, 0, sizeof(float), s);
   if (e != cudaSuccess) return e;
   kern<<<blocks, LB_THREADS, smem, s>>>(p, mags);
