@@ -183,7 +183,7 @@ nvfp4_status nvfp4_quantize(const void* x_bf16, int64_t rows, int64_t k, int64_t
     st = launch_amax(x_bf16, rows, k, ldx, amax_dev, s);
     if (st != NVFP4_OK) return st;
   }
-  return launch_quantize(x_bf16, rows, k, ldx, codes, sf, layout, g_dev, amax_dev, s);
+  return launch_quantize(x_bf16, rows, k, ldx, codes, sf, layout, g_dev, amax_dev, !amax_given, s);
 }
 
 nvfp4_status nvfp4_quantize_stochastic(const void* x_bf16, int64_t rows, int64_t k, int64_t ldx, void* codes,
@@ -203,7 +203,7 @@ nvfp4_status nvfp4_quantize_stochastic(const void* x_bf16, int64_t rows, int64_t
     st = launch_amax(x_bf16, rows, k, ldx, amax_dev, s);
     if (st != NVFP4_OK) return st;
   }
-  return launch_quantize_sr(x_bf16, rows, k, ldx, codes, sf, layout, g_dev, amax_dev, seed, offset, s);
+  return launch_quantize_sr(x_bf16, rows, k, ldx, codes, sf, layout, g_dev, amax_dev, !amax_given, seed, offset, s);
 }
 
 static nvfp4_status quantize_hadamard_common(const void* x_bf16, int64_t rows, int64_t k, int64_t ldx, int n,
@@ -226,8 +226,8 @@ static nvfp4_status quantize_hadamard_common(const void* x_bf16, int64_t rows, i
     st = launch_hadamard_amax(x_bf16, rows, k, ldx, n, amax_dev, s);
     if (st != NVFP4_OK) return st;
   }
-  return launch_hadamard_quantize(x_bf16, rows, k, ldx, n, codes, sf, layout, g_dev, amax_dev, stochastic, seed,
-                                  offset, s);
+  return launch_hadamard_quantize(x_bf16, rows, k, ldx, n, codes, sf, layout, g_dev, amax_dev, !amax_given, stochastic,
+                                  seed, offset, s);
 }
 
 nvfp4_status nvfp4_quantize_hadamard(const void* x_bf16, int64_t rows, int64_t k, int64_t ldx, int hadamard_order,
@@ -453,8 +453,8 @@ nvfp4_status gemm_quant_a_common(QaMode mode, const void* a_bf16, int64_t lda, c
   if (fused)
     return launch_gemm_quant_a_fused(a_bf16, lda, amax, a_codes, a_sf, g_a, counters, ticket, b_codes, b_sf_tc,
                                      g_b_dev, M, N, K, d, ldd, out_dtype, s);
-  if ((st = launch_quantize(a_bf16, M, K, lda, a_codes, a_sf, NVFP4_SF_TCGEN05, g_a, amax, s)) != NVFP4_OK)
-    return st;
+  st = launch_quantize(a_bf16, M, K, lda, a_codes, a_sf, NVFP4_SF_TCGEN05, g_a, amax, mode != QaMode::kAmaxGiven, s);
+  if (st != NVFP4_OK) return st;
   return launch_gemm(a_codes, a_sf, g_a, b_codes, b_sf_tc, g_b_dev, M, N, K, d, ldd, out_dtype, s);
 }
 

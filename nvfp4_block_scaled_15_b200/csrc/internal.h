@@ -35,19 +35,22 @@ nvfp4_status launch_amax(const void* x, int64_t rows, int64_t k, int64_t ldx, fl
 // does not clear *amax_dev: the caller zeroes it first.
 nvfp4_status launch_amax_reversed(const void* x, int64_t rows, int64_t k, int64_t ldx, float* amax_dev,
                                   cudaStream_t s);
+// Quantize passes.  after_amax: an amax pass over x has been launched on the
+// stream since x was written (with a given amax: not so).
 nvfp4_status launch_quantize(const void* x, int64_t rows, int64_t k, int64_t ldx, void* codes, void* sf,
-                             nvfp4_sf_layout layout, float* g_dev, const float* amax_dev, cudaStream_t s);
+                             nvfp4_sf_layout layout, float* g_dev, const float* amax_dev, bool after_amax,
+                             cudaStream_t s);
 // Quantize pass with stochastic rounding of the codes (Philox4x32-10 bits).
 nvfp4_status launch_quantize_sr(const void* x, int64_t rows, int64_t k, int64_t ldx, void* codes, void* sf,
-                                nvfp4_sf_layout layout, float* g_dev, const float* amax_dev, uint64_t seed,
-                                uint64_t offset, cudaStream_t s);
+                                nvfp4_sf_layout layout, float* g_dev, const float* amax_dev, bool after_amax,
+                                uint64_t seed, uint64_t offset, cudaStream_t s);
 // Hadamard-rotated quantizer (order n: a power of two <= 512 dividing k).
 nvfp4_status launch_hadamard_amax(const void* x, int64_t rows, int64_t k, int64_t ldx, int n, float* amax_dev,
                                   cudaStream_t s);
 // stochastic: round the codes stochastically (Philox4x32-10 bits from seed, offset).
 nvfp4_status launch_hadamard_quantize(const void* x, int64_t rows, int64_t k, int64_t ldx, int n, void* codes,
                                       void* sf, nvfp4_sf_layout layout, float* g_dev, const float* amax_dev,
-                                      bool stochastic, uint64_t seed, uint64_t offset, cudaStream_t s);
+                                      bool after_amax, bool stochastic, uint64_t seed, uint64_t offset, cudaStream_t s);
 nvfp4_status launch_swizzle(const void* src, int64_t rows, int64_t k, void* dst, cudaStream_t s);
 nvfp4_status launch_mx_quantize(const void* x, int64_t rows, int64_t k, int64_t ldx, void* codes, void* sf,
                                 nvfp4_sf_layout layout, cudaStream_t s);

@@ -156,10 +156,10 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const uint16_t* __re
   const int b0 = blockIdx.y * kSegBlocks + static_cast<int>(threadIdx.x);
   const int b1 = b0 + kThreads;
 
-  // Launched as a programmatic dependent of the amax pass.  x is not written
-  // by that pass, so its loads and the scale table go out before the wait and
-  // overlap the pass's tail; only the amax is read after it, and every store
-  // comes after it.  (The kernels that release dependents early are the amax
+  // Launched as a programmatic dependent of the amax pass (with a given amax in
+  // the plain order, launch_quantize_pdl).  x is not written by that pass, so its
+  // loads and the scale table go out before the wait and overlap the pass's tail;
+  // only the amax is read after it, and every store comes after it.  (The kernels that release dependents early are the amax
   // passes and the GEMV prologue, none of which writes x; the amax pass itself
   // starts only after all earlier work on the stream has finished.)
   uint32_t w0[kRows][8], w1[kRows][8];
@@ -736,9 +736,15 @@ __global__ void swizzle_kernel(const uint8_t* __restrict__ src, int rows, int kb
 
 constexpr int kQuantRows = 2;                  // rows per CTA of the quantize pass
 
+// after_amax: an amax pass over x lies between x's writer and the quantize pass,
+// which is launched as its programmatic dependent.  With a given amax the kernel
+// in front may be x's writer itself.  Its writes are certain to be visible only
+// behind the wait, and the quantize pass reads x before it: it is then launched
+// in the plain order.
 template <bool kTc, bool kWide, int kRows = kQuantRows>
 cudaError_t launch_quantize_pdl(dim3 grid, cudaStream_t s, const uint16_t* x, int rows, int k, int64_t ldx,
-                                uint8_t* codes, uint8_t* sf, float* g_dev, const float* amax_dev, int* status) {
+                                uint8_t* codes, uint8_t* sf, float* g_dev, const float* amax_dev, bool after_amax,
+                                int* status) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(kThreads);
@@ -747,7 +753,7 @@ cudaError_t launch_quantize_pdl(dim3 grid, cudaStream_t s, const uint16_t* x, in
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = after_amax ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, quantize_kernel<kTc, kWide, kRows>, x, rows, k, ldx, codes, sf, g_dev, amax_dev,
                             status);
 }
@@ -755,7 +761,8 @@ cudaError_t launch_quantize_pdl(dim3 grid, cudaStream_t s, const uint16_t* x, in
 template <bool kTc, bool kWide, bool kSR, bool kAdj>
 cudaError_t launch_hadamard_quantize_pdl(dim3 grid, cudaStream_t s, const uint16_t* x, int rows, int k, int64_t ldx,
                                          int n, float c, uint8_t* codes, uint8_t* sf, float* g_dev,
-                                         const float* amax_dev, uint64_t seed, uint64_t offset, int* status) {
+                                         const float* amax_dev, bool after_amax, uint64_t seed, uint64_t offset,
+                                         int* status) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(kThreads);
@@ -764,7 +771,7 @@ cudaError_t launch_hadamard_quantize_pdl(dim3 grid, cudaStream_t s, const uint16
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = after_amax ? 1 : 0;
   if constexpr (kAdj)
     return cudaLaunchKernelEx(&cfg, hadamard_quantize_sr_adj_kernel<kTc, kWide>, x, rows, k, ldx, n, c, codes, sf,
                               g_dev, amax_dev, static_cast<uint32_t>(seed), static_cast<uint32_t>(seed >> 32),
@@ -779,8 +786,8 @@ constexpr int kSRRows = 2;                     // rows per CTA of the stochastic
 
 template <bool kTc, bool kWide>
 cudaError_t launch_quantize_sr_pdl(dim3 grid, cudaStream_t s, const uint16_t* x, int rows, int k, int64_t ldx,
-                                   uint8_t* codes, uint8_t* sf, float* g_dev, const float* amax_dev, uint64_t seed,
-                                   uint64_t offset, int* status) {
+                                   uint8_t* codes, uint8_t* sf, float* g_dev, const float* amax_dev, bool after_amax,
+                                   uint64_t seed, uint64_t offset, int* status) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(kThreads);
@@ -789,7 +796,7 @@ cudaError_t launch_quantize_sr_pdl(dim3 grid, cudaStream_t s, const uint16_t* x,
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = after_amax ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, quantize_sr_kernel<kTc, kWide, kSRRows>, x, rows, k, ldx, codes, sf, g_dev, amax_dev,
                             static_cast<uint32_t>(seed), static_cast<uint32_t>(seed >> 32),
                             static_cast<uint32_t>(offset), static_cast<uint32_t>(offset >> 32), status);
@@ -828,7 +835,8 @@ nvfp4_status launch_amax_reversed(const void* x, int64_t rows, int64_t k, int64_
 }
 
 nvfp4_status launch_quantize(const void* x, int64_t rows, int64_t k, int64_t ldx, void* codes, void* sf,
-                             nvfp4_sf_layout layout, float* g_dev, const float* amax_dev, cudaStream_t s) {
+                             nvfp4_sf_layout layout, float* g_dev, const float* amax_dev, bool after_amax,
+                             cudaStream_t s) {
   int* status = device_status_ptr();
   if (!status) return NVFP4_ERR_CUDA;
   const uint16_t* xs = static_cast<const uint16_t*>(x);
@@ -839,16 +847,16 @@ nvfp4_status launch_quantize(const void* x, int64_t rows, int64_t k, int64_t ldx
   const int ir = static_cast<int>(rows), ik = static_cast<int>(k);
   if (grid_rows == 0 || segs == 0)   // nothing to quantize: still publish g (from the given amax)
     return launch_status(launch_quantize_pdl<false, false>(dim3(1, 1), s, xs, 0, 0, ldx, cs, ss, g_dev, amax_dev,
-                                                           status));
+                                                           after_amax, status));
   const dim3 grid(static_cast<unsigned>((grid_rows + kQuantRows - 1) / kQuantRows), segs);
   const bool wide = (reinterpret_cast<uintptr_t>(x) & 31u) == 0 && (ldx % 16) == 0;
   cudaError_t e;
   if (layout == NVFP4_SF_TCGEN05)
-    e = wide ? launch_quantize_pdl<true, true>(grid, s, xs, ir, ik, ldx, cs, ss, g_dev, amax_dev, status)
-             : launch_quantize_pdl<true, false>(grid, s, xs, ir, ik, ldx, cs, ss, g_dev, amax_dev, status);
+    e = wide ? launch_quantize_pdl<true, true>(grid, s, xs, ir, ik, ldx, cs, ss, g_dev, amax_dev, after_amax, status)
+             : launch_quantize_pdl<true, false>(grid, s, xs, ir, ik, ldx, cs, ss, g_dev, amax_dev, after_amax, status);
   else
-    e = wide ? launch_quantize_pdl<false, true>(grid, s, xs, ir, ik, ldx, cs, ss, g_dev, amax_dev, status)
-             : launch_quantize_pdl<false, false>(grid, s, xs, ir, ik, ldx, cs, ss, g_dev, amax_dev, status);
+    e = wide ? launch_quantize_pdl<false, true>(grid, s, xs, ir, ik, ldx, cs, ss, g_dev, amax_dev, after_amax, status)
+             : launch_quantize_pdl<false, false>(grid, s, xs, ir, ik, ldx, cs, ss, g_dev, amax_dev, after_amax, status);
   return launch_status(e);
 }
 
@@ -913,16 +921,17 @@ namespace {
 template <bool kSR, bool kAdj>
 cudaError_t dispatch_hadamard_layout(dim3 grid, bool tc, bool wide, cudaStream_t s, const uint16_t* x, int rows,
                                      int k, int64_t ldx, int n, float c, uint8_t* codes, uint8_t* sf, float* g_dev,
-                                     const float* amax_dev, uint64_t seed, uint64_t offset, int* status) {
+                                     const float* amax_dev, bool after_amax, uint64_t seed, uint64_t offset,
+                                     int* status) {
   if (tc)
     return wide ? launch_hadamard_quantize_pdl<true, true, kSR, kAdj>(grid, s, x, rows, k, ldx, n, c, codes, sf,
-                                                                      g_dev, amax_dev, seed, offset, status)
+                                                                      g_dev, amax_dev, after_amax, seed, offset, status)
                 : launch_hadamard_quantize_pdl<true, false, kSR, kAdj>(grid, s, x, rows, k, ldx, n, c, codes, sf,
-                                                                       g_dev, amax_dev, seed, offset, status);
+                                                                       g_dev, amax_dev, after_amax, seed, offset, status);
   return wide ? launch_hadamard_quantize_pdl<false, true, kSR, kAdj>(grid, s, x, rows, k, ldx, n, c, codes, sf,
-                                                                     g_dev, amax_dev, seed, offset, status)
+                                                                     g_dev, amax_dev, after_amax, seed, offset, status)
               : launch_hadamard_quantize_pdl<false, false, kSR, kAdj>(grid, s, x, rows, k, ldx, n, c, codes, sf,
-                                                                      g_dev, amax_dev, seed, offset, status);
+                                                                      g_dev, amax_dev, after_amax, seed, offset, status);
 }
 
 // The stochastic pass takes two adjacent blocks per thread for orders
@@ -933,13 +942,14 @@ cudaError_t dispatch_hadamard_layout(dim3 grid, bool tc, bool wide, cudaStream_t
 template <bool kSR>
 cudaError_t dispatch_hadamard_quantize(dim3 grid, bool tc, bool wide, cudaStream_t s, const uint16_t* x, int rows,
                                        int k, int64_t ldx, int n, float c, uint8_t* codes, uint8_t* sf, float* g_dev,
-                                       const float* amax_dev, uint64_t seed, uint64_t offset, int* status) {
+                                       const float* amax_dev, bool after_amax, uint64_t seed, uint64_t offset,
+                                       int* status) {
   if constexpr (kSR) {
     if (n >= kAdjMinOrder)
       return dispatch_hadamard_layout<true, true>(grid, tc, wide, s, x, rows, k, ldx, n, c, codes, sf, g_dev,
-                                                  amax_dev, seed, offset, status);
+                                                  amax_dev, after_amax, seed, offset, status);
   }
-  return dispatch_hadamard_layout<kSR, false>(grid, tc, wide, s, x, rows, k, ldx, n, c, codes, sf, g_dev, amax_dev,
+  return dispatch_hadamard_layout<kSR, false>(grid, tc, wide, s, x, rows, k, ldx, n, c, codes, sf, g_dev, amax_dev, after_amax,
                                               seed, offset, status);
 }
 
@@ -947,7 +957,7 @@ cudaError_t dispatch_hadamard_quantize(dim3 grid, bool tc, bool wide, cudaStream
 
 nvfp4_status launch_hadamard_quantize(const void* x, int64_t rows, int64_t k, int64_t ldx, int n, void* codes,
                                       void* sf, nvfp4_sf_layout layout, float* g_dev, const float* amax_dev,
-                                      bool stochastic, uint64_t seed, uint64_t offset, cudaStream_t s) {
+                                      bool after_amax, bool stochastic, uint64_t seed, uint64_t offset, cudaStream_t s) {
   int* status = device_status_ptr();
   if (!status) return NVFP4_ERR_CUDA;
   const uint16_t* xs = static_cast<const uint16_t*>(x);
@@ -965,16 +975,16 @@ nvfp4_status launch_hadamard_quantize(const void* x, int64_t rows, int64_t k, in
   const bool tc = !empty && layout == NVFP4_SF_TCGEN05;
   const bool wide = !empty && (reinterpret_cast<uintptr_t>(x) & 31u) == 0 && (ldx % 16) == 0;
   const cudaError_t e =
-      stochastic ? dispatch_hadamard_quantize<true>(grid, tc, wide, s, xs, ir, ik, ldx, n, c, cs, ss, g_dev, amax_dev,
+      stochastic ? dispatch_hadamard_quantize<true>(grid, tc, wide, s, xs, ir, ik, ldx, n, c, cs, ss, g_dev, amax_dev, after_amax,
                                                     seed, offset, status)
                  : dispatch_hadamard_quantize<false>(grid, tc, wide, s, xs, ir, ik, ldx, n, c, cs, ss, g_dev,
-                                                     amax_dev, seed, offset, status);
+                                                     amax_dev, after_amax, seed, offset, status);
   return launch_status(e);
 }
 
 nvfp4_status launch_quantize_sr(const void* x, int64_t rows, int64_t k, int64_t ldx, void* codes, void* sf,
-                                nvfp4_sf_layout layout, float* g_dev, const float* amax_dev, uint64_t seed,
-                                uint64_t offset, cudaStream_t s) {
+                                nvfp4_sf_layout layout, float* g_dev, const float* amax_dev, bool after_amax,
+                                uint64_t seed, uint64_t offset, cudaStream_t s) {
   int* status = device_status_ptr();
   if (!status) return NVFP4_ERR_CUDA;
   const uint16_t* xs = static_cast<const uint16_t*>(x);
@@ -984,20 +994,20 @@ nvfp4_status launch_quantize_sr(const void* x, int64_t rows, int64_t k, int64_t 
   const int64_t grid_rows = layout == NVFP4_SF_TCGEN05 ? round_up(rows, 128) : rows;
   const int ir = static_cast<int>(rows), ik = static_cast<int>(k);
   if (grid_rows == 0 || segs == 0)
-    return launch_status(launch_quantize_sr_pdl<false, false>(dim3(1, 1), s, xs, 0, 0, ldx, cs, ss, g_dev, amax_dev,
+    return launch_status(launch_quantize_sr_pdl<false, false>(dim3(1, 1), s, xs, 0, 0, ldx, cs, ss, g_dev, amax_dev, after_amax,
                                                               seed, offset, status));
   const dim3 grid(static_cast<unsigned>((grid_rows + kSRRows - 1) / kSRRows), segs);
   const bool wide = (reinterpret_cast<uintptr_t>(x) & 31u) == 0 && (ldx % 16) == 0;
   cudaError_t e;
   if (layout == NVFP4_SF_TCGEN05)
-    e = wide ? launch_quantize_sr_pdl<true, true>(grid, s, xs, ir, ik, ldx, cs, ss, g_dev, amax_dev, seed, offset,
+    e = wide ? launch_quantize_sr_pdl<true, true>(grid, s, xs, ir, ik, ldx, cs, ss, g_dev, amax_dev, after_amax, seed, offset,
                                                   status)
-             : launch_quantize_sr_pdl<true, false>(grid, s, xs, ir, ik, ldx, cs, ss, g_dev, amax_dev, seed, offset,
+             : launch_quantize_sr_pdl<true, false>(grid, s, xs, ir, ik, ldx, cs, ss, g_dev, amax_dev, after_amax, seed, offset,
                                                    status);
   else
-    e = wide ? launch_quantize_sr_pdl<false, true>(grid, s, xs, ir, ik, ldx, cs, ss, g_dev, amax_dev, seed, offset,
+    e = wide ? launch_quantize_sr_pdl<false, true>(grid, s, xs, ir, ik, ldx, cs, ss, g_dev, amax_dev, after_amax, seed, offset,
                                                    status)
-             : launch_quantize_sr_pdl<false, false>(grid, s, xs, ir, ik, ldx, cs, ss, g_dev, amax_dev, seed, offset,
+             : launch_quantize_sr_pdl<false, false>(grid, s, xs, ir, ik, ldx, cs, ss, g_dev, amax_dev, after_amax, seed, offset,
                                                     status);
   return launch_status(e);
 }
