@@ -405,7 +405,8 @@ NVFP4_API size_t nvfp4_workspace_bytes(nvfp4_op op, int64_t M, int64_t N, int64_
  * with the same rule as nvfp4_quantize (its own amax and global scale), and
  * pre-quantized weights w (codes [N, K/2], TCGEN05 scales, *g_w_dev).  The
  * weight stream dominates (decode is memory-bound: "NVIDIA NVFP4 与
- * Micro-Scaling" section 六).  y: out, bf16 [M, N], pitch ldy.
+ * Micro-Scaling" section 六).  y: out, bf16 [M, N], pitch ldy; must not
+ * overlap x.
  * workspace: device scratch of nvfp4_workspace_bytes(NVFP4_OP_GEMV_BATCHED, M, N, K)
  *   bytes (quantized x, its scales and g, fp32 partial sums, tile counters).
  *   It needs no clearing, before the first call or between calls:

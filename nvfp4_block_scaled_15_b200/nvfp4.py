@@ -535,6 +535,11 @@ def _rows_of(t, shape=None):
     return t.stride(0)
 
 
+def _apart(out, *inputs):
+    """Outputs that would be written while the kernels still read these inputs (columns of one buffer are apart)."""
+    assert all(out.data_ptr() != t.data_ptr() or out.numel() == 0 for t in inputs), "not in place: out is an input that is still read"
+
+
 class Normalized:
     """Result of layernorm: y [rows, k], mean and rstd [rows] fp32, amax (max |y|, one fp32) for quantize(y, amax=)."""
 
@@ -546,7 +551,7 @@ class Normalized:
 def layernorm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
               eps: float = 1e-5, out_dtype=torch.bfloat16, out: torch.Tensor | None = None,
               stream=None) -> Normalized:
-    """Layer norm of x [rows, k] (bf16 or fp32); weight and bias [k] of one dtype.  The amax makes the
+    """Layer norm of x [rows, k] (bf16 or fp32), not in place; weight and bias [k] of one dtype.  The amax makes the
     quantizer behind it a single pass: ``quantize(n.y, amax=n.amax)``."""
     rows, k = x.shape
     ldx = _rows_of(x)
@@ -554,6 +559,7 @@ def layernorm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.T
         assert t is None or (t.shape == (k,) and t.is_contiguous()), "contiguous [k] weight and bias"
     assert weight is None or bias is None or weight.dtype == bias.dtype, "weight and bias of one dtype"
     y = out if out is not None else torch.empty((rows, k), dtype=out_dtype, device=x.device)
+    _apart(y, x)
     stats = torch.empty(2 * rows + 1, dtype=torch.float32, device=x.device)
     mean, rstd, amax = stats[:rows], stats[rows:2 * rows], stats[2 * rows:]
     nvfp4_layernorm(x, _dtype_of(x), rows, k, ldx, weight, bias, _dtype_of(weight if weight is not None else bias), eps,
@@ -565,7 +571,8 @@ def layernorm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.T
 def layernorm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
                        weight: torch.Tensor | None = None, d_residual: torch.Tensor | None = None,
                        out: torch.Tensor | None = None, workspace=None, stream=None):
-    """(dx, dweight, dbias, amax of dx): dx in x's dtype with d_residual added, dweight and dbias fp32."""
+    """(dx, dweight, dbias, amax of dx): dx in x's dtype with d_residual added (out may be d_residual), dweight and dbias
+    fp32."""
     rows, k = x.shape
     for t in (mean, rstd):
         assert t.shape == (rows,) and t.dtype == torch.float32 and t.is_contiguous(), "mean and rstd of the forward call"
@@ -573,6 +580,7 @@ def layernorm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rs
     assert d_residual is None or d_residual.dtype == x.dtype, "d_residual in x's dtype"
     dx = out if out is not None else torch.empty((rows, k), dtype=x.dtype, device=x.device)
     assert dx.dtype == x.dtype, "dx in x's dtype"
+    _apart(dx, dy, x)
     grads = torch.empty(2 * k + 1, dtype=torch.float32, device=x.device)
     ws_bytes = nvfp4_workspace_bytes(OP_LAYERNORM_BACKWARD, rows, k, 0)
     ws = workspace if workspace is not None else torch.empty(ws_bytes, dtype=torch.uint8, device=x.device)
@@ -611,7 +619,8 @@ def gemm_epilogue(a: Quantized, b: Quantized, bias: torch.Tensor | None = None, 
 def gemv_batched_epilogue(x: torch.Tensor, w: Quantized, bias: torch.Tensor | None = None, act: str | None = None,
                           residual: torch.Tensor | None = None, out: torch.Tensor | None = None, workspace=None,
                           stream=None) -> torch.Tensor:
-    """y [M, N] = act(x w^T + bias) + residual for bf16 activations x [M, K] (M <= 32) and NVFP4 weights w."""
+    """y [M, N] = act(x w^T + bias) + residual for bf16 activations x [M, K] (M <= 32) and NVFP4 weights w; out may be
+    residual, not x."""
     assert x.dtype == torch.bfloat16 and x.shape[1] == w.k and w.layout == SF_TCGEN05
     m, k = x.shape
     n = w.rows
@@ -619,6 +628,7 @@ def gemv_batched_epilogue(x: torch.Tensor, w: Quantized, bias: torch.Tensor | No
     ws = workspace if workspace is not None else torch.empty(ws_bytes, dtype=torch.uint8, device=x.device)
     y = out if out is not None else torch.empty((m, n), dtype=torch.bfloat16, device=x.device)
     assert y.dtype == torch.bfloat16
+    _apart(y, x)
     ldr = _check_epilogue(m, n, bias, residual, y.dtype)
     nvfp4_gemv_batched_epilogue(x, m, _rows_of(x), w.codes, w.sf, w.g, n, k, bias, _dtype_of(bias), ACTIVATIONS[act],
                                 residual, ldr, y, _rows_of(y, (m, n)), ws, ws.numel(), stream)

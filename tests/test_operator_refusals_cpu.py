@@ -181,3 +181,29 @@ def test_pitch_of_a_single_row(nv):
     assert nv._rows_of(flat.as_strided((5, 1), (3, 9))) == 3
     with pytest.raises(AssertionError, match="overlap"):
         nv._rows_of(flat.as_strided((5, 1), (0, 1)))
+
+
+def test_helpers_refuse_an_output_on_an_input(nv):
+    """Kernels read rows again, or other blocks read them, after outputs are written: only a residual (or its gradient, or
+    the gradient that an epilogue is given) may be written in place."""
+    t, dy, square = (torch.zeros(9, 64, dtype=torch.bfloat16) for _ in range(3))
+    stat, w = torch.zeros(9), quantized(nv, 64, 64)
+    for call in (lambda: nv.layernorm(t, out=t), lambda: nv.layernorm_backward(dy, t, stat, stat, out=t),
+                 lambda: nv.layernorm_backward(dy, t, stat, stat, out=dy),
+                 lambda: nv.gemv_batched_epilogue(square, w, out=square),
+                 lambda: nv.gemv_batched_epilogue(square, w, residual=square, out=square)):
+        with pytest.raises(AssertionError, match="in place"):
+            call()
+
+
+def test_helpers_take_rows_side_by_side(nv, monkeypatch):
+    """An input and an output may be columns of one buffer; the in-place forms that the library has stay."""
+    for name in ("nvfp4_layernorm", "nvfp4_layernorm_backward", "nvfp4_gemv_batched_epilogue", "nvfp4_epilogue_backward"):
+        monkeypatch.setattr(nv, name, lambda *a, **kw: None)
+    both, stat, w = torch.zeros(9, 128, dtype=torch.bfloat16), torch.zeros(9), quantized(nv, 64, 64)
+    x, y, r = both[:, :64], both[:, 64:], torch.zeros(9, 64, dtype=torch.bfloat16)
+    nv.layernorm(x, out=y)
+    nv.layernorm_backward(x, x, stat, stat, d_residual=r, out=r)
+    nv.gemv_batched_epilogue(x, w, residual=r, out=r)
+    nv.gemv_batched_epilogue(x, w, out=y)
+    nv.epilogue_backward(r, x, "relu", out=r)
