@@ -3,9 +3,14 @@
 // fp32, the activations with their derivatives, and the maximum of stored
 // magnitudes.
 //
-// Activations, evaluated in fp32 (relative error below 2^-20; the 2-ulp
-// ex2 / rcp / fast-divide forms, since an output is rounded to 2^-9 or
-// compared at 2^-20, not at 2^-24):
+// Activations, evaluated in fp32 with the 2-ulp ex2 and rcp.  The rounding of an
+// exponential's argument w moves e^w by |w| roundings, so the relative error is
+// at most (8 + 2 X) 2^-23 with X the size of that argument (v^2 for gelu, 2 u for
+// gelu_tanh, v for silu).  Emulated with correctly rounded ex2 and rcp: about
+// 2^-20 for v > -2; in the negative tails, whose values are small against v,
+// 2^-17.7 (gelu) and 2^-16.1 (gelu_tanh) at v = -10 and 2^-18 (silu) at v = -87.
+// Outputs in bf16 are rounded to 2^-9, so only fp32 ones show it.  A logistic or
+// a tail below 2^-126 is 0: silu is from v = -87.4 down.
 //   relu       max(v, 0); a NaN stays a NaN
 //   gelu       v Phi(v) = max(v, 0) - |v| g with g = erfc(|v| / sqrt 2) / 2, so
 //              the negative tail keeps its relative accuracy (1 + erf cancels)

@@ -1586,9 +1586,12 @@ template <typename TX, typename TDY>
 cudaError_t dispatch_backward(const LnBwdParams& p, bool vec, float* dgamma, float* dbeta, uint32_t* mags, cudaStream_t s) {
   if (p.k <= LB_SHORT_K) return run_backward_short<TX, TDY>(p, dgamma, dbeta, mags, s);
   // The kernel without a ring: fp32 rows at every size, whose accesses fill whole sectors (1500 x 1155 13.9 us against
-  // 23.9 of the ring, 20000 x 1155 88 against 176, 3000 x 8001 105 against 196).  With a 16-bit type up to a few million
-  // elements (by their bytes), where it wins by its blocks' earlier start: bf16 100 x 1155 9.2 against 12.4 us, 8000 x 301
-  // 20 against 22; 700 x 4095 39 against 24, 20000 x 1155 266 against 111; fp32 x with bf16 dy 3000 x 1155 47 against 36
+  // 23.9 of the ring, 20000 x 1155 88 against 176, 3000 x 8001 105 against 196).  With a 16-bit type up to 2^23 bytes of dy
+  // and x.  Where these lie in L2, behind the kernels that wrote them, its blocks' earlier start wins (device time, without
+  // and ring): bf16 100 x 1155 8.4 and 11.2 us, 1537 x 1155 (7 MB) 14.9 and 17.5, 8000 x 301 (10 MB) 16.5 and 19.9, 20000 x
+  // 1155 (92 MB) 153 and 93.  Out of memory the ring's loads ahead win earlier: 100 x 1155 10.1 and 11.5, 4000 x 301 (5 MB)
+  // 14.0 and 15.6, 1537 x 1155 20.6 and 17.7, 8000 x 301 22.1 and 21.9, 3000 x 1155 (14 MB) 33.4 and 23.6.  The bound lies
+  // between the two; fp32 with bf16 likewise (1537 x 1155, 11 MB: 16.1 and 18.8 out of L2, 24.5 and 19.5 out of memory).
   if (!vec && p.k <= LB_ODD_K &&
       (!kRingAlone<TX, TDY, true> ||
        p.rows * p.k * static_cast<int64_t>(sizeof(TX) + sizeof(TDY)) <= (int64_t{1} << 23)))
