@@ -174,12 +174,6 @@ __device__ __forceinline__ void act_values(float2 (&x)[N], int act) {
   });
 }
 
-__device__ __forceinline__ float act_value(float v, int act) {
-  float2 x[1] = {both(v)};
-  act_values(x, act);
-  return x[0].x;
-}
-
 // A chunk: 8 elements as 4 pairs.
 struct Chunk {
   float2 v[4];

@@ -1286,11 +1286,9 @@ __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>:
         tm = t % tiles_m;
         tn = t / tiles_m;
       }
-      if constexpr (kE == EPI_TMA)
-        ep.start(p, tmE, tm * 256 + static_cast<int>(rank) * 128 + quad * 32, tn * C::BN + half * HALF,
-                 b == 0 && half == 1 ? 64 : 0);
       [[maybe_unused]] const int shared_first = b == 0 && half == 1 ? 64 : 0;
       [[maybe_unused]] const int epi_row = tm * 256 + static_cast<int>(rank) * 128 + quad * 32;
+      if constexpr (kE == EPI_TMA) ep.start(p, tmE, epi_row, tn * C::BN + half * HALF, shared_first);
       if constexpr (kE == EPI_ROWS_BF16 || kE == EPI_ROWS_F32) bias_in<HALF>(p, tn * C::BN + half * HALF, ep.bias);
       if (!mbar_wait_bounded(&acc_full[b], static_cast<uint32_t>(j >> 1) & 1u, abort_flag, p.wait_limit_ns, p.status)) break;
       tc_fence_after();
@@ -1322,10 +1320,9 @@ __global__ void __launch_bounds__(kQA ? PairCfg<kMx>::THREADS_QA : PairCfg<kMx>:
       if constexpr (kE == EPI_TMA) {
         // 64 columns at a time, the columns shared with the other accumulator first
         const bool shared_cols = (b == 0 && half == 1) || (b == 1 && half == 0);
-        const int first = (b == 0 && half == 1) ? 64 : 0;
 #pragma unroll 1
         for (int part = 0; part < 2; ++part) {
-          const int c_off = part == 0 ? first : 64 - first;
+          const int c_off = part == 0 ? shared_first : 64 - shared_first;
           uint32_t w[64];
           tmem_ld_32x32b_x32(taddr + c_off, w);
           tmem_ld_32x32b_x32(taddr + c_off + 32, w + 32);
@@ -1769,13 +1766,13 @@ nvfp4_status run_gemm(const void* a_codes, const void* a_sf, const float* g_a, c
 
 }  // namespace
 
-// Most 128 x 128 tiles of an epilogue GEMM that takes one of them per SM instead
-// of a 256 x 256 tile per CTA pair (or a 128 x 256 tile per SM for M <= 128):
+// An epilogue GEMM of at most one 128 x 128 tile per SM takes those instead of a
+// 256 x 256 tile per CTA pair (or a 128 x 256 tile per SM for M <= 128):
 // 64 x 8192 x 8192 24.6 against 38.4 us, 301 x 1001 x 2112 fp32 16.4 against 22.7,
 // 1024 x 2048 x 2048 15.5 against 16.4; with more tiles than SMs the larger ones
 // win: 2048 x 2048 x 8192 26.7 against 37.8 us.  (At the lower clocks behind a
 // GEMM that met the power cap: 301 x 1001 x 2112 20.5 against 29.4.)
-constexpr int64_t EPI_SMALL_TILES = 148;
+static bool few_small_tiles(int64_t M, int64_t N) { return ((M + 127) / 128) * ((N + 127) / 128) <= device_sm_count(); }
 
 template <bool kMx>
 nvfp4_status dispatch_gemm(const void* a_codes, const void* a_sf, const float* g_a, const void* b_codes,
@@ -1783,7 +1780,7 @@ nvfp4_status dispatch_gemm(const void* a_codes, const void* a_sf, const float* g
                            nvfp4_out_dtype out, const QuantOut* q, cudaStream_t s, const Epilogue* epi = nullptr) {
   if (N <= 128) return run_gemm<128, kMx>(a_codes, a_sf, g_a, b_codes, b_sf, g_b, M, N, K, d, ldd, out, q, s, epi);
   // few tiles: more and smaller ones, one SM each
-  if (epi && ((M + 127) / 128) * ((N + 127) / 128) <= EPI_SMALL_TILES)
+  if (epi && few_small_tiles(M, N))
     return run_gemm<128, kMx>(a_codes, a_sf, g_a, b_codes, b_sf, g_b, M, N, K, d, ldd, out, q, s, epi);
   if (M <= 128) return run_gemm<256, kMx>(a_codes, a_sf, g_a, b_codes, b_sf, g_b, M, N, K, d, ldd, out, q, s, epi);
   return run_gemm_pair<kMx>(a_codes, a_sf, g_a, b_codes, b_sf, g_b, M, N, K, d, ldd, out, q, s, nullptr, epi);

@@ -528,7 +528,7 @@ __device__ __forceinline__ int tagged_arrive(unsigned long long* c, unsigned lon
     if (prev == cur) return same ? static_cast<int>(cur & 0xFFFFull) : 0;
     cur = prev;
   }
-  return 0;   // eight contributors per tile cannot contend 64 times; reached only on corruption
+  return 0;   // a tile's contributors (two, or GF_MAX_K / BK / GV_PART_STAGES = 4 parts) cannot contend 64 times; reached only on corruption
 }
 
 template <bool kE>

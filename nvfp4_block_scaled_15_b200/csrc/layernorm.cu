@@ -452,7 +452,7 @@ __device__ __forceinline__ Chunk param_chunk(const float* p, int c) {
 constexpr int LF_THREADS = 256;        // of a block, up to rows of LF_THREADS * 32; 512 beyond
 template <typename TX, int NV>
 constexpr int lf_blocks(int threads) {  // blocks per SM
-  return (NV <= 4 ? (sizeof(TX) == 2 ? 1024 : 768) : (sizeof(TX) == 2 ? 512 : 512)) / threads;
+  return (NV <= 4 ? (sizeof(TX) == 2 ? 1024 : 768) : 512) / threads;
 }
 template <int NV>
 constexpr int lf_max_k() { return 512 * 8 * NV; }
