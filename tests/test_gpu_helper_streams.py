@@ -74,3 +74,33 @@ def test_default_stream_by_its_handle(lib, operands):
     o = operands
     y = lib.layernorm(o["x"], o["g"], o["b"], stream=0)
     assert torch.equal(y.y, o["n"].y) and torch.cuda.current_stream() == torch.cuda.default_stream()
+
+
+@pytest.mark.parametrize("given", ["stream", "handle"])
+def test_captured_with_the_stream_named(lib, operands, given):
+    """Helpers given the very stream that a graph is captured on: what they allocate is the graph's, replays take new
+    contents."""
+    o = operands
+    x = o["x"].clone()
+    side = torch.cuda.Stream()
+
+    def step(**kw):
+        n = lib.layernorm(x, o["g"], o["b"], **kw)
+        q = lib.quantize(n.y, amax=n.amax, **kw)
+        d, pre = lib.gemm_epilogue(q, o["w"], o["bias"], "gelu", pre=True, **kw)
+        few = lib.gemv_batched_epilogue(x[:9], o["w"], o["bias"], "silu", **kw)
+        back = lib.epilogue_backward(o["dd"], pre, "gelu", **kw)
+        return [d, pre, few, *back, *lib.layernorm_backward(o["x"], x, n.mean, n.rstd, o["g"], **kw)]
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = step(stream=side if given == "stream" else side.cuda_stream)
+    for seed in (5, 6):
+        x.copy_(activations(seed, M, K))
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, (a, v) in enumerate(zip(got, step())):
+            assert torch.equal(a, v), i
+    assert lib.nvfp4_check_device_status() == lib.OK
