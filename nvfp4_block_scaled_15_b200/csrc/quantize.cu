@@ -159,9 +159,10 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const uint16_t* __re
   // Launched as a programmatic dependent of the amax pass (with a given amax in
   // the plain order, launch_quantize_pdl).  x is not written by that pass, so its
   // loads and the scale table go out before the wait and overlap the pass's tail;
-  // only the amax is read after it, and every store comes after it.  (The kernels that release dependents early are the amax
-  // passes and the GEMV prologue, none of which writes x; the amax pass itself
-  // starts only after all earlier work on the stream has finished.)
+  // only the amax is read after it, and every store comes after it.  (The kernels
+  // that release dependents early are the amax passes and the GEMV prologue, none
+  // of which writes x; the amax pass itself starts only after all earlier work on
+  // the stream has finished.)
   uint32_t w0[kRows][8], w1[kRows][8];
 #pragma unroll
   for (int j = 0; j < kRows; ++j)
